@@ -517,3 +517,9 @@ def conv2d(x, w, bias=None, residual=None, *, stride=1, pads=0, dilation=1, grou
     conv_forward(p, x, w, bias, residual, out, scratch, scratch.numel() * scratch.element_size()
                  if scratch is not None else 0, stream)
     return out
+
+
+from .dense import *  # noqa: E402,F401,F403 - the dense operators (include/linear.h)
+from .dense import __all__ as _dense_all  # noqa: E402
+
+__all__ += _dense_all

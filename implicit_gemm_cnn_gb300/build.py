@@ -21,7 +21,8 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libconv.so")
-SOURCES = ["conv_api.cu", "conv_ffma.cu", "conv_depthwise.cu", "conv_tc.cu", "conv_tcw.cu", "conv_integer.cu", "conv_transpose.cu", "conv_winograd.cu", "conv_pointwise.cu"]
+SOURCES = ["conv_api.cu", "conv_ffma.cu", "conv_depthwise.cu", "conv_tc.cu", "conv_tcw.cu", "conv_integer.cu", "conv_transpose.cu", "conv_winograd.cu", "conv_pointwise.cu",
+           "dense_api.cu", "dense_ffma.cu", "clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 
@@ -37,7 +38,7 @@ def nvcc() -> str:
 
 
 def _inputs_mtime() -> float:
-    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, "conv.h"), __file__]
+    files = [os.path.join(CSRC, f) for f in os.listdir(CSRC)] + [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)] + [__file__]
     return max(os.path.getmtime(f) for f in files)
 
 

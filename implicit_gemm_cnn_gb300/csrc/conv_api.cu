@@ -567,6 +567,8 @@ std::map<ClusterKey, bool> g_cluster_fits;
 
 }  // namespace
 
+conv_status conv::current_device(int* dev, int* sm) { return device_info(dev, sm); }
+
 bool conv::cluster_fits(const void* func, int cluster, int threads, size_t smem) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) {

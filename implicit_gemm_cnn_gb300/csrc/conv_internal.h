@@ -180,6 +180,10 @@ struct Plan {
   PwPlan pw;
 };
 
+// The current device's ordinal and SM count; CONV_ERR_DEVICE if it is no sm_103
+// device (conv_api.cu).
+conv_status current_device(int* dev, int* sm);
+
 // Opt `func` in to `bytes` of dynamic shared memory on the current device.
 // The opted-in size only grows and is remembered per (kernel, device); the
 // check and the update hold one lock, so concurrent host threads never lower

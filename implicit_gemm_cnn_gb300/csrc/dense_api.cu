@@ -1,0 +1,769 @@
+// dense_api.cu -- the C ABI of the dense operators (linear.h): validation,
+// planning and dispatch.  Everything here runs on the host; a call only
+// enqueues.  A plan is a function of the problem and the SM count (and of
+// whether the operands' addresses are 16-byte aligned), so the order of every
+// sum is too.
+#include <math.h>
+#include <stdio.h>
+#include <string.h>
+
+#include <algorithm>
+#include <utility>
+#include <vector>
+
+#include "dense_internal.h"
+
+using namespace conv;
+
+namespace {
+
+constexpr long long kI32 = 2147483647LL;
+constexpr long long kMaxElems = 1LL << 40;   // of one matrix
+constexpr uint32_t kFlags = CONV_LINEAR_FLAG_RESIDUAL_LAST | CONV_LINEAR_FLAG_UNALIGNED | CONV_LINEAR_FLAG_FORCE_FFMA |
+                            CONV_LINEAR_FLAG_NO_FEW_ROWS;
+
+size_t align256(size_t v) { return (v + 255) / 256 * 256; }
+long long round8(long long v) { return (v + 7) / 8 * 8; }
+size_t elem_size(int dtype) { return dtype == CONV_F32 ? 4 : 2; }
+
+// Row stride as given (0: dense); false if it is below the width or too large.
+bool stride_of(int64_t given, long long width, long long* out) {
+  *out = given == 0 ? width : given;
+  return *out >= width && *out <= (1LL << 36);
+}
+// The elements of rows x width at `stride`, if that is in range.
+bool elems_ok(long long rows, long long stride) {
+  long long n;
+  return !__builtin_mul_overflow(rows, stride, &n) && n <= kMaxElems;
+}
+size_t range_bytes(long long rows, long long width, long long stride, size_t es) {
+  return rows < 1 ? 0 : (static_cast<size_t>(rows - 1) * stride + width) * es;
+}
+
+struct LinearShape {
+  long long ldx, ldw, ldr, ldy;
+};
+conv_status validate(const conv_linear_problem* p, LinearShape* s) {
+  if (!p) return CONV_ERR_NULL;
+  if (p->dtype < CONV_F32 || p->dtype > CONV_BF16) return CONV_ERR_DTYPE;
+  if (p->act < CONV_ACT_IDENTITY || p->act > CONV_ACT_GELU_TANH) return CONV_ERR_ACT;
+  if (p->flags & ~kFlags) return CONV_ERR_ARG;
+  if (p->rows < 0 || p->c_in < 1 || p->c_out < 1) return CONV_ERR_SHAPE;
+  if (p->rows > kI32 - 1024 || p->c_in > kI32 - 1024 || p->c_out > kI32 - 1024) return CONV_ERR_SHAPE;
+  if (!stride_of(p->x_stride, p->c_in, &s->ldx) || !stride_of(p->w_stride, p->c_in, &s->ldw) ||
+      !stride_of(p->residual_stride, p->c_out, &s->ldr) || !stride_of(p->y_stride, p->c_out, &s->ldy))
+    return CONV_ERR_SHAPE;
+  if (!elems_ok(p->rows, s->ldx) || !elems_ok(p->c_out, s->ldw) || !elems_ok(p->rows, s->ldy) ||
+      (p->has_residual && !elems_ok(p->rows, s->ldr)) || !elems_ok(p->rows, round8(p->c_out)))
+    return CONV_ERR_OVERFLOW;
+  return CONV_OK;
+}
+
+struct GatedShape {
+  long long ldx, ldr, ldy, ldh;  // ldh: row length of h, g, u, dg, du as the library keeps them
+};
+conv_status validate(const conv_gated_problem* p, GatedShape* s) {
+  if (!p) return CONV_ERR_NULL;
+  if (p->dtype < CONV_F32 || p->dtype > CONV_BF16) return CONV_ERR_DTYPE;
+  if (p->act < CONV_ACT_IDENTITY || p->act > CONV_ACT_GELU_TANH) return CONV_ERR_ACT;
+  if (p->flags & ~(kFlags & ~CONV_LINEAR_FLAG_RESIDUAL_LAST)) return CONV_ERR_ARG;
+  if (p->rows < 0 || p->c_in < 1 || p->hidden < 1 || p->c_out < 1) return CONV_ERR_SHAPE;
+  if (p->rows > kI32 - 1024 || p->c_in > kI32 - 1024 || p->hidden > kI32 - 1024 || p->c_out > kI32 - 1024)
+    return CONV_ERR_SHAPE;
+  if (!stride_of(p->x_stride, p->c_in, &s->ldx) || !stride_of(p->residual_stride, p->c_out, &s->ldr) ||
+      !stride_of(p->y_stride, p->c_out, &s->ldy))
+    return CONV_ERR_SHAPE;
+  s->ldh = round8(p->hidden);
+  if (!elems_ok(p->rows, s->ldx) || !elems_ok(p->rows, s->ldy) || (p->has_residual && !elems_ok(p->rows, s->ldr)) ||
+      !elems_ok(p->rows, s->ldh) || !elems_ok(round8(p->c_in), s->ldh) || !elems_ok(round8(p->c_out), s->ldh))
+    return CONV_ERR_OVERFLOW;
+  return CONV_OK;
+}
+
+bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+
+// ---- one product: which kernel, and its scratch ------------------------------
+enum Variant { V_FFMA = 0 };
+struct Product {
+  Variant variant;
+  DenseFfmaPlan ffma;
+  size_t part_bytes;   // planes of the k ranges
+  int launches;
+};
+
+// `g` without addresses.  `tc`: 16-bit operands with rows a tensor-core copy can take.
+Product plan_product(const DenseGemm& g, int dtype, bool tc, uint32_t flags, int sm) {
+  (void)dtype; (void)tc; (void)flags;
+  Product r = {};
+  r.variant = V_FFMA;
+  r.ffma = dense_ffma_plan(g, sm);
+  if (r.ffma.split > 1)
+    r.part_bytes = static_cast<size_t>(r.ffma.split) * dense_products(g) * g.M * g.N * sizeof(float);
+  r.launches = r.ffma.split > 1 ? 2 : 1;
+  return r;
+}
+
+cudaError_t launch_product(const Product& r, DenseGemm g, int dtype, void* part, cudaStream_t s) {
+  g.split = r.ffma.split;
+  g.k_per_split = r.ffma.k_per_split;
+  g.part = static_cast<float*>(part);
+  cudaError_t err = launch_dense_ffma(r.ffma, g, dtype, s);
+  if (err == cudaSuccess && g.split > 1) err = launch_dense_reduce(g, dtype, s);
+  return err;
+}
+
+void describe_product(const Product& r, const DenseGemm& g, int sm, char* buf, size_t len) {
+  snprintf(buf, len, "ffma tile=%dx%d split=%d products=%d sums over %lld sms=%d launches=%d", r.ffma.bm, r.ffma.bn,
+           r.ffma.split, dense_products(g), static_cast<long long>(g.segs) * g.K, sm, r.launches);
+}
+
+// A 16-bit operand's copy into aligned rows, where its rows need one.
+struct Copy {
+  bool on;
+  long long rows, cols, ld_in, ld;
+  size_t off, bytes;
+};
+struct Layout {
+  size_t total = 0;
+  size_t take(size_t bytes) {
+    const size_t at = total;
+    total = align256(total + bytes);
+    return at;
+  }
+  Copy copy(int dtype, bool unaligned, long long rows, long long cols, long long ld) {
+    Copy c = {};
+    c.on = dtype != CONV_F32 && (unaligned || ld % 8 != 0) && rows > 0;
+    c.rows = rows; c.cols = cols; c.ld_in = ld;
+    c.ld = c.on ? round8(cols) : ld;
+    if (c.on) {
+      c.bytes = static_cast<size_t>(rows) * c.ld * 2;
+      c.off = take(c.bytes);
+    }
+    return c;
+  }
+};
+// The operand as the product reads it: the copy (enqueued here), or itself.
+cudaError_t resolve(const Copy& c, const void* in, char* scratch, const void** out, cudaStream_t s) {
+  *out = in;
+  if (!c.on) return cudaSuccess;
+  *out = scratch + c.off;
+  return launch_dense_repack(in, c.ld_in, scratch + c.off, c.ld, c.rows, c.cols, s);
+}
+
+DenseGemm make_gemm(long long m, long long n, long long k, int a_mn, int b_mn, long long lda, long long ldb) {
+  DenseGemm g;
+  memset(&g, 0, sizeof(g));
+  g.M = static_cast<int>(m); g.N = static_cast<int>(n); g.K = static_cast<int>(k);
+  g.a_mn = a_mn; g.b_mn = b_mn;
+  g.segs = 1; g.batch = 1;
+  g.lda = lda; g.ldb = ldb;
+  g.split = 1;
+  g.epi.mode = EPI_LINEAR;
+  return g;
+}
+
+// ---- linear -----------------------------------------------------------------
+// Whether copies are planned for unaligned addresses, or the CUDA-core kernel reads them.
+struct Mode {
+  bool copies;   // every 16-bit operand is copied
+  bool tc;       // the tensor-core kernels may run
+};
+Mode mode_of(uint32_t flags, int dtype) {
+  Mode m;
+  m.tc = dtype != CONV_F32 && !(flags & CONV_LINEAR_FLAG_FORCE_FFMA);
+  m.copies = m.tc && (flags & CONV_LINEAR_FLAG_UNALIGNED);
+  return m;
+}
+
+struct LinearPlan {
+  Copy x, w, dy;
+  DenseGemm fwd, dx, dw;
+  Product pfwd, pdx, pdw;
+  size_t part_off, dz_off, col_off, total;
+  long long ldz;
+  int col_blocks;
+  bool dz;   // dz is written (an activation); else dy stands for it
+};
+
+LinearPlan plan_linear(const conv_linear_problem* p, const LinearShape& sh, const Mode& mode, int sm) {
+  LinearPlan r = {};
+  Layout l;
+  const int dt = mode.tc ? p->dtype : CONV_F32;  // what copies go by
+  r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
+  r.w = l.copy(dt, mode.copies, p->c_out, p->c_in, sh.ldw);
+  r.fwd = make_gemm(p->rows, p->c_out, p->c_in, 0, 0, r.x.ld, r.w.ld);
+  DenseEpi& e = r.fwd.epi;
+  e.act = p->act; e.alpha = p->act_alpha; e.beta = p->act_beta;
+  e.residual_last = (p->flags & CONV_LINEAR_FLAG_RESIDUAL_LAST) != 0;
+  e.ldr = sh.ldr; e.ldy = sh.ldy; e.ldp = p->c_out;
+  if (p->rows > 0) r.pfwd = plan_product(r.fwd, p->dtype, mode.tc, p->flags, sm);
+  r.part_off = l.take(r.pfwd.part_bytes);
+  r.total = l.total;
+  return r;
+}
+
+LinearPlan plan_linear_backward(const conv_linear_problem* p, const LinearShape& sh, const Mode& mode, int sm) {
+  LinearPlan r = {};
+  Layout l;
+  const int dt = mode.tc ? p->dtype : CONV_F32;
+  r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
+  r.w = l.copy(dt, mode.copies, p->c_out, p->c_in, sh.ldw);
+  r.dz = p->act != CONV_ACT_IDENTITY;
+  if (r.dz) {
+    r.ldz = round8(p->c_out);
+    r.dz_off = l.take(static_cast<size_t>(p->rows) * r.ldz * elem_size(p->dtype));
+  } else {
+    r.dy = l.copy(dt, mode.copies, p->rows, p->c_out, sh.ldy);
+    r.ldz = r.dy.ld;
+  }
+  if (p->rows > 0) {
+    r.col_blocks = dense_col_blocks(p->rows, p->c_out, sm);
+    r.col_off = l.take(static_cast<size_t>(r.col_blocks) * p->c_out * sizeof(float));
+    r.dx = make_gemm(p->rows, p->c_in, p->c_out, 0, 1, r.ldz, r.w.ld);
+    r.dx.epi.ldy = p->c_in;
+    r.pdx = plan_product(r.dx, p->dtype, mode.tc, p->flags, sm);
+    r.dw = make_gemm(p->c_out, p->c_in, p->rows, 1, 1, r.ldz, r.x.ld);
+    r.dw.epi.ldy = p->c_in;
+    r.pdw = plan_product(r.dw, p->dtype, mode.tc, p->flags, sm);
+  }
+  r.part_off = l.take(std::max(r.pdx.part_bytes, r.pdw.part_bytes));
+  r.total = l.total;
+  return r;
+}
+
+// Outputs overlap neither inputs, nor scratch, nor one another.
+struct Ranges {
+  struct R { const void* p; size_t n; };
+  R in[8], out[8];  // the most that a call has
+  int ins = 0, outs = 0;
+  void add_in(const void* p, size_t n) { if (p && n) in[ins++] = {p, n}; }
+  void add_out(const void* p, size_t n) { if (p && n) out[outs++] = {p, n}; }
+  bool clash() const {
+    auto hit = [](const R& a, const R& b) {
+      const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
+      return x < y + b.n && y < x + a.n;
+    };
+    for (int i = 0; i < outs; ++i) {
+      for (int j = 0; j < ins; ++j) if (hit(out[i], in[j])) return true;
+      for (int j = 0; j < i; ++j) if (hit(out[i], out[j])) return true;
+    }
+    return false;
+  }
+};
+
+bool scratch_bad(const void* scratch, size_t have, size_t need) {
+  return need > 0 && (!scratch || have < need || reinterpret_cast<uintptr_t>(scratch) % 256 != 0);
+}
+
+// The mode for these addresses: where one is unaligned, copies if the scratch
+// has room for them, else the CUDA-core kernel.
+template <typename PlanFn>
+auto plan_for(uint32_t flags, int dtype, std::initializer_list<const void*> operands, size_t have, PlanFn plan)
+    -> decltype(plan(Mode{})) {
+  Mode m = mode_of(flags, dtype);
+  bool all = true;
+  for (const void* p : operands) all = all && aligned16(p);
+  if (m.tc && !all && !m.copies) {
+    m.copies = true;
+    auto r = plan(m);
+    if (r.total <= have) return r;
+    m.copies = m.tc = false;
+  }
+  return plan(m);
+}
+
+#define CONV_TRY(call)                                   \
+  do {                                                   \
+    if ((call) != cudaSuccess) return CONV_ERR_CUDA;     \
+  } while (0)
+
+// ---- gated ------------------------------------------------------------------
+struct GatedPlan {
+  Copy x, wg, wu, wd, dy;
+  DenseGemm up, down;                 // forward
+  DenseGemm dh, dx, dwgu, dwd;        // backward
+  Product pup, pdown, pdh, pdx, pdwgu, pdwd;
+  size_t h_off, dg_off, du_off, part_off, total;
+};
+struct GatedSaved {
+  size_t g_off, u_off, h_off, total;
+};
+GatedSaved gated_saved(const conv_gated_problem* p, const GatedShape& sh) {
+  Layout l;
+  GatedSaved s;
+  const size_t n = static_cast<size_t>(p->rows) * sh.ldh;
+  s.g_off = l.take(n * 4);
+  s.u_off = l.take(n * 4);
+  s.h_off = l.take(n * elem_size(p->dtype));
+  s.total = l.total;
+  return s;
+}
+
+GatedPlan plan_gated(const conv_gated_problem* p, const GatedShape& sh, const Mode& mode, int sm, bool saved) {
+  GatedPlan r = {};
+  Layout l;
+  const int dt = mode.tc ? p->dtype : CONV_F32;
+  r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
+  r.wg = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
+  r.wu = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
+  r.wd = l.copy(dt, mode.copies, p->c_out, p->hidden, p->hidden);
+  if (!saved) r.h_off = l.take(static_cast<size_t>(p->rows) * sh.ldh * elem_size(p->dtype));
+  if (p->rows > 0) {
+    r.up = make_gemm(p->rows, p->hidden, p->c_in, 0, 0, r.x.ld, r.wg.ld);
+    r.up.dual = 1;
+    r.up.epi.mode = EPI_GATED;
+    r.up.epi.act = p->act; r.up.epi.alpha = p->act_alpha; r.up.epi.beta = p->act_beta;
+    r.up.epi.ldy = sh.ldh; r.up.epi.ldp = sh.ldh;
+    r.pup = plan_product(r.up, p->dtype, mode.tc, p->flags, sm);
+    r.down = make_gemm(p->rows, p->c_out, p->hidden, 0, 0, sh.ldh, r.wd.ld);
+    r.down.epi.ldr = sh.ldr; r.down.epi.ldy = sh.ldy;
+    r.pdown = plan_product(r.down, p->dtype, mode.tc, p->flags, sm);
+  }
+  r.part_off = l.take(std::max(r.pup.part_bytes, r.pdown.part_bytes));
+  r.total = l.total;
+  return r;
+}
+
+GatedPlan plan_gated_backward(const conv_gated_problem* p, const GatedShape& sh, const Mode& mode, int sm) {
+  GatedPlan r = {};
+  Layout l;
+  const int dt = mode.tc ? p->dtype : CONV_F32;
+  r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
+  r.wg = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
+  r.wu = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
+  r.wd = l.copy(dt, mode.copies, p->c_out, p->hidden, p->hidden);
+  r.dy = l.copy(dt, mode.copies, p->rows, p->c_out, sh.ldy);
+  const size_t n = static_cast<size_t>(p->rows) * sh.ldh * elem_size(p->dtype);
+  r.dg_off = l.take(n);
+  r.du_off = l.take(n);
+  if (p->rows > 0) {
+    r.dh = make_gemm(p->rows, p->hidden, p->c_out, 0, 1, r.dy.ld, r.wd.ld);
+    r.dh.epi.mode = EPI_GATED_BWD;
+    r.dh.epi.act = p->act; r.dh.epi.alpha = p->act_alpha; r.dh.epi.beta = p->act_beta;
+    r.dh.epi.ldy = sh.ldh; r.dh.epi.ldp = sh.ldh;
+    r.pdh = plan_product(r.dh, p->dtype, mode.tc, p->flags, sm);
+    r.dx = make_gemm(p->rows, p->c_in, p->hidden, 0, 1, sh.ldh, r.wg.ld);
+    r.dx.segs = 2;
+    r.dx.epi.ldy = p->c_in;
+    r.pdx = plan_product(r.dx, p->dtype, mode.tc, p->flags, sm);
+    r.dwgu = make_gemm(p->hidden, p->c_in, p->rows, 1, 1, sh.ldh, r.x.ld);
+    r.dwgu.batch = 2;
+    r.dwgu.epi.ldy = p->c_in;
+    r.pdwgu = plan_product(r.dwgu, p->dtype, mode.tc, p->flags, sm);
+    r.dwd = make_gemm(p->c_out, p->hidden, p->rows, 1, 1, r.dy.ld, sh.ldh);
+    r.dwd.epi.ldy = p->hidden;
+    r.pdwd = plan_product(r.dwd, p->dtype, mode.tc, p->flags, sm);
+  }
+  r.part_off = l.take(std::max({r.pdh.part_bytes, r.pdx.part_bytes, r.pdwgu.part_bytes, r.pdwd.part_bytes}));
+  r.total = l.total;
+  return r;
+}
+
+// The pointer checks of conv_clip_grads.
+conv_status clip_check(int64_t count, const void* const* in, void* const* out, const int64_t* sizes,
+                       const int32_t* dtypes, const float* norm, const void* scratch, size_t have, size_t need) {
+  // ranges sorted by address: an output touches no other range but its own input's, exactly
+  struct R { uintptr_t lo, hi; int64_t tensor; bool out; };
+  std::vector<R> ranges;
+  ranges.reserve(static_cast<size_t>(count) * 2 + 2);
+  for (int64_t i = 0; i < count; ++i) {
+    if (dtypes[i] < CONV_F32 || dtypes[i] > CONV_BF16) return CONV_ERR_DTYPE;
+    if (sizes[i] == 0) continue;
+    const size_t es = elem_size(dtypes[i]), n = static_cast<size_t>(sizes[i]) * es;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]);
+    if (!a || (out && !out[i])) return CONV_ERR_NULL;
+    if (a % es) return CONV_ERR_ARG;
+    ranges.push_back({a, a + n, i, false});
+    if (out) {
+      const uintptr_t b = reinterpret_cast<uintptr_t>(out[i]);
+      if (b % es) return CONV_ERR_ARG;
+      if (b != a) ranges.push_back({b, b + n, i, true});
+      else ranges.back().out = true;
+    }
+  }
+  if (scratch_bad(scratch, have, need)) return CONV_ERR_SCRATCH;
+  ranges.push_back({reinterpret_cast<uintptr_t>(scratch), reinterpret_cast<uintptr_t>(scratch) + need, -1, true});
+  ranges.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, -2, true});
+  std::sort(ranges.begin(), ranges.end(), [](const R& a, const R& b) { return a.lo < b.lo; });
+  // the furthest end so far of any range, and of the written ones
+  uintptr_t end = 0, end_out = 0;
+  for (const R& r : ranges) {
+    if (r.lo < end_out || (r.out && r.lo < end)) return CONV_ERR_ALIAS;
+    end = std::max(end, r.hi);
+    if (r.out) end_out = std::max(end_out, r.hi);
+  }
+  return CONV_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+conv_status conv_linear_scratch_bytes(const conv_linear_problem* p, size_t* bytes) {
+  if (!bytes) return CONV_ERR_NULL;
+  LinearShape sh;
+  conv_status st = validate(p, &sh);
+  int dev, sm;
+  if (st == CONV_OK) st = current_device(&dev, &sm);
+  if (st == CONV_OK) *bytes = plan_linear(p, sh, mode_of(p->flags, p->dtype), sm).total;
+  return st;
+}
+
+conv_status conv_linear_backward_scratch_bytes(const conv_linear_problem* p, size_t* bytes) {
+  if (!bytes) return CONV_ERR_NULL;
+  LinearShape sh;
+  conv_status st = validate(p, &sh);
+  int dev, sm;
+  if (st == CONV_OK) st = current_device(&dev, &sm);
+  if (st == CONV_OK) *bytes = plan_linear_backward(p, sh, mode_of(p->flags, p->dtype), sm).total;
+  return st;
+}
+
+conv_status conv_linear_describe_plan(const conv_linear_problem* p, int32_t pass, int32_t sm_count, char* buf,
+                                      size_t len) {
+  if (!buf || !len) return CONV_ERR_NULL;
+  if (pass < 0 || pass > 2 || sm_count < 1) return CONV_ERR_ARG;
+  LinearShape sh;
+  const conv_status st = validate(p, &sh);
+  if (st != CONV_OK) return st;
+  if (p->rows == 0) {
+    snprintf(buf, len, "nothing launches=0");
+    return CONV_OK;
+  }
+  const Mode mode = mode_of(p->flags, p->dtype);
+  if (pass == 0) {
+    const LinearPlan r = plan_linear(p, sh, mode, sm_count);
+    describe_product(r.pfwd, r.fwd, sm_count, buf, len);
+  } else {
+    const LinearPlan r = plan_linear_backward(p, sh, mode, sm_count);
+    describe_product(pass == 1 ? r.pdx : r.pdw, pass == 1 ? r.dx : r.dw, sm_count, buf, len);
+  }
+  return CONV_OK;
+}
+
+conv_status conv_linear_forward(const conv_linear_problem* p, const void* x, const void* w, const void* bias,
+                                const void* residual, void* y, float* pre, void* scratch, size_t scratch_bytes,
+                                void* stream) {
+  LinearShape sh;
+  conv_status st = validate(p, &sh);
+  if (st != CONV_OK) return st;
+  if (p->rows == 0) return CONV_OK;
+  if (!x || !w || !y || (p->has_bias && !bias) || (p->has_residual && !residual)) return CONV_ERR_NULL;
+  const size_t es = elem_size(p->dtype);
+  Ranges ranges;
+  ranges.add_in(x, range_bytes(p->rows, p->c_in, sh.ldx, es));
+  ranges.add_in(w, range_bytes(p->c_out, p->c_in, sh.ldw, es));
+  if (p->has_bias) ranges.add_in(bias, p->c_out * es);
+  if (p->has_residual) ranges.add_in(residual, range_bytes(p->rows, p->c_out, sh.ldr, es));
+  ranges.add_out(y, range_bytes(p->rows, p->c_out, sh.ldy, es));
+  ranges.add_out(pre, static_cast<size_t>(p->rows) * p->c_out * 4);
+  if (ranges.clash()) return CONV_ERR_ALIAS;
+  int dev, sm;
+  st = current_device(&dev, &sm);
+  if (st != CONV_OK) return st;
+  const LinearPlan r = plan_for(p->flags, p->dtype, {x, w}, scratch_bytes,
+                                [&](const Mode& m) { return plan_linear(p, sh, m, sm); });
+  if (scratch_bad(scratch, scratch_bytes, r.total)) return CONV_ERR_SCRATCH;
+  ranges.add_out(r.total ? scratch : nullptr, r.total);
+  if (ranges.clash()) return CONV_ERR_ALIAS;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(scratch);
+  DenseGemm g = r.fwd;
+  CONV_TRY(resolve(r.x, x, base, &g.a[0], s));
+  CONV_TRY(resolve(r.w, w, base, &g.b[0], s));
+  g.epi.bias = p->has_bias ? bias : nullptr;
+  g.epi.residual = p->has_residual ? residual : nullptr;
+  g.epi.y = y;
+  g.epi.pre = pre;
+  CONV_TRY(launch_product(r.pfwd, g, p->dtype, base + r.part_off, s));
+  return CONV_OK;
+}
+
+conv_status conv_linear_backward(const conv_linear_problem* p, const void* x, const void* w, const float* pre,
+                                 const void* dy, void* dx, void* dw, void* dbias, void* dresidual, void* scratch,
+                                 size_t scratch_bytes, void* stream) {
+  LinearShape sh;
+  conv_status st = validate(p, &sh);
+  if (st != CONV_OK) return st;
+  const size_t es = elem_size(p->dtype);
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  const bool act = p->act != CONV_ACT_IDENTITY;
+  if (p->rows > 0 && (!dy || (dw && !x) || (dx && !w) || (act && !pre))) return CONV_ERR_NULL;
+  Ranges ranges;
+  if (p->rows > 0) {
+    if (dw) ranges.add_in(x, range_bytes(p->rows, p->c_in, sh.ldx, es));
+    if (dx) ranges.add_in(w, range_bytes(p->c_out, p->c_in, sh.ldw, es));
+    if (act) ranges.add_in(pre, static_cast<size_t>(p->rows) * p->c_out * 4);
+    ranges.add_in(dy, range_bytes(p->rows, p->c_out, sh.ldy, es));
+  }
+  ranges.add_out(dx, static_cast<size_t>(p->rows) * p->c_in * es);
+  ranges.add_out(dw, static_cast<size_t>(p->c_out) * p->c_in * es);
+  ranges.add_out(dbias, p->c_out * es);
+  ranges.add_out(dresidual, static_cast<size_t>(p->rows) * p->c_out * es);
+  if (ranges.clash()) return CONV_ERR_ALIAS;
+  int dev, sm;
+  st = current_device(&dev, &sm);
+  if (st != CONV_OK) return st;
+  if (p->rows == 0) {
+    if (dw) CONV_TRY(cudaMemsetAsync(dw, 0, static_cast<size_t>(p->c_out) * p->c_in * es, s));
+    if (dbias) CONV_TRY(cudaMemsetAsync(dbias, 0, p->c_out * es, s));
+    return CONV_OK;
+  }
+  // an operand that no wanted output reads does not count
+  const LinearPlan r = plan_for(p->flags, p->dtype, {dw ? x : nullptr, dx ? w : nullptr, act || !(dx || dw) ? nullptr : dy},
+                                scratch_bytes, [&](const Mode& m) { return plan_linear_backward(p, sh, m, sm); });
+  if (scratch_bad(scratch, scratch_bytes, r.total)) return CONV_ERR_SCRATCH;
+  ranges.add_out(r.total ? scratch : nullptr, r.total);
+  if (ranges.clash()) return CONV_ERR_ALIAS;
+  char* base = static_cast<char*>(scratch);
+  const bool last = (p->flags & CONV_LINEAR_FLAG_RESIDUAL_LAST) != 0;
+  // dz, and its column sums
+  void* dz = r.dz && (dx || dw) ? base + r.dz_off : nullptr;
+  if (dz || dbias)
+    CONV_TRY(launch_dense_dz(dy, sh.ldy, pre, dz, r.ldz, dbias, reinterpret_cast<float*>(base + r.col_off), r.col_blocks,
+                             p->rows, p->c_out, p->act, p->act_alpha, p->act_beta, p->dtype, s));
+  if (dresidual) {
+    if (act && !last)
+      CONV_TRY(launch_dense_dz(dy, sh.ldy, pre, dresidual, p->c_out, nullptr, nullptr, r.col_blocks, p->rows, p->c_out,
+                               p->act, p->act_alpha, p->act_beta, p->dtype, s));
+    else
+      CONV_TRY(cudaMemcpy2DAsync(dresidual, p->c_out * es, dy, sh.ldy * es, p->c_out * es, p->rows,
+                                 cudaMemcpyDeviceToDevice, s));
+  }
+  const void* z = dz;
+  if (!r.dz && (dx || dw)) CONV_TRY(resolve(r.dy, dy, base, &z, s));
+  if (dx) {
+    DenseGemm g = r.dx;
+    g.a[0] = z;
+    CONV_TRY(resolve(r.w, w, base, &g.b[0], s));
+    g.epi.y = dx;
+    CONV_TRY(launch_product(r.pdx, g, p->dtype, base + r.part_off, s));
+  }
+  if (dw) {
+    DenseGemm g = r.dw;
+    g.a[0] = z;
+    CONV_TRY(resolve(r.x, x, base, &g.b[0], s));
+    g.epi.y = dw;
+    CONV_TRY(launch_product(r.pdw, g, p->dtype, base + r.part_off, s));
+  }
+  return CONV_OK;
+}
+
+conv_status conv_gated_scratch_bytes(const conv_gated_problem* p, size_t* bytes) {
+  if (!bytes) return CONV_ERR_NULL;
+  GatedShape sh;
+  conv_status st = validate(p, &sh);
+  int dev, sm;
+  if (st == CONV_OK) st = current_device(&dev, &sm);
+  if (st == CONV_OK) *bytes = plan_gated(p, sh, mode_of(p->flags, p->dtype), sm, false).total;
+  return st;
+}
+
+conv_status conv_gated_backward_scratch_bytes(const conv_gated_problem* p, size_t* bytes) {
+  if (!bytes) return CONV_ERR_NULL;
+  GatedShape sh;
+  conv_status st = validate(p, &sh);
+  int dev, sm;
+  if (st == CONV_OK) st = current_device(&dev, &sm);
+  if (st == CONV_OK) *bytes = plan_gated_backward(p, sh, mode_of(p->flags, p->dtype), sm).total;
+  return st;
+}
+
+conv_status conv_gated_saved_bytes(const conv_gated_problem* p, size_t* bytes) {
+  if (!bytes) return CONV_ERR_NULL;
+  GatedShape sh;
+  const conv_status st = validate(p, &sh);
+  if (st == CONV_OK) *bytes = gated_saved(p, sh).total;
+  return st;
+}
+
+conv_status conv_gated_forward(const conv_gated_problem* p, const void* x, const void* w_gate, const void* w_up,
+                               const void* w_down, const void* residual, void* y, void* saved, void* scratch,
+                               size_t scratch_bytes, void* stream) {
+  GatedShape sh;
+  conv_status st = validate(p, &sh);
+  if (st != CONV_OK) return st;
+  if (p->rows == 0) return CONV_OK;
+  if (!x || !w_gate || !w_up || !w_down || !y || (p->has_residual && !residual)) return CONV_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(saved) % 256) return CONV_ERR_ARG;
+  const size_t es = elem_size(p->dtype);
+  const size_t wbytes = static_cast<size_t>(p->hidden) * p->c_in * es;
+  const GatedSaved keep = gated_saved(p, sh);
+  Ranges ranges;
+  ranges.add_in(x, range_bytes(p->rows, p->c_in, sh.ldx, es));
+  ranges.add_in(w_gate, wbytes);
+  ranges.add_in(w_up, wbytes);
+  ranges.add_in(w_down, static_cast<size_t>(p->c_out) * p->hidden * es);
+  if (p->has_residual) ranges.add_in(residual, range_bytes(p->rows, p->c_out, sh.ldr, es));
+  ranges.add_out(y, range_bytes(p->rows, p->c_out, sh.ldy, es));
+  ranges.add_out(saved, keep.total);
+  if (ranges.clash()) return CONV_ERR_ALIAS;
+  int dev, sm;
+  st = current_device(&dev, &sm);
+  if (st != CONV_OK) return st;
+  const GatedPlan r = plan_for(p->flags, p->dtype, {x, w_gate, w_up, w_down}, scratch_bytes,
+                               [&](const Mode& m) { return plan_gated(p, sh, m, sm, saved != nullptr); });
+  if (scratch_bad(scratch, scratch_bytes, r.total)) return CONV_ERR_SCRATCH;
+  ranges.add_out(r.total ? scratch : nullptr, r.total);
+  if (ranges.clash()) return CONV_ERR_ALIAS;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  char* base = static_cast<char*>(scratch);
+  char* kept = static_cast<char*>(saved);
+  void* h = saved ? kept + keep.h_off : base + r.h_off;
+  DenseGemm g = r.up;
+  CONV_TRY(resolve(r.x, x, base, &g.a[0], s));
+  CONV_TRY(resolve(r.wg, w_gate, base, &g.b[0], s));
+  CONV_TRY(resolve(r.wu, w_up, base, &g.b[1], s));
+  g.epi.y = h;
+  if (saved) {
+    g.epi.pre = reinterpret_cast<float*>(kept + keep.g_off);
+    g.epi.pre2 = reinterpret_cast<float*>(kept + keep.u_off);
+  }
+  CONV_TRY(launch_product(r.pup, g, p->dtype, base + r.part_off, s));
+  g = r.down;
+  g.a[0] = h;
+  CONV_TRY(resolve(r.wd, w_down, base, &g.b[0], s));
+  g.epi.residual = p->has_residual ? residual : nullptr;
+  g.epi.y = y;
+  CONV_TRY(launch_product(r.pdown, g, p->dtype, base + r.part_off, s));
+  return CONV_OK;
+}
+
+conv_status conv_gated_backward(const conv_gated_problem* p, const void* x, const void* w_gate, const void* w_up,
+                                const void* w_down, const void* saved, const void* dy, void* dx, void* dw_gate,
+                                void* dw_up, void* dw_down, void* scratch, size_t scratch_bytes, void* stream) {
+  GatedShape sh;
+  conv_status st = validate(p, &sh);
+  if (st != CONV_OK) return st;
+  const size_t es = elem_size(p->dtype);
+  const size_t wbytes = static_cast<size_t>(p->hidden) * p->c_in * es;
+  const size_t wdbytes = static_cast<size_t>(p->c_out) * p->hidden * es;
+  const bool dgu = dx || dw_gate || dw_up;
+  if (p->rows > 0 && (!dy || !saved || (dgu && !w_down) || ((dw_gate || dw_up) && !x) || (dx && (!w_gate || !w_up))))
+    return CONV_ERR_NULL;
+  if (reinterpret_cast<uintptr_t>(saved) % 256) return CONV_ERR_ARG;
+  const GatedSaved keep = gated_saved(p, sh);
+  Ranges ranges;
+  if (p->rows > 0) {
+    if (dw_gate || dw_up) ranges.add_in(x, range_bytes(p->rows, p->c_in, sh.ldx, es));
+    if (dx) {
+      ranges.add_in(w_gate, wbytes);
+      ranges.add_in(w_up, wbytes);
+    }
+    if (dgu) ranges.add_in(w_down, wdbytes);
+    ranges.add_in(saved, keep.total);
+    ranges.add_in(dy, range_bytes(p->rows, p->c_out, sh.ldy, es));
+  }
+  ranges.add_out(dx, static_cast<size_t>(p->rows) * p->c_in * es);
+  ranges.add_out(dw_gate, wbytes);
+  ranges.add_out(dw_up, wbytes);
+  ranges.add_out(dw_down, wdbytes);
+  if (ranges.clash()) return CONV_ERR_ALIAS;
+  int dev, sm;
+  st = current_device(&dev, &sm);
+  if (st != CONV_OK) return st;
+  cudaStream_t s = static_cast<cudaStream_t>(stream);
+  if (p->rows == 0) {
+    if (dw_gate) CONV_TRY(cudaMemsetAsync(dw_gate, 0, wbytes, s));
+    if (dw_up) CONV_TRY(cudaMemsetAsync(dw_up, 0, wbytes, s));
+    if (dw_down) CONV_TRY(cudaMemsetAsync(dw_down, 0, wdbytes, s));
+    return CONV_OK;
+  }
+  const bool dwgu = dw_gate || dw_up;
+  const GatedPlan r = plan_for(
+      p->flags, p->dtype, {dwgu ? x : nullptr, dx ? w_gate : nullptr, dx ? w_up : nullptr, dgu ? w_down : nullptr, dy},
+      scratch_bytes, [&](const Mode& m) { return plan_gated_backward(p, sh, m, sm); });
+  if (scratch_bad(scratch, scratch_bytes, r.total)) return CONV_ERR_SCRATCH;
+  ranges.add_out(r.total ? scratch : nullptr, r.total);
+  if (ranges.clash()) return CONV_ERR_ALIAS;
+  char* base = static_cast<char*>(scratch);
+  const char* kept = static_cast<const char*>(saved);
+  void* part = base + r.part_off;
+  const void* dyc = dy;
+  CONV_TRY(resolve(r.dy, dy, base, &dyc, s));
+  if (dgu) {
+    DenseGemm g = r.dh;
+    g.a[0] = dyc;
+    CONV_TRY(resolve(r.wd, w_down, base, &g.b[0], s));
+    g.epi.pre = reinterpret_cast<float*>(const_cast<char*>(kept + keep.g_off));
+    g.epi.pre2 = reinterpret_cast<float*>(const_cast<char*>(kept + keep.u_off));
+    g.epi.y = base + r.dg_off;
+    g.epi.y2 = base + r.du_off;
+    CONV_TRY(launch_product(r.pdh, g, p->dtype, part, s));
+  }
+  if (dx) {
+    DenseGemm g = r.dx;
+    g.a[0] = base + r.dg_off;
+    g.a[1] = base + r.du_off;
+    CONV_TRY(resolve(r.wg, w_gate, base, &g.b[0], s));
+    CONV_TRY(resolve(r.wu, w_up, base, &g.b[1], s));
+    g.epi.y = dx;
+    CONV_TRY(launch_product(r.pdx, g, p->dtype, part, s));
+  }
+  if (dwgu) {
+    DenseGemm g = r.dwgu;
+    Product q = r.pdwgu;
+    CONV_TRY(resolve(r.x, x, base, &g.b[0], s));
+    g.b[1] = g.b[0];
+    g.a[0] = base + r.dg_off;
+    g.a[1] = base + r.du_off;
+    g.epi.y = dw_gate;
+    g.epi.y2 = dw_up;
+    if (!dw_gate || !dw_up) {  // one of the two: its planes fit where both would
+      g.batch = 1;
+      if (!dw_gate) g.a[0] = g.a[1], g.epi.y = dw_up;
+    }
+    CONV_TRY(launch_product(q, g, p->dtype, part, s));
+  }
+  if (dw_down) {
+    DenseGemm g = r.dwd;
+    g.a[0] = dyc;
+    g.b[0] = kept + keep.h_off;
+    g.epi.y = dw_down;
+    CONV_TRY(launch_product(r.pdwd, g, p->dtype, part, s));
+  }
+  return CONV_OK;
+}
+
+conv_status conv_clip_scratch_bytes(int64_t count, const int64_t* sizes, size_t* bytes) {
+  if (!bytes || (count > 0 && !sizes)) return CONV_ERR_NULL;
+  if (count < 0 || count > (1 << 24)) return CONV_ERR_SHAPE;
+  for (int64_t i = 0; i < count; ++i)
+    if (sizes[i] < 0 || sizes[i] > kMaxElems) return CONV_ERR_SHAPE;
+  *bytes = clip_scratch_bytes(count, sizes);
+  return CONV_OK;
+}
+
+conv_status conv_clip_grads(int64_t count, const void* const* in, void* const* out, const int64_t* sizes,
+                            const int32_t* dtypes, float max_norm, float eps, float* norm, void* scratch,
+                            size_t scratch_bytes, void* stream) {
+  if (!norm || (count > 0 && (!in || !sizes || !dtypes))) return CONV_ERR_NULL;
+  size_t need;
+  conv_status st = conv_clip_scratch_bytes(count, sizes, &need);
+  if (st != CONV_OK) return st;
+  if (!(max_norm >= 0.0f) || !(eps >= 0.0f)) return CONV_ERR_ARG;
+  try {  // the list of ranges is host memory
+    st = clip_check(count, in, out, sizes, dtypes, norm, scratch, scratch_bytes, need);
+  } catch (...) {
+    st = CONV_ERR_OVERFLOW;
+  }
+  if (st != CONV_OK) return st;
+  int dev, sm;
+  st = current_device(&dev, &sm);
+  if (st != CONV_OK) return st;
+  CONV_TRY(launch_clip(count, in, out, sizes, dtypes, max_norm, eps, norm, scratch, sm,
+                       static_cast<cudaStream_t>(stream)));
+  return CONV_OK;
+}
+
+conv_status conv_linear_device_error(uint32_t* word, int32_t reset) {
+  if (!word) return CONV_ERR_NULL;
+  (void)reset;
+  int dev, sm;
+  const conv_status st = current_device(&dev, &sm);
+  if (st != CONV_OK) return st;
+  *word = 0;
+  return CONV_OK;
+}
+
+}  // extern "C"

@@ -1,0 +1,369 @@
+// dense_ffma.cu -- the dense products on the CUDA cores: float32 layers, and
+// 16-bit operands of an alignment that the tensor-core kernel's copies cannot
+// take.  Also the ordered sum of k ranges, and the elementwise helpers of the
+// backward passes.
+//
+// A block computes a BM x BN tile of D = A B^T in register tiles of TM x TN per
+// thread, operands staged k-row by k-row in shared memory (As[k][m], Bs[k][n])
+// as float32, the next stage's values held in registers while the current one
+// is multiplied.  A thread's rows and columns are groups of four, half a tile
+// apart, so that its shared-memory reads are 16 bytes and free of bank
+// conflicts.  The same split serves the gated product: the column groups of
+// the first half are gate columns, those of the second half the up columns of
+// the same positions, so g and u of one element meet in one thread.
+#include <algorithm>
+
+#include "dense_internal.h"
+
+namespace conv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kBK = 16;
+
+// One operand's stage: R = 16 * T / kThreads values per thread.  k-major: 16
+// consecutive k of a row (64 or 32 bytes) per 16 lanes; mn-major: whole rows of
+// consecutive m.
+template <typename T, int TILE>
+struct Loader {
+  static constexpr int R = TILE * kBK / kThreads;
+  const T* p;
+  long long step_i, step_k;  // between a thread's values; between stages
+  int r0, k0, dr, dk;        // the first value's row and k in the tile, and their steps
+  __device__ __forceinline__ void init(const void* base, long long ld, int mn, int row, long long k, int tid) {
+    if (mn) {
+      r0 = tid % TILE; k0 = tid / TILE; dr = 0; dk = kThreads / TILE;
+      p = static_cast<const T*>(base) + (k + k0) * ld + row + r0;
+      step_i = dk * ld; step_k = kBK * ld;
+    } else {
+      r0 = tid / kBK; k0 = tid % kBK; dr = kThreads / kBK; dk = 0;
+      p = static_cast<const T*>(base) + (row + r0) * ld + k + k0;
+      step_i = dr * ld; step_k = kBK;
+    }
+  }
+  // values of the stage; `rows`, `ks`: how many of the tile's rows and of the stage's k exist
+  __device__ __forceinline__ void load(float (&v)[R], int rows, long long ks) {
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      v[i] = (r0 + i * dr < rows && k0 + i * dk < ks) ? to_f32(p[i * step_i]) : 0.0f;
+    p += step_k;
+  }
+  template <int P>
+  __device__ __forceinline__ void store(float (&s)[kBK][P], const float (&v)[R], int at) const {
+#pragma unroll
+    for (int i = 0; i < R; ++i) s[k0 + i * dk][at + r0 + i * dr] = v[i];
+  }
+};
+
+template <typename T, int BM, int BN, bool DUAL>
+__global__ void __launch_bounds__(kThreads, BM * BN >= 128 * 128 ? 1 : 2) dense_ffma(const DenseGemm g) {
+  constexpr int TM = BM / 16, TN = BN / 16;
+  constexpr int BNL = DUAL ? BN / 2 : BN;  // columns of the output tile
+  __shared__ float As[2][kBK][BM + 4];
+  __shared__ float Bs[2][kBK][BN + 4];
+  const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
+  const int products = DUAL ? 1 : g.batch;
+  const int which = blockIdx.z % products, range = blockIdx.z / products;
+  const int ntiles = (g.N + BNL - 1) / BNL;
+  const int m0 = static_cast<int>(blockIdx.x / ntiles) * BM, n0 = static_cast<int>(blockIdx.x % ntiles) * BNL;
+  const int rows_a = min(BM, g.M - m0), rows_b = min(BNL, g.N - n0);
+
+  float acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = 0.0f;
+
+  const long long k_end_all = static_cast<long long>(g.segs) * g.K;
+  const long long k_lo = range * g.k_per_split;
+  const long long k_hi = min(k_lo + g.k_per_split, k_end_all);
+  for (int seg = 0; seg < g.segs; ++seg) {
+    // this segment's part of the range
+    const long long lo = max(k_lo - static_cast<long long>(seg) * g.K, 0LL);
+    const long long hi = min(k_hi - static_cast<long long>(seg) * g.K, static_cast<long long>(g.K));
+    if (lo >= hi) continue;
+    Loader<T, BM> la;
+    Loader<T, BNL> lb, lb2;
+    const int op = g.segs > 1 ? seg : which;
+    la.init(g.a[op], g.lda, g.a_mn, m0, lo, tid);
+    lb.init(g.b[op], g.ldb, g.b_mn, n0, lo, tid);
+    if (DUAL) lb2.init(g.b[1], g.ldb, g.b_mn, n0, lo, tid);
+    float va[Loader<T, BM>::R], vb[Loader<T, BNL>::R], vb2[DUAL ? Loader<T, BNL>::R : 1];
+    auto load = [&](long long k) {
+      la.load(va, rows_a, hi - k);
+      lb.load(vb, rows_b, hi - k);
+      if constexpr (DUAL) lb2.load(vb2, rows_b, hi - k);
+    };
+    auto store = [&](int s) {
+      la.store(As[s], va, 0);
+      lb.store(Bs[s], vb, 0);
+      if constexpr (DUAL) lb2.store(Bs[s], vb2, BNL);
+    };
+    __syncthreads();  // the previous segment's last stage has been read
+    load(lo);
+    store(0);
+    __syncthreads();
+    int s = 0;
+    for (long long k = lo; k < hi; k += kBK) {
+      const bool more = k + kBK < hi;
+      if (more) load(k + kBK);
+#pragma unroll
+      for (int kk = 0; kk < kBK; ++kk) {
+        float a[TM], b[TN];
+#pragma unroll
+        for (int i = 0; i < TM; i += 4)
+          *reinterpret_cast<float4*>(a + i) = *reinterpret_cast<const float4*>(&As[s][kk][i / 4 * (BM / 2) + ty * 4]);
+#pragma unroll
+        for (int j = 0; j < TN; j += 4)
+          *reinterpret_cast<float4*>(b + j) = *reinterpret_cast<const float4*>(&Bs[s][kk][j / 4 * (BN / 2) + tx * 4]);
+#pragma unroll
+        for (int i = 0; i < TM; ++i)
+#pragma unroll
+          for (int j = 0; j < TN; ++j) acc[i][j] = fmaf(a[i], b[j], acc[i][j]);
+      }
+      if (more) {
+        store(s ^ 1);  // read last before the previous barrier
+        __syncthreads();
+        s ^= 1;
+      }
+    }
+  }
+
+  constexpr int NC = DUAL ? TN / 2 : TN;
+  int col[NC];
+  bool okc[NC];
+#pragma unroll
+  for (int j = 0; j < NC; ++j) {
+    col[j] = n0 + (DUAL ? 0 : j / 4 * (BN / 2)) + tx * 4 + j % 4;
+    okc[j] = col[j] < g.N;
+  }
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int m = m0 + i / 4 * (BM / 2) + ty * 4 + i % 4;
+    if (m >= g.M) continue;
+    if (g.split > 1) {
+      const long long plane = static_cast<long long>(g.M) * g.N;
+      const int planes = DUAL ? 2 : products;
+      float* part = g.part + (static_cast<long long>(range) * planes + which) * plane + static_cast<long long>(m) * g.N;
+#pragma unroll
+      for (int j = 0; j < NC; ++j)
+        if (okc[j]) {
+          part[col[j]] = acc[i][j];
+          if constexpr (DUAL) part[plane + col[j]] = acc[i][j + NC];
+        }
+    } else {
+      float v[NC], u[NC];
+#pragma unroll
+      for (int j = 0; j < NC; ++j) {
+        v[j] = acc[i][j];
+        u[j] = DUAL ? acc[i][j + (DUAL ? NC : 0)] : 0.0f;
+      }
+      dense_epilogue<T, NC>(g.epi, which, m, col, okc, v, u);
+    }
+  }
+}
+
+// y[m][n] from the planes of the k ranges: four columns per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) dense_reduce(const DenseGemm g) {
+  const long long quads = (static_cast<long long>(g.N) + 3) / 4;
+  const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (idx >= quads * g.M) return;
+  const int which = blockIdx.y;
+  const int m = static_cast<int>(idx / quads), n = static_cast<int>(idx % quads) * 4;
+  const long long plane = static_cast<long long>(g.M) * g.N;
+  const int planes = g.dual ? 2 : g.batch;
+  const float* p = g.part + which * plane + static_cast<long long>(m) * g.N + n;
+  float v[4] = {0, 0, 0, 0}, u[4] = {0, 0, 0, 0};
+  int col[4];
+  bool ok[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) { col[j] = n + j; ok[j] = n + j < g.N; }
+  const bool vec = g.N % 4 == 0;  // planes are 16-byte aligned then
+  for (int s = 0; s < g.split; ++s) {
+    if (vec) {
+      const float4 t = *reinterpret_cast<const float4*>(p);
+      v[0] += t.x; v[1] += t.y; v[2] += t.z; v[3] += t.w;
+      if (g.dual) {
+        const float4 q = *reinterpret_cast<const float4*>(p + plane);
+        u[0] += q.x; u[1] += q.y; u[2] += q.z; u[3] += q.w;
+      }
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (ok[j]) {
+          v[j] += p[j];
+          if (g.dual) u[j] += p[plane + j];
+        }
+    }
+    p += planes * plane;
+  }
+  dense_epilogue<T, 4>(g.epi, which, m, col, ok, v, u);
+}
+
+__global__ void __launch_bounds__(256) dense_repack(const uint16_t* in, long long ld_in, uint16_t* out, long long ld_out,
+                                                    long long rows, long long cols) {
+  // a warp copies 256 columns of a row at a time
+  const long long chunks = (cols + 255) / 256;
+  const long long warp = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32;
+  const long long warps = static_cast<long long>(gridDim.x) * 8;
+  const int lane = threadIdx.x % 32;
+  for (long long w = warp; w < rows * chunks; w += warps) {
+    const long long r = w / chunks, c0 = w % chunks * 256;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const long long c = c0 + i * 32 + lane;
+      if (c < cols) out[r * ld_out + c] = in[r * ld_in + c];
+    }
+  }
+}
+
+// dz and the column sums of a row block: a thread takes two columns of every
+// eighth row of the block; the eight partial sums are added in order.
+template <typename T>
+__global__ void __launch_bounds__(256) dense_dz(const T* dy, long long ld_dy, const float* pre, T* dz, long long ld_dz,
+                                                float* part, int rows_per_block, long long rows, long long cols,
+                                                int act, float alpha, float beta) {
+  constexpr bool FAST = sizeof(T) == 2;
+  __shared__ float2 sums[8][32];
+  const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
+  const long long c = static_cast<long long>(blockIdx.x) * 64 + tx * 2;
+  const long long r0 = static_cast<long long>(blockIdx.y) * rows_per_block;
+  const long long r1 = min(r0 + rows_per_block, rows);
+  const bool ok0 = c < cols, ok1 = c + 1 < cols;
+  float2 sum = make_float2(0.0f, 0.0f);
+  for (long long r = r0 + ty; r < r1; r += 8) {
+    float v[2] = {0.0f, 0.0f};
+    if (ok0) v[0] = to_f32(dy[r * ld_dy + c]);
+    if (ok1) v[1] = to_f32(dy[r * ld_dy + c + 1]);
+    if (act != ACT_IDENTITY) {
+      float t[2] = {ok0 ? pre[r * cols + c] : 0.0f, ok1 ? pre[r * cols + c + 1] : 0.0f}, d[2];
+      dense_activate_grad<FAST, 2>(t, d, act, alpha, beta);
+      v[0] *= d[0];
+      v[1] *= d[1];
+    }
+    if (dz) {
+      if (ok0) dz[r * ld_dz + c] = from_f32<T>(v[0]);
+      if (ok1) dz[r * ld_dz + c + 1] = from_f32<T>(v[1]);
+    }
+    sum.x += v[0];
+    sum.y += v[1];
+  }
+  if (!part) return;
+  sums[ty][tx] = sum;
+  __syncthreads();
+  if (ty == 0) {
+    float2 t = sums[0][tx];
+#pragma unroll
+    for (int i = 1; i < 8; ++i) { t.x += sums[i][tx].x; t.y += sums[i][tx].y; }
+    float* p = part + static_cast<long long>(blockIdx.y) * cols + c;
+    if (ok0) p[0] = t.x;
+    if (ok1) p[1] = t.y;
+  }
+}
+template <typename T>
+__global__ void __launch_bounds__(256) dense_colsum(const float* part, T* out, int blocks, long long cols) {
+  const long long c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  if (c >= cols) return;
+  float s = 0.0f;
+  for (int b = 0; b < blocks; ++b) s += part[b * cols + c];
+  out[c] = from_f32<T>(s);
+}
+
+template <typename T, int BM, int BN, bool DUAL>
+cudaError_t go(const DenseGemm& g, cudaStream_t s) {
+  const int bnl = DUAL ? BN / 2 : BN;
+  const dim3 grid(static_cast<unsigned>(((g.N + bnl - 1LL) / bnl) * ((g.M + BM - 1LL) / BM)), 1,
+                  static_cast<unsigned>((DUAL ? 1 : g.batch) * g.split));
+  dense_ffma<T, BM, BN, DUAL><<<grid, kThreads, 0, s>>>(g);
+  return cudaGetLastError();
+}
+template <typename T>
+cudaError_t by_tile(const DenseFfmaPlan& p, const DenseGemm& g, cudaStream_t s) {
+  if (g.dual) return p.bm == 128 ? go<T, 128, 128, true>(g, s) : go<T, 64, 128, true>(g, s);
+  return p.bm == 128 ? go<T, 128, 128, false>(g, s) : go<T, 64, 64, false>(g, s);
+}
+
+template <typename T>
+cudaError_t dz_go(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, void* dbias, float* part,
+                  int blocks, long long rows, long long cols, int act, float alpha, float beta, cudaStream_t s) {
+  const int per = static_cast<int>((rows + blocks - 1) / blocks);
+  const dim3 grid(static_cast<unsigned>((cols + 63) / 64), static_cast<unsigned>((rows + per - 1) / per));
+  dense_dz<T><<<grid, 256, 0, s>>>(static_cast<const T*>(dy), ld_dy, pre, static_cast<T*>(dz), ld_dz,
+                                   dbias ? part : nullptr, per, rows, cols, act, alpha, beta);
+  cudaError_t err = cudaGetLastError();
+  if (err != cudaSuccess || !dbias) return err;
+  dense_colsum<T><<<static_cast<unsigned>((cols + 255) / 256), 256, 0, s>>>(part, static_cast<T*>(dbias),
+                                                                         static_cast<int>(grid.y), cols);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+DenseFfmaPlan dense_ffma_plan(const DenseGemm& g, int sm) {
+  DenseFfmaPlan p;
+  auto tiles = [&](int bm, int bnl) {
+    return ((g.M + bm - 1LL) / bm) * ((g.N + bnl - 1LL) / bnl) * g.batch;
+  };
+  const int bnl_large = g.dual ? 64 : 128, bnl_small = 64;
+  // large tiles where they fill the device twice over; else small ones
+  if (tiles(128, bnl_large) >= 2LL * sm) { p.bm = 128; p.bn = bnl_large; }
+  else { p.bm = 64; p.bn = bnl_small; }
+  const long long t = tiles(p.bm, p.bn), k = static_cast<long long>(g.segs) * g.K;
+  // two blocks per SM; k in ranges of at least 128 terms where the tiles are fewer
+  long long split = 1;
+  if (t < 2LL * sm && k >= 256) split = std::min<long long>({(2LL * sm) / t, k / 128, 16});
+  if (split < 1) split = 1;
+  p.k_per_split = ((k + split - 1) / split + kBK - 1) / kBK * kBK;
+  p.split = static_cast<int>((k + p.k_per_split - 1) / p.k_per_split);
+  if (p.split <= 1) { p.split = 1; p.k_per_split = k; }
+  return p;
+}
+
+cudaError_t launch_dense_ffma(const DenseFfmaPlan& p, const DenseGemm& g, int dtype, cudaStream_t s) {
+  switch (dtype) {
+    case CONV_F32: return by_tile<float>(p, g, s);
+    case CONV_F16: return by_tile<__half>(p, g, s);
+    default: return by_tile<__nv_bfloat16>(p, g, s);
+  }
+}
+
+cudaError_t launch_dense_reduce(const DenseGemm& g, int dtype, cudaStream_t s) {
+  const long long quads = (static_cast<long long>(g.N) + 3) / 4 * g.M;
+  const dim3 grid(static_cast<unsigned>((quads + 255) / 256), static_cast<unsigned>(g.dual ? 1 : g.batch));
+  switch (dtype) {
+    case CONV_F32: dense_reduce<float><<<grid, 256, 0, s>>>(g); break;
+    case CONV_F16: dense_reduce<__half><<<grid, 256, 0, s>>>(g); break;
+    default: dense_reduce<__nv_bfloat16><<<grid, 256, 0, s>>>(g); break;
+  }
+  return cudaGetLastError();
+}
+
+cudaError_t launch_dense_repack(const void* in, long long ld_in, void* out, long long ld_out, long long rows,
+                                long long cols, cudaStream_t s) {
+  const long long warps = rows * ((cols + 255) / 256);
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>((warps + 7) / 8, 1 << 16));
+  dense_repack<<<blocks, 256, 0, s>>>(static_cast<const uint16_t*>(in), ld_in, static_cast<uint16_t*>(out), ld_out, rows,
+                                      cols);
+  return cudaGetLastError();
+}
+
+int dense_col_blocks(long long rows, long long cols, int sm) {
+  // row blocks of at least kColRowsMin rows, about 16 blocks per SM in all
+  const long long strips = (cols + 63) / 64;
+  const long long want = std::max<long long>(1, 16LL * sm / strips);
+  return static_cast<int>(std::max<long long>(1, std::min<long long>({want, (rows + kColRowsMin - 1) / kColRowsMin, 65535})));
+}
+
+cudaError_t launch_dense_dz(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, void* dbias,
+                            float* part, int blocks, long long rows, long long cols, int act, float alpha, float beta,
+                            int dtype, cudaStream_t s) {
+  switch (dtype) {
+    case CONV_F32: return dz_go<float>(dy, ld_dy, pre, dz, ld_dz, dbias, part, blocks, rows, cols, act, alpha, beta, s);
+    case CONV_F16: return dz_go<__half>(dy, ld_dy, pre, dz, ld_dz, dbias, part, blocks, rows, cols, act, alpha, beta, s);
+    default:
+      return dz_go<__nv_bfloat16>(dy, ld_dy, pre, dz, ld_dz, dbias, part, blocks, rows, cols, act, alpha, beta, s);
+  }
+}
+
+}  // namespace conv

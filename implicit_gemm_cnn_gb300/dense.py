@@ -1,0 +1,466 @@
+"""The dense operators of the library (include/linear.h): the linear layer, the
+gated feed-forward block and the clipping of gradients by their global norm.
+
+``conv_linear_*``, ``conv_gated_*`` and ``conv_clip_*`` keep the C names and
+only marshal arguments; ``linear``, ``linear_backward``, ``gated_ffn``,
+``gated_ffn_backward`` and ``clip_grad_norm`` take CUDA tensors and allocate
+outputs and scratch with torch."""
+from __future__ import annotations
+
+import ctypes
+
+from . import ACTIVATIONS, DTYPES, _check, _dtype_name, _ptr, load
+
+__all__ = [
+    "LinearProblem", "GatedProblem", "LINEAR_ACTIVATIONS", "FLAG_LINEAR_RESIDUAL_LAST", "FLAG_LINEAR_UNALIGNED",
+    "FLAG_LINEAR_FORCE_FFMA", "FLAG_LINEAR_NO_FEW_ROWS", "make_linear_problem", "make_gated_problem",
+    "conv_linear_scratch_bytes", "conv_linear_backward_scratch_bytes", "conv_linear_describe_plan",
+    "conv_linear_forward", "conv_linear_backward", "conv_gated_scratch_bytes", "conv_gated_backward_scratch_bytes",
+    "conv_gated_saved_bytes", "conv_gated_forward", "conv_gated_backward", "conv_clip_scratch_bytes",
+    "conv_clip_grads", "conv_linear_device_error", "linear", "linear_backward", "gated_ffn", "gated_ffn_backward",
+    "clip_grad_norm",
+]
+
+LINEAR_ACTIVATIONS = dict(ACTIVATIONS, gelu=9, gelu_tanh=10)
+FLAG_LINEAR_RESIDUAL_LAST = 0x1
+FLAG_LINEAR_UNALIGNED = 0x2
+FLAG_LINEAR_FORCE_FFMA = 0x4
+FLAG_LINEAR_NO_FEW_ROWS = 0x8
+
+
+class LinearProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "rows", "c_in", "c_out", "x_stride", "w_stride", "residual_stride", "y_stride")] + [
+        ("act", ctypes.c_int32), ("act_alpha", ctypes.c_float), ("act_beta", ctypes.c_float),
+        ("dtype", ctypes.c_int32), ("has_bias", ctypes.c_int32), ("has_residual", ctypes.c_int32),
+        ("flags", ctypes.c_uint32)]
+
+
+class GatedProblem(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int64) for n in (
+        "rows", "c_in", "hidden", "c_out", "x_stride", "residual_stride", "y_stride")] + [
+        ("act", ctypes.c_int32), ("act_alpha", ctypes.c_float), ("act_beta", ctypes.c_float),
+        ("dtype", ctypes.c_int32), ("has_residual", ctypes.c_int32), ("flags", ctypes.c_uint32)]
+
+
+_lib = None
+
+
+def _load() -> ctypes.CDLL:
+    global _lib
+    if _lib is None:
+        lib = load()
+        P, vp, sz = ctypes.POINTER, ctypes.c_void_p, ctypes.c_size_t
+        i64, i32, f = ctypes.c_int64, ctypes.c_int32, ctypes.c_float
+        lp, gp = P(LinearProblem), P(GatedProblem)
+        for name, args in {
+            "conv_linear_scratch_bytes": [lp, P(sz)],
+            "conv_linear_backward_scratch_bytes": [lp, P(sz)],
+            "conv_linear_describe_plan": [lp, i32, i32, ctypes.c_char_p, sz],
+            "conv_linear_forward": [lp] + [vp] * 7 + [sz, vp],
+            "conv_linear_backward": [lp] + [vp] * 9 + [sz, vp],
+            "conv_gated_scratch_bytes": [gp, P(sz)],
+            "conv_gated_backward_scratch_bytes": [gp, P(sz)],
+            "conv_gated_saved_bytes": [gp, P(sz)],
+            "conv_gated_forward": [gp] + [vp] * 8 + [sz, vp],
+            "conv_gated_backward": [gp] + [vp] * 11 + [sz, vp],
+            "conv_clip_scratch_bytes": [i64, P(i64), P(sz)],
+            "conv_clip_grads": [i64, vp, vp, vp, vp, f, f, vp, vp, sz, vp],
+            "conv_linear_device_error": [P(ctypes.c_uint32), i32],
+        }.items():
+            fn = getattr(lib, name)
+            fn.argtypes = args
+            fn.restype = ctypes.c_int
+        _lib = lib
+    return _lib
+
+
+def make_linear_problem(rows, c_in, c_out, *, dtype="f32", x_stride=0, w_stride=0, residual_stride=0, y_stride=0,
+                        act="identity", alpha=0.0, beta=0.0, has_bias=False, has_residual=False,
+                        flags=0) -> LinearProblem:
+    return LinearProblem(int(rows), int(c_in), int(c_out), int(x_stride), int(w_stride), int(residual_stride),
+                         int(y_stride), LINEAR_ACTIVATIONS[act], float(alpha), float(beta), DTYPES[dtype],
+                         1 if has_bias else 0, 1 if has_residual else 0, int(flags))
+
+
+def make_gated_problem(rows, c_in, hidden, c_out, *, dtype="f32", x_stride=0, residual_stride=0, y_stride=0,
+                       act="silu", alpha=0.0, beta=0.0, has_residual=False, flags=0) -> GatedProblem:
+    return GatedProblem(int(rows), int(c_in), int(hidden), int(c_out), int(x_stride), int(residual_stride),
+                        int(y_stride), LINEAR_ACTIVATIONS[act], float(alpha), float(beta), DTYPES[dtype],
+                        1 if has_residual else 0, int(flags))
+
+
+# ---- the C functions, same names --------------------------------------------
+def _stream_handle(stream):
+    if stream is None:
+        import torch
+        return torch.cuda.current_stream().cuda_stream or None
+    return (stream.cuda_stream if hasattr(stream, "cuda_stream") else stream) or None
+
+
+def _bytes(name, p) -> int:
+    n = ctypes.c_size_t()
+    _check(getattr(_load(), name)(ctypes.byref(p), ctypes.byref(n)), name)
+    return n.value
+
+
+def conv_linear_scratch_bytes(p: LinearProblem) -> int:
+    return _bytes("conv_linear_scratch_bytes", p)
+
+
+def conv_linear_backward_scratch_bytes(p: LinearProblem) -> int:
+    return _bytes("conv_linear_backward_scratch_bytes", p)
+
+
+def conv_linear_describe_plan(p: LinearProblem, which: int, sm_count: int) -> str:
+    buf = ctypes.create_string_buffer(512)
+    _check(_load().conv_linear_describe_plan(ctypes.byref(p), int(which), int(sm_count), buf, len(buf)),
+           "conv_linear_describe_plan")
+    return buf.value.decode()
+
+
+def conv_linear_forward(p: LinearProblem, x, w, bias, residual, y, pre=None, scratch=None, scratch_bytes: int = 0,
+                        stream=None) -> None:
+    _check(_load().conv_linear_forward(ctypes.byref(p), _ptr(x), _ptr(w), _ptr(bias), _ptr(residual), _ptr(y),
+                                       _ptr(pre), _ptr(scratch), scratch_bytes, _stream_handle(stream)),
+           "conv_linear_forward")
+
+
+def conv_linear_backward(p: LinearProblem, x, w, pre, dy, dx, dw, dbias, dresidual, scratch=None,
+                         scratch_bytes: int = 0, stream=None) -> None:
+    _check(_load().conv_linear_backward(ctypes.byref(p), _ptr(x), _ptr(w), _ptr(pre), _ptr(dy), _ptr(dx), _ptr(dw),
+                                        _ptr(dbias), _ptr(dresidual), _ptr(scratch), scratch_bytes,
+                                        _stream_handle(stream)), "conv_linear_backward")
+
+
+def conv_gated_scratch_bytes(p: GatedProblem) -> int:
+    return _bytes("conv_gated_scratch_bytes", p)
+
+
+def conv_gated_backward_scratch_bytes(p: GatedProblem) -> int:
+    return _bytes("conv_gated_backward_scratch_bytes", p)
+
+
+def conv_gated_saved_bytes(p: GatedProblem) -> int:
+    return _bytes("conv_gated_saved_bytes", p)
+
+
+def conv_gated_forward(p: GatedProblem, x, w_gate, w_up, w_down, residual, y, saved=None, scratch=None,
+                       scratch_bytes: int = 0, stream=None) -> None:
+    _check(_load().conv_gated_forward(ctypes.byref(p), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down),
+                                      _ptr(residual), _ptr(y), _ptr(saved), _ptr(scratch), scratch_bytes,
+                                      _stream_handle(stream)), "conv_gated_forward")
+
+
+def conv_gated_backward(p: GatedProblem, x, w_gate, w_up, w_down, saved, dy, dx, dw_gate, dw_up, dw_down,
+                        scratch=None, scratch_bytes: int = 0, stream=None) -> None:
+    _check(_load().conv_gated_backward(ctypes.byref(p), _ptr(x), _ptr(w_gate), _ptr(w_up), _ptr(w_down), _ptr(saved),
+                                       _ptr(dy), _ptr(dx), _ptr(dw_gate), _ptr(dw_up), _ptr(dw_down), _ptr(scratch),
+                                       scratch_bytes, _stream_handle(stream)), "conv_gated_backward")
+
+
+def conv_clip_scratch_bytes(sizes) -> int:
+    n = ctypes.c_size_t()
+    sizes = (ctypes.c_int64 * len(sizes))(*sizes)
+    _check(_load().conv_clip_scratch_bytes(len(sizes), sizes, ctypes.byref(n)), "conv_clip_scratch_bytes")
+    return n.value
+
+
+def conv_clip_grads(inputs, outputs, sizes, dtypes, max_norm, eps, norm, scratch=None, scratch_bytes: int = 0,
+                    stream=None) -> None:
+    """``inputs`` / ``outputs`` (or None: the norm alone) are tensors or device
+    addresses, ``sizes`` their element counts, ``dtypes`` names of DTYPES."""
+    n = len(inputs)
+    vps = ctypes.c_void_p * n
+    _check(_load().conv_clip_grads(
+        n, vps(*[_ptr(t) for t in inputs]), None if outputs is None else vps(*[_ptr(t) for t in outputs]),
+        (ctypes.c_int64 * n)(*sizes), (ctypes.c_int32 * n)(*[DTYPES[d] for d in dtypes]), float(max_norm), float(eps),
+        _ptr(norm), _ptr(scratch), scratch_bytes, _stream_handle(stream)), "conv_clip_grads")
+
+
+def conv_linear_device_error(reset: bool = True) -> int:
+    word = ctypes.c_uint32()
+    _check(_load().conv_linear_device_error(ctypes.byref(word), 1 if reset else 0), "conv_linear_device_error")
+    return word.value
+
+
+# ---- conveniences -----------------------------------------------------------
+def _rows(t, width, what):
+    """(rows, row stride) of a tensor [..., width] whose rows are evenly spaced
+    and whose elements of a row are adjacent; ValueError for any other."""
+    shape, strides = t.shape, t.stride()
+    n = len(shape)
+    if n == 0 or shape[-1] != width:
+        raise ValueError(f"{what} must be [..., {width}], not {tuple(shape)}")
+    if width > 1 and strides[-1] != 1:
+        raise ValueError(f"{what}: the elements of a row must be adjacent")
+    rows, stride = 1, 0
+    for i in range(n - 2, -1, -1):
+        if shape[i] == 1:
+            continue
+        if stride == 0:
+            stride = strides[i]
+        elif strides[i] != stride * rows:
+            raise ValueError(f"{what}: rows must be evenly spaced")
+        rows *= shape[i]
+    if rows == 0:
+        return 0, 0
+    if rows > 1 and stride < width:
+        raise ValueError(f"{what}: rows must not overlap")
+    return rows, stride if rows > 1 else 0
+
+
+def _same(x, others):
+    for what, t in others:
+        if t is not None and (t.dtype != x.dtype or t.device != x.device):
+            raise ValueError(f"{what} must share x's element type and device")
+    if x.device.type != "cuda":
+        raise ValueError("operands must be CUDA tensors")
+
+
+class _On:
+    """The stream of a call.  Memory that torch allocates for the call belongs to
+    that stream, so that it is not handed out again while the call's kernels
+    still run; the call runs on the operands' device."""
+
+    __slots__ = ("handle", "ctx")
+
+    def __init__(self, device, stream):
+        import torch
+        self.ctx = None
+        if stream is None:
+            if device.index is not None and device.index != torch.cuda.current_device():
+                self.ctx = torch.cuda.device(device)
+            self.handle = torch.cuda.current_stream(device).cuda_stream
+        else:
+            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+            self.ctx = torch.cuda.stream(s)
+            self.handle = s.cuda_stream
+
+    def __enter__(self):
+        if self.ctx is not None:
+            self.ctx.__enter__()
+        return self.handle
+
+    def __exit__(self, *exc):
+        if self.ctx is not None:
+            self.ctx.__exit__(*exc)
+
+
+def _unaligned(tensors) -> bool:
+    return any(t is not None and t.data_ptr() % 16 for t in tensors)
+
+
+def _scratch(need, given, device):
+    """(tensor or None, bytes)"""
+    import torch
+    if given is not None:
+        return given, given.numel() * given.element_size()
+    if need == 0:
+        return None, 0
+    return torch.empty(need, dtype=torch.uint8, device=device), need
+
+
+def _dense_out(out, shape, like, what):
+    import torch
+    if out is None:
+        return torch.empty(shape, dtype=like.dtype, device=like.device)
+    if tuple(out.shape) != tuple(shape) or out.dtype != like.dtype or out.device != like.device or \
+            not out.is_contiguous():
+        raise ValueError(f"{what} must be a contiguous {tuple(shape)} tensor of x's element type and device")
+    return out
+
+
+def linear(x, w, bias=None, residual=None, *, act="identity", alpha=0.0, beta=0.0, residual_last=False, save=False,
+           out=None, scratch=None, flags=0, stream=None):
+    """y = act(x w^T + bias + residual) on CUDA tensors: x [..., c_in], w
+    [c_out, c_in], bias [c_out], residual and y [..., c_out], one element type.
+    Rows may be strided.  ``residual_last``: y = act(x w^T + bias) + residual.
+    With ``save``, returns (y, pre): pre is the activation's argument in float32
+    for ``linear_backward`` (None for the identity, which needs none)."""
+    import torch
+    dt = _dtype_name(x)
+    if w.dim() != 2:
+        raise ValueError("w must be [c_out, c_in]")
+    c_out, c_in = w.shape
+    _same(x, (("w", w), ("bias", bias), ("residual", residual), ("out", out)))
+    rows, ldx = _rows(x, c_in, "x")
+    _, ldw = _rows(w, c_in, "w")
+    y_shape = x.shape[:-1] + (c_out,)
+    ldr = ldy = 0
+    if bias is not None and (bias.dim() != 1 or bias.shape[0] != c_out or not bias.is_contiguous()):
+        raise ValueError("bias must be a contiguous [c_out]")
+    if residual is not None:
+        if residual.shape != y_shape:
+            raise ValueError("residual must have y's shape")
+        ldr = _rows(residual, c_out, "residual")[1]
+    if out is not None:
+        if out.shape != y_shape:
+            raise ValueError("out must have y's shape")
+        ldy = _rows(out, c_out, "out")[1]
+    if residual_last:
+        flags |= FLAG_LINEAR_RESIDUAL_LAST
+    if dt != "f32" and _unaligned((x, w)):
+        flags |= FLAG_LINEAR_UNALIGNED
+    with _On(x.device, stream) as handle:
+        if out is None:
+            out = torch.empty(y_shape, dtype=x.dtype, device=x.device)
+        pre = torch.empty(y_shape, dtype=torch.float32, device=x.device) if save and act != "identity" else None
+        p = LinearProblem(rows, c_in, c_out, ldx, ldw, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, DTYPES[dt],
+                          0 if bias is None else 1, 0 if residual is None else 1, flags)
+        buf, n = _scratch(conv_linear_scratch_bytes(p) if scratch is None else 0, scratch, x.device)
+        conv_linear_forward(p, x, w, bias, residual, out, pre, buf, n, handle)
+    return (out, pre) if save else out
+
+
+def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, residual_last=False, need_dx=True,
+                    need_dw=True, need_dbias=False, need_dresidual=False, dx=None, dw=None, scratch=None, flags=0,
+                    stream=None):
+    """The gradients of ``linear`` for dy [..., c_out]: (dx, dw, dbias,
+    dresidual), None where not wanted.  ``pre`` is what linear(..., save=True)
+    returned; act, alpha, beta and residual_last are that call's."""
+    import torch
+    dt = _dtype_name(x)
+    if w.dim() != 2:
+        raise ValueError("w must be [c_out, c_in]")
+    c_out, c_in = w.shape
+    _same(x, (("w", w), ("dy", dy)))
+    rows, ldx = _rows(x, c_in, "x")
+    _, ldw = _rows(w, c_in, "w")
+    if dy.shape != x.shape[:-1] + (c_out,):
+        raise ValueError("dy must have y's shape")
+    ldy = _rows(dy, c_out, "dy")[1]
+    if act != "identity":
+        if pre is None:
+            raise ValueError("this activation's gradient needs pre (linear(..., save=True))")
+        if pre.shape != dy.shape or pre.dtype != torch.float32 or pre.device != x.device or not pre.is_contiguous():
+            raise ValueError("pre must be a contiguous float32 tensor of y's shape")
+    else:
+        pre = None
+    if residual_last:
+        flags |= FLAG_LINEAR_RESIDUAL_LAST
+    if dt != "f32" and _unaligned((x if need_dw else None, w if need_dx else None, dy if pre is None else None)):
+        flags |= FLAG_LINEAR_UNALIGNED
+    with _On(x.device, stream) as handle:
+        dx = _dense_out(dx, x.shape, x, "dx") if need_dx else None
+        dw = _dense_out(dw, w.shape, x, "dw") if need_dw else None
+        dbias = torch.empty(c_out, dtype=x.dtype, device=x.device) if need_dbias else None
+        dres = torch.empty(dy.shape, dtype=x.dtype, device=x.device) if need_dresidual else None
+        p = LinearProblem(rows, c_in, c_out, ldx, ldw, 0, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, DTYPES[dt], 0, 0,
+                          flags)
+        buf, n = _scratch(conv_linear_backward_scratch_bytes(p) if scratch is None else 0, scratch, x.device)
+        conv_linear_backward(p, x, w, pre, dy, dx, dw, dbias, dres, buf, n, handle)
+    return dx, dw, dbias, dres
+
+
+def _gated(x, w_gate, w_up, w_down):
+    if w_gate.dim() != 2 or w_down.dim() != 2 or w_gate.shape != w_up.shape or w_down.shape[1] != w_gate.shape[0]:
+        raise ValueError("w_gate and w_up must be [hidden, c_in], w_down [c_out, hidden]")
+    for what, t in (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down)):
+        if not t.is_contiguous():
+            raise ValueError(f"{what} must be contiguous")
+    hidden, c_in = w_gate.shape
+    return c_in, hidden, w_down.shape[0]
+
+
+def gated_ffn(x, w_gate, w_up, w_down, residual=None, *, act="silu", alpha=0.0, beta=0.0, save=False, out=None,
+              scratch=None, flags=0, stream=None):
+    """y = (act(x w_gate^T) * (x w_up^T)) w_down^T + residual on CUDA tensors: x
+    [..., c_in], w_gate and w_up [hidden, c_in], w_down [c_out, hidden],
+    residual and y [..., c_out].  With ``save``, returns (y, saved) for
+    ``gated_ffn_backward``."""
+    import torch
+    dt = _dtype_name(x)
+    _same(x, (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down), ("residual", residual), ("out", out)))
+    c_in, hidden, c_out = _gated(x, w_gate, w_up, w_down)
+    rows, ldx = _rows(x, c_in, "x")
+    y_shape = x.shape[:-1] + (c_out,)
+    ldr = ldy = 0
+    if residual is not None:
+        if residual.shape != y_shape:
+            raise ValueError("residual must have y's shape")
+        ldr = _rows(residual, c_out, "residual")[1]
+    if out is not None:
+        if out.shape != y_shape:
+            raise ValueError("out must have y's shape")
+        ldy = _rows(out, c_out, "out")[1]
+    if dt != "f32" and _unaligned((x, w_gate, w_up, w_down)):
+        flags |= FLAG_LINEAR_UNALIGNED
+    with _On(x.device, stream) as handle:
+        if out is None:
+            out = torch.empty(y_shape, dtype=x.dtype, device=x.device)
+        p = GatedProblem(rows, c_in, hidden, c_out, ldx, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, DTYPES[dt],
+                         0 if residual is None else 1, flags)
+        saved = torch.empty(conv_gated_saved_bytes(p), dtype=torch.uint8, device=x.device) if save else None
+        buf, n = _scratch(conv_gated_scratch_bytes(p) if scratch is None else 0, scratch, x.device)
+        conv_gated_forward(p, x, w_gate, w_up, w_down, residual, out, saved, buf, n, handle)
+    return (out, saved) if save else out
+
+
+def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=0.0, beta=0.0, need_dx=True,
+                       need_dw=True, scratch=None, flags=0, stream=None):
+    """The gradients of ``gated_ffn`` for dy [..., c_out]: (dx, dw_gate, dw_up,
+    dw_down), None where not wanted.  ``saved`` is what gated_ffn(...,
+    save=True) returned; act, alpha and beta are that call's.  The residual's
+    gradient is dy."""
+    import torch
+    dt = _dtype_name(x)
+    _same(x, (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down), ("dy", dy)))
+    c_in, hidden, c_out = _gated(x, w_gate, w_up, w_down)
+    rows, ldx = _rows(x, c_in, "x")
+    if dy.shape != x.shape[:-1] + (c_out,):
+        raise ValueError("dy must have y's shape")
+    ldy = _rows(dy, c_out, "dy")[1]
+    if dt != "f32" and _unaligned((x, w_gate, w_up, w_down, dy)):
+        flags |= FLAG_LINEAR_UNALIGNED
+    p = GatedProblem(rows, c_in, hidden, c_out, ldx, 0, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, DTYPES[dt], 0, flags)
+    if saved.dtype != torch.uint8 or saved.device != x.device or saved.numel() != conv_gated_saved_bytes(p):
+        raise ValueError("saved must be what gated_ffn(..., save=True) returned for this problem")
+    with _On(x.device, stream) as handle:
+        dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
+        dws = [torch.empty(w.shape, dtype=x.dtype, device=x.device) if need_dw else None
+               for w in (w_gate, w_up, w_down)]
+        buf, n = _scratch(conv_gated_backward_scratch_bytes(p) if scratch is None else 0, scratch, x.device)
+        conv_gated_backward(p, x, w_gate, w_up, w_down, saved, dy, dx, *dws, buf, n, handle)
+    return (dx, *dws)
+
+
+def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, scratch=None, stream=None):
+    """The 2-norm of all tensors of ``grads`` together (a float32 scalar on the
+    device), and the tensors scaled by min(1, max_norm / (norm + eps)): in
+    place, or into the tensors of ``out``.  Tensors are contiguous, of any mix
+    of the element types."""
+    import torch
+    grads = list(grads)
+    outs = grads if out is None else list(out)
+    if len(outs) != len(grads):
+        raise ValueError("out must have one tensor per gradient")
+    if not grads:
+        raise ValueError("no gradients")
+    device = grads[0].device
+    if device.type != "cuda":
+        raise ValueError("operands must be CUDA tensors")
+    n = len(grads)
+    names = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
+    for g, o in zip(grads, outs):
+        if g.dtype not in names:
+            raise TypeError(f"unsupported element type {g.dtype}")
+        if not g.is_contiguous() or g.device != device:
+            raise ValueError("gradients must be contiguous and on one device")
+        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or o.device != device or not o.is_contiguous()):
+            raise ValueError("out must be contiguous tensors of the gradients' shapes and element types")
+    vps = ctypes.c_void_p * n
+    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
+    ins = vps(*[g.data_ptr() for g in grads])
+    to = ins if out is None else vps(*[o.data_ptr() for o in outs])
+    types = (ctypes.c_int32 * n)(*[names[g.dtype] for g in grads])
+    with _On(device, stream) as handle:
+        norm = torch.empty((), dtype=torch.float32, device=device)
+        if scratch is None:
+            need = ctypes.c_size_t()
+            _check(_load().conv_clip_scratch_bytes(n, sizes, ctypes.byref(need)), "conv_clip_scratch_bytes")
+            scratch = torch.empty(need.value, dtype=torch.uint8, device=device)
+        _check(_load().conv_clip_grads(n, ins, to, sizes, types, float(max_norm), float(eps), norm.data_ptr(),
+                                       scratch.data_ptr(), scratch.numel() * scratch.element_size(), handle or None),
+               "conv_clip_grads")
+    return norm

@@ -1,0 +1,174 @@
+"""The dense operators' C ABI on the host: exports, struct layouts, refusals
+before anything touches a device, and the Python checks of arguments."""
+import ctypes
+import os
+import re
+
+import pytest
+import torch
+
+import implicit_gemm_cnn_gb300 as conv
+from implicit_gemm_cnn_gb300 import build as conv_build, dense
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+OK, SHAPE, OVERFLOW, DTYPE, ACT, NULL, SCRATCH, ALIAS, DEVICE, CUDA, ARG = range(11)
+
+
+@pytest.fixture(scope="module")
+def lib():
+    conv_build.build()
+    return dense._load()
+
+
+def test_exports_every_declared_symbol(lib):
+    text = open(os.path.join(ROOT, "include", "linear.h")).read()
+    names = re.findall(r"CONV_API\s+[\w\s\*]+?\b(conv_\w+)\s*\(", text)
+    assert len(names) == 13, names
+    for name in names:
+        assert hasattr(lib, name), name
+        assert name in conv.__all__ and callable(getattr(conv, name))
+
+
+def test_struct_layouts_match_the_header():
+    assert ctypes.sizeof(conv.LinearProblem) == 88 and conv.LinearProblem.act.offset == 56
+    assert conv.LinearProblem.flags.offset == 80
+    assert ctypes.sizeof(conv.GatedProblem) == 80 and conv.GatedProblem.flags.offset == 76
+
+
+def describe(lib, **kw):
+    a = dict(rows=4, c_in=8, c_out=8, dtype="bf16")
+    a.update(kw)
+    p = conv.make_linear_problem(a.pop("rows"), a.pop("c_in"), a.pop("c_out"), **a)
+    buf = ctypes.create_string_buffer(256)
+    return lib.conv_linear_describe_plan(ctypes.byref(p), 0, 152, buf, 256)
+
+
+def test_linear_validation(lib):
+    assert describe(lib) == OK and describe(lib, rows=0) == OK
+    for kw, want in [(dict(rows=-1), SHAPE), (dict(c_in=0), SHAPE), (dict(c_out=0), SHAPE), (dict(rows=2 ** 31), SHAPE),
+                     (dict(x_stride=7), SHAPE), (dict(w_stride=7), SHAPE), (dict(y_stride=7), SHAPE),
+                     (dict(residual_stride=-1), SHAPE), (dict(x_stride=2 ** 40), SHAPE),
+                     (dict(rows=2 ** 30, c_in=2 ** 20), OVERFLOW), (dict(flags=0x100), ARG)]:
+        assert describe(lib, **kw) == want, kw
+    p = conv.make_linear_problem(4, 8, 8)
+    buf = ctypes.create_string_buffer(256)
+    ref = ctypes.byref(p)
+    assert lib.conv_linear_describe_plan(ref, 3, 152, buf, 256) == ARG
+    assert lib.conv_linear_describe_plan(ref, 0, 0, buf, 256) == ARG
+    assert lib.conv_linear_describe_plan(ref, 0, 152, None, 0) == NULL
+    assert lib.conv_linear_describe_plan(None, 0, 152, buf, 256) == NULL
+    p.dtype = 3
+    assert lib.conv_linear_describe_plan(ref, 0, 152, buf, 256) == DTYPE
+    p.dtype, p.act = 0, 11
+    assert lib.conv_linear_describe_plan(ref, 0, 152, buf, 256) == ACT
+
+
+def test_convolutions_do_not_take_the_dense_activations(lib):
+    p = conv.make_problem((1, 4, 8, 8), (4, 4, 3, 3))
+    p.act = 9
+    ho = ctypes.c_int64()
+    assert lib.conv_output_shape(ctypes.byref(p), ctypes.byref(ho), ctypes.byref(ho)) == ACT
+
+
+def test_linear_pointer_refusals(lib):
+    """Reported before a device is asked for: the addresses are never used."""
+    p = conv.make_linear_problem(4, 8, 8, has_bias=True, has_residual=True)
+    x, w, b, r, y, pre = (0x10000 * i for i in range(1, 7))
+    f = lib.conv_linear_forward
+
+    def call(*a):
+        return f(ctypes.byref(p), *a, None, 0, None)
+    for missing in range(5):
+        args = [x, w, b, r, y, pre]
+        args[missing] = None
+        assert call(*args) == NULL, missing
+    assert f(None, x, w, b, r, y, pre, None, 0, None) == NULL
+    for bad in (x + 127, w, b + 4, r + 100):
+        assert call(x, w, b, r, bad, None) == ALIAS
+    assert call(x, w, b, r, y, y + 64) == ALIAS and call(x, w, b, r, y, x) == ALIAS
+    p.rows = 0
+    assert call(None, None, None, None, None, None) == OK  # nothing to do
+    p.rows = 4
+    g = lib.conv_linear_backward
+    dy, dx, dw, db, dr = (0x100000 * i for i in range(1, 6))
+
+    def back(x, w, pre, dy, dx, dw, db, dr):
+        return g(ctypes.byref(p), x, w, pre, dy, dx, dw, db, dr, None, 0, None)
+    assert back(x, w, None, None, dx, dw, db, dr) == NULL
+    assert back(None, w, None, dy, None, dw, None, None) == NULL
+    assert back(x, None, None, dy, dx, None, None, None) == NULL
+    assert back(x, w, None, dy, dx, dx, None, None) == ALIAS and back(x, w, None, dy, dy, None, None, None) == ALIAS
+    p.act = 2
+    assert back(x, w, None, dy, dx, None, None, None) == NULL  # pre
+    if not torch.cuda.is_available():
+        p.act = 0
+        assert call(x, w, b, r, y, None) == DEVICE and back(x, w, None, dy, dx, dw, db, dr) == DEVICE
+
+
+def test_gated_refusals(lib):
+    n = ctypes.c_size_t()
+    for kw, want in [(dict(), OK), (dict(hidden=0), SHAPE), (dict(rows=-1), SHAPE), (dict(x_stride=3), SHAPE),
+                     (dict(flags=1), ARG)]:
+        a = dict(rows=4, c_in=8, hidden=16, c_out=8)
+        a.update(kw)
+        p = conv.make_gated_problem(a.pop("rows"), a.pop("c_in"), a.pop("hidden"), a.pop("c_out"), **a)
+        assert lib.conv_gated_saved_bytes(ctypes.byref(p), ctypes.byref(n)) == want, kw
+    p = conv.make_gated_problem(4, 8, 16, 8, has_residual=True)
+    x, g, u, d, r, y, s = (0x10000 * i for i in range(1, 8))
+    f = lib.conv_gated_forward
+    for missing in range(6):
+        args = [x, g, u, d, r, y]
+        args[missing] = None
+        assert f(ctypes.byref(p), *args, None, None, 0, None) == NULL
+    assert f(ctypes.byref(p), x, g, u, d, r, x, None, None, 0, None) == ALIAS
+    assert f(ctypes.byref(p), x, g, u, d, r, y, s + 16, None, 0, None) == ARG  # saved is 256-byte aligned
+    assert f(ctypes.byref(p), x, g, u, d, r, y, x, None, 0, None) == ALIAS
+    b = lib.conv_gated_backward
+    dy, dx, dg, du, dd = (0x100000 * i for i in range(1, 6))
+    assert b(ctypes.byref(p), x, g, u, d, None, dy, dx, dg, du, dd, None, 0, None) == NULL
+    assert b(ctypes.byref(p), x, g, u, d, s, None, dx, dg, du, dd, None, 0, None) == NULL
+    assert b(ctypes.byref(p), None, g, u, d, s, dy, None, dg, None, None, None, 0, None) == NULL
+    assert b(ctypes.byref(p), x, g, u, d, s, dy, dx, dg, dg, dd, None, 0, None) == ALIAS
+    # the block's saved state: g and u in float32 and h, rows of a multiple of 8 elements
+    p = conv.make_gated_problem(10, 8, 13, 8, dtype="f16")
+    assert conv.conv_gated_saved_bytes(p) == 768 + 768 + 512
+
+
+def test_clip_refusals(lib):
+    a, b, norm, scratch = 0x10000, 0x20000, 0x30000, 0x40000
+    need = conv.conv_clip_scratch_bytes([100, 50])
+
+    def call(ins=(a, b), outs=None, sizes=(100, 50), types=(0, 2), max_norm=1.0, eps=1e-6, norm=norm, scratch=scratch,
+             n=need):
+        k = len(ins)
+        vp = ctypes.c_void_p * k
+        return lib.conv_clip_grads(k, vp(*ins), vp(*(outs or ins)), (ctypes.c_int64 * k)(*sizes),
+                                   (ctypes.c_int32 * k)(*types), max_norm, eps, norm, scratch, n, None)
+    assert call(ins=(a, None)) == NULL and call(norm=None) == NULL and call(outs=(a, None)) == NULL
+    assert call(sizes=(100, -1)) == SHAPE and call(types=(0, 3)) == DTYPE
+    assert call(max_norm=-1.0) == ARG and call(max_norm=float("nan")) == ARG and call(eps=-1.0) == ARG
+    assert call(ins=(a + 2, b)) == ARG and call(ins=(a, b + 1)) == ARG
+    assert call(scratch=None) == SCRATCH and call(n=need - 1) == SCRATCH and call(scratch=scratch + 8) == SCRATCH
+    assert call(ins=(a, a + 64)) == ALIAS                      # two tensors over each other, in place
+    assert call(outs=(a + 4, b + 0x8000)) == ALIAS             # an output shifted over its input
+    assert call(outs=(0x50000, 0x50000 + 64)) == ALIAS         # outputs over each other
+    assert call(norm=a + 8) == ALIAS and call(scratch=0x10000, ins=(0x10000, b)) == ALIAS
+    assert lib.conv_clip_scratch_bytes(-1, None, ctypes.byref(ctypes.c_size_t())) == SHAPE
+    if not torch.cuda.is_available():
+        assert call() == DEVICE
+
+
+def test_python_argument_checks():
+    x, w = torch.zeros(4, 8), torch.zeros(6, 8)
+    with pytest.raises(ValueError, match="CUDA"):
+        conv.linear(x, w)
+    with pytest.raises(TypeError):
+        conv.linear(x.double(), w.double())
+    for rows, want in [(torch.zeros(3, 8), (3, 8)), (torch.zeros(2, 3, 8), (6, 8)), (torch.zeros(8), (1, 0)),
+                       (torch.zeros(3, 20)[:, 4:12], (3, 20)), (torch.zeros(0, 8), (0, 0)),
+                       (torch.zeros(2, 3, 20)[:, :, :8], (6, 20)), (torch.zeros(1, 1, 8), (1, 0))]:
+        assert dense._rows(rows, 8, "x") == want
+    for bad in (torch.zeros(3, 7), torch.zeros(8, 3).t(), torch.zeros(2, 4, 20)[:, :3, :8], torch.zeros(1, 8).expand(3, 8),
+                torch.zeros(3, 16)[:, ::2], torch.zeros(())):
+        with pytest.raises(ValueError):
+            dense._rows(bad, 8, "x")

@@ -1,0 +1,367 @@
+"""The dense operators on the GPU against their float64 definitions, each value
+within the bound that dense_ref derives for it."""
+import pytest
+import torch
+
+import implicit_gemm_cnn_gb300 as conv
+import dense_ref as ref
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+ACTS = [("identity", 0, 0), ("relu", 0, 0), ("silu", 0, 0), ("sigmoid", 0, 0), ("tanh", 0, 0), ("hard_swish", 0, 0),
+        ("hard_sigmoid", 0.2, 0.5), ("clip", -0.7, 0.9), ("leaky_relu", 0.1, 0), ("gelu", 0, 0), ("gelu_tanh", 0, 0)]
+
+
+def rand(*shape, dtype, seed, scale=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g, dtype=torch.float64) * scale).to(ref.TORCH[dtype])
+
+
+def cuda(*ts):
+    return [t.cuda() if t is not None else None for t in ts]
+
+
+def wide(*ts):
+    return [t.double() if t is not None else None for t in ts]
+
+
+def linear_case(rows, c_in, c_out, dtype, act="identity", alpha=0.0, beta=0.0, bias=True, residual=True, last=False,
+                flags=0, seed=0, scale=1.0):
+    x = rand(rows, c_in, dtype=dtype, seed=seed)
+    w = rand(c_out, c_in, dtype=dtype, seed=seed + 1, scale=scale * c_in ** -0.5)
+    b = rand(c_out, dtype=dtype, seed=seed + 2) if bias else None
+    r = rand(rows, c_out, dtype=dtype, seed=seed + 3) if residual else None
+    dy = rand(rows, c_out, dtype=dtype, seed=seed + 4, scale=0.1)
+    X, W, B, R, DY = cuda(x, w, b, r, dy)
+    y, pre = conv.linear(X, W, B, R, act=act, alpha=alpha, beta=beta, residual_last=last, save=True, flags=flags)
+    y2 = conv.linear(X, W, B, R, act=act, alpha=alpha, beta=beta, residual_last=last, flags=flags)
+    grads = conv.linear_backward(DY, X, W, pre, act=act, alpha=alpha, beta=beta, residual_last=last, need_dbias=True,
+                                 need_dresidual=True, flags=flags)
+    torch.cuda.synchronize()
+    assert conv.conv_linear_device_error() == 0
+    assert torch.equal(y, y2)
+    x, w, b, r, dy = wide(x, w, b, r, dy)
+    want = ref.linear64(x, w, b, r, act, alpha, beta, last, dtype)
+    ref.check(y, want["y"], "y")
+    if act != "identity":
+        ref.check(pre, want["z"], "pre")
+    back = ref.linear_backward64(dy, x, w, *want["z"], act, alpha, beta, last, dtype)
+    for name, got in zip(("dx", "dw", "dbias", "dresidual"), grads):
+        ref.check(got, back[name], name)
+
+
+# rows, c_in, c_out: one of everything, odd ones, sizes around tiles and ranges
+SIZES = [(1, 1, 1), (1, 8, 8), (1, 64, 129), (2, 7, 5), (3, 65, 64), (5, 200, 33), (8, 1024, 24), (12, 250, 301),
+         (16, 264, 256), (17, 512, 40), (33, 96, 1000), (64, 72, 200), (100, 136, 120), (127, 320, 257),
+         (129, 129, 127), (200, 1000, 72), (256, 64, 256), (300, 257, 515), (513, 40, 384), (640, 520, 264)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size", SIZES, ids=str)
+def test_linear_sizes(size, dtype):
+    linear_case(*size, dtype, act="gelu_tanh", seed=sum(size))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", ACTS, ids=lambda a: a[0])
+@pytest.mark.parametrize("rows", [3, 150])
+def test_linear_activations(act, dtype, rows):
+    linear_case(rows, 48, 72, dtype, *act, seed=11, scale=2.0)
+    linear_case(rows, 48, 72, dtype, *act, last=True, bias=False, seed=12, scale=2.0)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("flags", [conv.FLAG_LINEAR_FORCE_FFMA, conv.FLAG_LINEAR_NO_FEW_ROWS,
+                                   conv.FLAG_LINEAR_UNALIGNED])
+def test_linear_other_kernels(flags, dtype):
+    linear_case(9, 200, 130, dtype, act="silu", flags=flags)
+    linear_case(150, 200, 130, dtype, act="silu", flags=flags)
+
+
+def test_linear_long_sums_and_many_tiles():
+    linear_case(40, 9000, 48, "bf16", seed=21)
+    linear_case(2100, 300, 1400, "f16", act="silu", seed=22)
+    linear_case(1, 20000, 17, "f16", seed=23)
+    linear_case(70, 3000, 50, "f32", seed=24)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [0, 1, 5, 150])
+def test_linear_strides_and_alignments(rows, dtype):
+    """Rows of a wider array, at an odd offset and at an aligned one; outputs too. What lies between the rows stays."""
+    for off, pad in ((0, 8), (1, 5), (8, 24), (3, 0)):
+        c_in, c_out = 80, 56
+        xs, ws = rand(rows, c_in + off + pad, dtype=dtype, seed=1), rand(c_out, c_in + off + pad, dtype=dtype, seed=2,
+                                                                         scale=0.1)
+        rs = rand(rows, c_out + off + pad, dtype=dtype, seed=3)
+        X, W, R = cuda(xs, ws, rs)
+        full = torch.full((rows, c_out + off + pad), 77.0, dtype=ref.TORCH[dtype], device="cuda")
+        x, w, r, out = X[:, off:off + c_in], W[:, off:off + c_in], R[:, off:off + c_out], full[:, off:off + c_out]
+        y = conv.linear(x, w, None, r, act="silu", out=out)
+        torch.cuda.synchronize()
+        want = ref.linear64(*wide(x.cpu(), w.cpu(), None, r.cpu()), "silu", 0, 0, False, dtype)
+        ref.check(y, want["y"], (off, pad))
+        assert (full[:, :off] == 77).all() and (full[:, off + c_out:] == 77).all()
+        dyf = rand(rows, c_out + off + pad, dtype=dtype, seed=4).cuda()
+        dy = dyf[:, off:off + c_out]
+        dx, dw, db, _ = conv.linear_backward(dy, x, w, need_dbias=True)
+        torch.cuda.synchronize()
+        back = ref.linear_backward64(*wide(dy.cpu(), x.cpu(), w.cpu()), *want["z"], "identity", 0, 0, False, dtype)
+        for name, got in (("dx", dx), ("dw", dw), ("dbias", db)):
+            ref.check(got, back[name], (name, off, pad))
+
+
+def test_linear_unaligned_without_scratch_runs_the_cuda_core_kernel():
+    x, w = rand(40, 81, dtype="f16", seed=1).cuda()[:, 1:], rand(24, 88, dtype="f16", seed=2).cuda()[:, :80]
+    p = conv.make_linear_problem(40, 80, 24, dtype="f16", x_stride=88, w_stride=88)
+    x = torch.cat([x, x[:, :8]], 1).contiguous().flatten()[4:4 + 40 * 88 - 8]  # 8 bytes off a 16-byte boundary
+    need = conv.conv_linear_scratch_bytes(p)
+    scratch = torch.empty(max(need, 1), dtype=torch.uint8, device="cuda")
+    y = torch.empty(40, 24, dtype=torch.float16, device="cuda")
+    conv.conv_linear_forward(p, x, w, None, None, y, None, scratch, need)
+    torch.cuda.synchronize()
+    xs = torch.as_strided(x, (40, 80), (88, 1))
+    ref.check(y, ref.linear64(*wide(xs.cpu(), w.cpu(), None, None), "identity", 0, 0, False, "f16")["y"])
+
+
+def test_linear_leading_dimensions_and_another_stream():
+    x, w = rand(2, 3, 5, 64, dtype="bf16", seed=1).cuda(), rand(40, 64, dtype="bf16", seed=2, scale=0.1).cuda()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    y = conv.linear(x, w, act="gelu", stream=side)
+    y_raw = conv.linear(x, w, act="gelu", stream=side.cuda_stream)
+    side.synchronize()
+    assert y.shape == (2, 3, 5, 40) and torch.equal(y, y_raw)
+    want = ref.linear64(*wide(x.cpu().reshape(30, 64), w.cpu(), None, None), "gelu", 0, 0, False, "bf16")["y"]
+    ref.check(y.reshape(30, 40), want)
+
+
+@pytest.mark.parametrize("rows", [4, 140])
+def test_linear_infinities_and_nan_stay_in_their_rows(rows):
+    for dtype in ("f32", "f16", "bf16"):
+        x, w = rand(rows, 64, dtype=dtype, seed=1).cuda(), rand(40, 64, dtype=dtype, seed=2).cuda()
+        x[1, 5], x[2, 7] = float("nan"), float("inf")
+        y = conv.linear(x, w)
+        assert y[1].isnan().all() and not y[2].isfinite().any()
+        assert y[0].isfinite().all() and y[3:].isfinite().all()
+
+
+def test_linear_is_the_same_every_time():
+    x, w = rand(260, 2000, dtype="bf16", seed=1).cuda(), rand(136, 2000, dtype="bf16", seed=2).cuda()
+    first = conv.linear(x, w, act="silu", save=True)
+    grads = conv.linear_backward(first[0], x, w, first[1], act="silu", need_dbias=True)
+    for _ in range(3):
+        y, pre = conv.linear(x, w, act="silu", save=True)
+        again = conv.linear_backward(y, x, w, pre, act="silu", need_dbias=True)
+        for a, b in zip((y, pre) + again[:3], first + grads[:3]):
+            assert torch.equal(a, b)
+
+
+def gated_case(rows, c_in, hidden, c_out, dtype, act="silu", alpha=0.0, beta=0.0, residual=True, flags=0, seed=0):
+    x = rand(rows, c_in, dtype=dtype, seed=seed)
+    wg, wu = (rand(hidden, c_in, dtype=dtype, seed=seed + i, scale=c_in ** -0.5) for i in (1, 2))
+    wd = rand(c_out, hidden, dtype=dtype, seed=seed + 3, scale=hidden ** -0.5)
+    r = rand(rows, c_out, dtype=dtype, seed=seed + 4) if residual else None
+    dy = rand(rows, c_out, dtype=dtype, seed=seed + 5, scale=0.1)
+    X, WG, WU, WD, R, DY = cuda(x, wg, wu, wd, r, dy)
+    kw = dict(act=act, alpha=alpha, beta=beta, flags=flags)
+    y, saved = conv.gated_ffn(X, WG, WU, WD, R, save=True, **kw)
+    y2 = conv.gated_ffn(X, WG, WU, WD, R, **kw)
+    grads = conv.gated_ffn_backward(DY, X, WG, WU, WD, saved, **kw)
+    torch.cuda.synchronize()
+    assert conv.conv_linear_device_error() == 0
+    assert torch.equal(y, y2)
+    want = ref.gated64(*wide(x, wg, wu, wd, r), act, alpha, beta, dtype, dy.double())
+    for name, got in zip(("y", "dx", "dw_gate", "dw_up", "dw_down"), (y,) + grads):
+        ref.check(got, want[name], name)
+
+
+GATED = [(1, 1, 1, 1), (1, 64, 128, 64), (2, 9, 7, 5), (3, 200, 65, 33), (8, 256, 520, 256), (12, 72, 301, 40),
+         (16, 128, 136, 96), (17, 64, 200, 72), (40, 1000, 48, 56), (64, 128, 384, 128), (130, 96, 257, 80),
+         (200, 264, 129, 136), (257, 64, 500, 300), (520, 136, 264, 136)]
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("size", GATED, ids=str)
+def test_gated_sizes(size, dtype):
+    gated_case(*size, dtype, seed=sum(size))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("act", ACTS, ids=lambda a: a[0])
+@pytest.mark.parametrize("rows", [2, 140])
+def test_gated_activations(act, dtype, rows):
+    gated_case(rows, 40, 88, 56, dtype, *act, residual=False, seed=5)
+
+
+@pytest.mark.parametrize("flags", [conv.FLAG_LINEAR_FORCE_FFMA, conv.FLAG_LINEAR_NO_FEW_ROWS,
+                                   conv.FLAG_LINEAR_UNALIGNED])
+def test_gated_other_kernels(flags):
+    gated_case(7, 72, 136, 64, "bf16", flags=flags)
+    gated_case(150, 72, 136, 64, "f16", flags=flags)
+
+
+def test_gated_some_gradients_and_no_rows():
+    x, wg, wu, wd = (t.cuda() for t in (rand(70, 48, dtype="bf16", seed=1), rand(96, 48, dtype="bf16", seed=2),
+                                        rand(96, 48, dtype="bf16", seed=3), rand(48, 96, dtype="bf16", seed=4)))
+    y, saved = conv.gated_ffn(x, wg, wu, wd, save=True)
+    full = conv.gated_ffn_backward(y, x, wg, wu, wd, saved)
+    dx = conv.gated_ffn_backward(y, x, wg, wu, wd, saved, need_dw=False)
+    dw = conv.gated_ffn_backward(y, x, wg, wu, wd, saved, need_dx=False)
+    assert torch.equal(dx[0], full[0]) and dx[1:] == (None, None, None)
+    assert dw[0] is None and all(torch.equal(a, b) for a, b in zip(dw[1:], full[1:]))
+    # one of the two projections' gradients alone
+    p = conv.make_gated_problem(70, 48, 96, 48, dtype="bf16")
+    n = conv.conv_gated_backward_scratch_bytes(p)
+    scratch = torch.empty(n, dtype=torch.uint8, device="cuda")
+    for i in (1, 2):
+        one = torch.empty_like(wg)
+        conv.conv_gated_backward(p, x, wg, wu, wd, saved, y, None, one if i == 1 else None, one if i == 2 else None, None,
+                                 scratch, n)
+        assert torch.equal(one, full[i])
+    e = x[:0]
+    y, saved = conv.gated_ffn(e, wg, wu, wd, save=True)
+    none = conv.gated_ffn_backward(y, e, wg, wu, wd, saved)
+    assert y.shape == (0, 48) and none[0].shape == (0, 48) and not any(t.any() for t in none[1:])
+
+
+def test_gradients_against_differences():
+    """The gradients along a direction, against central differences of the float64 definition (step 1e-4: its own error
+    is some 1e-8 of the terms), within the sum of the values' bounds."""
+    step = 1e-4
+    x, w, b = rand(6, 20, dtype="f32", seed=1), rand(9, 20, dtype="f32", seed=2, scale=0.3), rand(9, dtype="f32", seed=3)
+    dy = rand(6, 9, dtype="f32", seed=4)
+    X, W, B, DY = cuda(x, w, b, dy)
+    for act, al, be in ACTS:
+        _, pre = conv.linear(X, W, B, act=act, alpha=al, beta=be, save=True)
+        got = conv.linear_backward(DY, X, W, pre, act=act, alpha=al, beta=be, need_dbias=True)
+        x64, w64, b64, dy64 = wide(x, w, b, dy)
+        z = ref.linear64(x64, w64, b64, None, act, al, be, False, "f32")["z"]
+        bounds = ref.linear_backward64(dy64, x64, w64, *z, act, al, be, False, "f32")
+        if any((z[0] - c).abs().min() < 1e-2 for c in ref.corners(act, al, be)):
+            continue  # a difference across a corner is no slope
+
+        def loss(x_, w_, b_):
+            return (ref.act64(x_ @ w_.T + b_, act, al, be) * dy64).sum()
+        for i, name in enumerate(("dx", "dw", "dbias")):
+            d = torch.randn((x64, w64, b64)[i].shape, generator=torch.Generator().manual_seed(i), dtype=torch.float64)
+            args = [x64, w64, b64]
+            up, down = list(args), list(args)
+            up[i], down[i] = args[i] + step * d, args[i] - step * d
+            slope = (loss(*up) - loss(*down)) / (2 * step)
+            mine = (got[i].cpu().double() * d).sum()
+            assert abs(mine - slope) <= (bounds[name][1] * d.abs()).sum() + 1e-5, (act, name)
+    wg, wu, wd = (rand(*s, dtype="f32", seed=9 + i, scale=0.3) for i, s in enumerate([(14, 20), (14, 20), (9, 14)]))
+    G, U, D = cuda(wg, wu, wd)
+    for act in ("silu", "gelu", "gelu_tanh", "tanh"):
+        _, saved = conv.gated_ffn(X, G, U, D, act=act, save=True)
+        got = conv.gated_ffn_backward(DY, X, G, U, D, saved, act=act)
+        args = wide(x, wg, wu, wd)
+        bounds = ref.gated64(*args, None, act, 0, 0, "f32", dy.double())
+
+        def block(x_, g_, u_, d_):
+            return (((ref.act64(x_ @ g_.T, act) * (x_ @ u_.T)) @ d_.T) * dy.double()).sum()
+        for i, name in enumerate(("dx", "dw_gate", "dw_up", "dw_down")):
+            d = torch.randn(args[i].shape, generator=torch.Generator().manual_seed(i), dtype=torch.float64)
+            up, down = list(args), list(args)
+            up[i], down[i] = args[i] + step * d, args[i] - step * d
+            slope = (block(*up) - block(*down)) / (2 * step)
+            mine = (got[i].cpu().double() * d).sum()
+            assert abs(mine - slope) <= (bounds[name][1] * d.abs()).sum() + 1e-5, (act, name)
+
+
+# ---- clipping ---------------------------------------------------------------
+def clip64(tensors, max_norm, eps):
+    norm = torch.stack([t.double().square().sum() for t in tensors]).sum().sqrt() if tensors else torch.tensor(0.0)
+    scale = min(1.0, float(max_norm / (norm + eps)) if float(norm) + eps else 1.0)
+    return norm, scale
+
+
+def check_clip(tensors, max_norm, eps=1e-6, out=None, **kw):
+    host = [t.cpu() for t in tensors]
+    norm, scale = clip64(host, max_norm, eps)
+    got = conv.clip_grad_norm(tensors, max_norm, eps=eps, out=out, **kw)
+    torch.cuda.synchronize()
+    # at most 32 float32 roundings per group of squares, then float64: 2^-19 of the sum, half of that of its root
+    assert abs(got.item() - norm.item()) <= 2.0 ** -19 * norm.item() + 1e-45, (got.item(), norm.item())
+    names = {torch.float32: "f32", torch.float16: "f16", torch.bfloat16: "bf16"}
+    for t, o in zip(host, tensors if out is None else out):
+        want = t.double() * scale
+        d = names[t.dtype]
+        ref.check(o, (want, (2.0 ** -18 + ref.HALF_UNIT[d]) * want.abs() + ref.TINY[d]), tuple(t.shape))
+    if out is not None:
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(tensors, host))
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("in_place", [True, False])
+@pytest.mark.parametrize("bound", [0.5, 1e6])
+def test_clip_sizes(dtype, in_place, bound):
+    sizes = [1, 3, 7, 8, 9, 16, 100, 1000, 16383, 16384, 16385, 16400, 40000, 70001, 0, 5]
+    ts = [rand(n, dtype=dtype, seed=i).cuda() for i, n in enumerate(sizes)]
+    check_clip(ts, bound, out=None if in_place else [torch.full_like(t, 3.0) for t in ts])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_clip_views_at_every_offset(dtype):
+    flat = rand(40000, dtype=dtype, seed=1).cuda()
+    out = torch.full_like(flat, 9.0)
+    for shift in (0, 1, 3):  # inputs and outputs that lie differently within 16 bytes
+        ins, outs, at = [], [], 0
+        for n in (5, 17, 1, 64, 16391, 9, 3, 20000):
+            ins.append(flat[at:at + n])
+            outs.append(out[at + shift:at + n + shift])
+            at += n + 1
+        check_clip(ins, 1.0, out=outs)
+
+
+def test_clip_many_tensors_of_mixed_types():
+    g = torch.Generator().manual_seed(3)
+    for count in (63, 64, 65, 1024, 2300):
+        sizes = torch.randint(1, 300, (count,), generator=g).tolist()
+        ts = [rand(n, dtype=("f32", "f16", "bf16")[i % 3], seed=i).cuda() for i, n in enumerate(sizes)]
+        check_clip(ts, 2.0)
+        check_clip(ts, 1.0, out=[torch.empty_like(t) for t in ts])
+
+
+@pytest.mark.parametrize("dtype,low,high", [("f32", 1e-30, 1e30), ("bf16", 1e-30, 1e30), ("f16", 1e-7, 6e4)])
+def test_clip_neither_overflows_nor_vanishes(dtype, low, high):
+    for scale in (low, high):
+        check_clip([(rand(5000, dtype="f32", seed=1).clamp(-1, 1) * scale).to(ref.TORCH[dtype]).cuda()], scale, eps=0.0)
+    mixed = torch.ones(5000, dtype=ref.TORCH[dtype])
+    mixed[::2] = high
+    check_clip([mixed.cuda(), (torch.ones(77) * low).to(ref.TORCH[dtype]).cuda()], high, eps=0.0)
+    tiny = torch.full((1000,), 2.0 ** -149 if dtype == "f32" else 2.0 ** -133 if dtype == "bf16" else 2.0 ** -24,
+                      dtype=ref.TORCH[dtype]).cuda()
+    norm = conv.clip_grad_norm([tiny.clone()], 1e30)
+    want = tiny.cpu().double().norm().item()
+    assert abs(norm.item() - want) <= 2.0 ** -19 * want + 2.0 ** -149
+
+
+def test_clip_zero_nan_and_infinity():
+    z = torch.zeros(100, device="cuda")
+    assert conv.clip_grad_norm([z], 1.0).item() == 0 and not z.any()
+    assert conv.clip_grad_norm([z], 0.0, eps=0.0).item() == 0 and not z.any()
+    a, b = torch.ones(100, device="cuda"), torch.ones(20000, device="cuda", dtype=torch.bfloat16)
+    b[777] = float("inf")
+    assert conv.clip_grad_norm([a, b], 1.0).item() == float("inf")
+    assert not a.any() and b[777].isnan() and not b[:777].any() and not b[778:].any()
+    a, b = torch.ones(100, device="cuda"), torch.ones(20000, device="cuda", dtype=torch.float16)
+    b[5] = float("nan")
+    assert conv.clip_grad_norm([a, b], 1.0).isnan() and a.isnan().all() and b.isnan().all()
+
+
+def test_clip_the_norm_alone():
+    t = rand(30000, dtype="bf16", seed=1).cuda()
+    before = t.clone()
+    norm = torch.empty((), device="cuda")
+    n = conv.conv_clip_scratch_bytes([30000])
+    scratch = torch.empty(n, dtype=torch.uint8, device="cuda")
+    conv.conv_clip_grads([t], None, [30000], ["bf16"], 1.0, 1e-6, norm, scratch, n)
+    want = before.double().norm().item()
+    assert torch.equal(t, before) and abs(norm.item() - want) <= 2.0 ** -19 * want
+    conv.conv_clip_grads([], None, [], [], 1.0, 1e-6, norm, scratch, n)
+    assert norm.item() == 0
