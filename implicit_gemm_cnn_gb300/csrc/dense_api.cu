@@ -83,38 +83,56 @@ conv_status validate(const conv_gated_problem* p, GatedShape* s) {
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // ---- one product: which kernel, and its scratch ------------------------------
-enum Variant { V_FFMA = 0 };
+enum Variant { V_FFMA = 0, V_TC = 1 };
 struct Product {
   Variant variant;
   DenseFfmaPlan ffma;
+  DenseTcPlan tc;
+  int split;
   size_t part_bytes;   // planes of the k ranges
   int launches;
 };
 
 // `g` without addresses.  `tc`: 16-bit operands with rows a tensor-core copy can take.
-Product plan_product(const DenseGemm& g, int dtype, bool tc, uint32_t flags, int sm) {
-  (void)dtype; (void)tc; (void)flags;
+Product plan_product(const DenseGemm& g, bool tc, uint32_t flags, int sm) {
+  (void)flags;
   Product r = {};
-  r.variant = V_FFMA;
-  r.ffma = dense_ffma_plan(g, sm);
-  if (r.ffma.split > 1)
-    r.part_bytes = static_cast<size_t>(r.ffma.split) * dense_products(g) * g.M * g.N * sizeof(float);
-  r.launches = r.ffma.split > 1 ? 2 : 1;
+  if (tc) {
+    r.variant = V_TC;
+    r.tc = dense_tc_plan(g, sm);
+    r.split = r.tc.split;
+  } else {
+    r.variant = V_FFMA;
+    r.ffma = dense_ffma_plan(g, sm);
+    r.split = r.ffma.split;
+  }
+  if (r.split > 1) r.part_bytes = static_cast<size_t>(r.split) * dense_products(g) * g.M * g.N * sizeof(float);
+  r.launches = r.split > 1 ? 2 : 1;
   return r;
 }
 
 cudaError_t launch_product(const Product& r, DenseGemm g, int dtype, void* part, cudaStream_t s) {
-  g.split = r.ffma.split;
-  g.k_per_split = r.ffma.k_per_split;
+  g.split = r.split;
   g.part = static_cast<float*>(part);
-  cudaError_t err = launch_dense_ffma(r.ffma, g, dtype, s);
+  cudaError_t err;
+  if (r.variant == V_TC) {
+    err = launch_dense_tc(r.tc, g, dtype, s);
+  } else {
+    g.k_per_split = r.ffma.k_per_split;
+    err = launch_dense_ffma(r.ffma, g, dtype, s);
+  }
   if (err == cudaSuccess && g.split > 1) err = launch_dense_reduce(g, dtype, s);
   return err;
 }
 
 void describe_product(const Product& r, const DenseGemm& g, int sm, char* buf, size_t len) {
-  snprintf(buf, len, "ffma tile=%dx%d split=%d products=%d sums over %lld sms=%d launches=%d", r.ffma.bm, r.ffma.bn,
-           r.ffma.split, dense_products(g), static_cast<long long>(g.segs) * g.K, sm, r.launches);
+  const long long k = static_cast<long long>(g.segs) * g.K;
+  if (r.variant == V_TC)
+    snprintf(buf, len, "tcgen05 tile=%dx%d sms_per_tile=%d tiles=%lld split=%d products=%d sums over %lld sms=%d launches=%d",
+             128 * r.tc.cg, r.tc.nt, r.tc.cg, r.tc.tiles, r.split, dense_products(g), k, sm, r.launches);
+  else
+    snprintf(buf, len, "ffma tile=%dx%d split=%d products=%d sums over %lld sms=%d launches=%d", r.ffma.bm, r.ffma.bn,
+             r.split, dense_products(g), k, sm, r.launches);
 }
 
 // A 16-bit operand's copy into aligned rows, where its rows need one.
@@ -196,7 +214,7 @@ LinearPlan plan_linear(const conv_linear_problem* p, const LinearShape& sh, cons
   e.act = p->act; e.alpha = p->act_alpha; e.beta = p->act_beta;
   e.residual_last = (p->flags & CONV_LINEAR_FLAG_RESIDUAL_LAST) != 0;
   e.ldr = sh.ldr; e.ldy = sh.ldy; e.ldp = p->c_out;
-  if (p->rows > 0) r.pfwd = plan_product(r.fwd, p->dtype, mode.tc, p->flags, sm);
+  if (p->rows > 0) r.pfwd = plan_product(r.fwd, mode.tc, p->flags, sm);
   r.part_off = l.take(r.pfwd.part_bytes);
   r.total = l.total;
   return r;
@@ -221,10 +239,10 @@ LinearPlan plan_linear_backward(const conv_linear_problem* p, const LinearShape&
     r.col_off = l.take(static_cast<size_t>(r.col_blocks) * p->c_out * sizeof(float));
     r.dx = make_gemm(p->rows, p->c_in, p->c_out, 0, 1, r.ldz, r.w.ld);
     r.dx.epi.ldy = p->c_in;
-    r.pdx = plan_product(r.dx, p->dtype, mode.tc, p->flags, sm);
+    r.pdx = plan_product(r.dx, mode.tc, p->flags, sm);
     r.dw = make_gemm(p->c_out, p->c_in, p->rows, 1, 1, r.ldz, r.x.ld);
     r.dw.epi.ldy = p->c_in;
-    r.pdw = plan_product(r.dw, p->dtype, mode.tc, p->flags, sm);
+    r.pdw = plan_product(r.dw, mode.tc, p->flags, sm);
   }
   r.part_off = l.take(std::max(r.pdx.part_bytes, r.pdw.part_bytes));
   r.total = l.total;
@@ -314,10 +332,10 @@ GatedPlan plan_gated(const conv_gated_problem* p, const GatedShape& sh, const Mo
     r.up.epi.mode = EPI_GATED;
     r.up.epi.act = p->act; r.up.epi.alpha = p->act_alpha; r.up.epi.beta = p->act_beta;
     r.up.epi.ldy = sh.ldh; r.up.epi.ldp = sh.ldh;
-    r.pup = plan_product(r.up, p->dtype, mode.tc, p->flags, sm);
+    r.pup = plan_product(r.up, mode.tc, p->flags, sm);
     r.down = make_gemm(p->rows, p->c_out, p->hidden, 0, 0, sh.ldh, r.wd.ld);
     r.down.epi.ldr = sh.ldr; r.down.epi.ldy = sh.ldy;
-    r.pdown = plan_product(r.down, p->dtype, mode.tc, p->flags, sm);
+    r.pdown = plan_product(r.down, mode.tc, p->flags, sm);
   }
   r.part_off = l.take(std::max(r.pup.part_bytes, r.pdown.part_bytes));
   r.total = l.total;
@@ -341,18 +359,18 @@ GatedPlan plan_gated_backward(const conv_gated_problem* p, const GatedShape& sh,
     r.dh.epi.mode = EPI_GATED_BWD;
     r.dh.epi.act = p->act; r.dh.epi.alpha = p->act_alpha; r.dh.epi.beta = p->act_beta;
     r.dh.epi.ldy = sh.ldh; r.dh.epi.ldp = sh.ldh;
-    r.pdh = plan_product(r.dh, p->dtype, mode.tc, p->flags, sm);
+    r.pdh = plan_product(r.dh, mode.tc, p->flags, sm);
     r.dx = make_gemm(p->rows, p->c_in, p->hidden, 0, 1, sh.ldh, r.wg.ld);
     r.dx.segs = 2;
     r.dx.epi.ldy = p->c_in;
-    r.pdx = plan_product(r.dx, p->dtype, mode.tc, p->flags, sm);
+    r.pdx = plan_product(r.dx, mode.tc, p->flags, sm);
     r.dwgu = make_gemm(p->hidden, p->c_in, p->rows, 1, 1, sh.ldh, r.x.ld);
     r.dwgu.batch = 2;
     r.dwgu.epi.ldy = p->c_in;
-    r.pdwgu = plan_product(r.dwgu, p->dtype, mode.tc, p->flags, sm);
+    r.pdwgu = plan_product(r.dwgu, mode.tc, p->flags, sm);
     r.dwd = make_gemm(p->c_out, p->hidden, p->rows, 1, 1, r.dy.ld, sh.ldh);
     r.dwd.epi.ldy = p->hidden;
-    r.pdwd = plan_product(r.dwd, p->dtype, mode.tc, p->flags, sm);
+    r.pdwd = plan_product(r.dwd, mode.tc, p->flags, sm);
   }
   r.part_off = l.take(std::max({r.pdh.part_bytes, r.pdx.part_bytes, r.pdwgu.part_bytes, r.pdwd.part_bytes}));
   r.total = l.total;
@@ -758,11 +776,10 @@ conv_status conv_clip_grads(int64_t count, const void* const* in, void* const* o
 
 conv_status conv_linear_device_error(uint32_t* word, int32_t reset) {
   if (!word) return CONV_ERR_NULL;
-  (void)reset;
   int dev, sm;
   const conv_status st = current_device(&dev, &sm);
   if (st != CONV_OK) return st;
-  *word = 0;
+  CONV_TRY(dense_error_word(word, reset));
   return CONV_OK;
 }
 

@@ -17,6 +17,18 @@ struct DenseFfmaPlan {
 DenseFfmaPlan dense_ffma_plan(const DenseGemm& g, int sm);
 cudaError_t launch_dense_ffma(const DenseFfmaPlan& p, const DenseGemm& g, int dtype, cudaStream_t s);
 
+// Tensor-core product (dense_tc.cuh): 16-bit operands on 16-byte boundaries.
+struct DenseTcPlan {
+  int cg, nt;       // SMs per tile, MMA columns: tiles of 128 * cg x nt (nt / 2 gated)
+  int split;        // k ranges
+  int kb_range;     // 64-term blocks of a range
+  long long tiles;
+  int blocks;       // persistent blocks
+};
+DenseTcPlan dense_tc_plan(const DenseGemm& g, int sm);
+cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype, cudaStream_t s);
+cudaError_t dense_error_word(uint32_t* word, int reset);
+
 // Adds the k ranges' planes in order and applies the epilogue.
 cudaError_t launch_dense_reduce(const DenseGemm& g, int dtype, cudaStream_t s);
 

@@ -1,0 +1,186 @@
+// dense_tc.cu -- the tensor-core product's host side: tile choice, tensor maps,
+// launch, and the error word of its bounded waits.
+#include <string.h>
+
+#include <algorithm>
+#include <mutex>
+
+#include <cudaTypedefs.h>
+
+#include "dense_tc.cuh"
+
+namespace conv {
+
+cudaError_t launch_dense_tc_f16(const DenseTcPlan& t, int mode, const DenseTcArgs& args, const DenseTcMaps& maps,
+                                cudaStream_t s);
+cudaError_t launch_dense_tc_bf16(const DenseTcPlan& t, int mode, const DenseTcArgs& args, const DenseTcMaps& maps,
+                                 cudaStream_t s);
+
+namespace {
+
+__device__ uint32_t g_dense_err;
+
+// The driver's tensor-map encoder, looked up once.
+PFN_cuTensorMapEncodeTiled_v12000 encoder() {
+  static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+  static std::once_flag once;
+  std::call_once(once, [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+        q == cudaDriverEntryPointSuccess)
+      fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    else
+      cudaGetLastError();
+  });
+  return fn;
+}
+// The error word's address on the current device, looked up once per device.
+uint32_t* error_word() {
+  static std::mutex mu;
+  static uint32_t* at[64] = {};
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) {
+    cudaGetLastError();
+    return nullptr;
+  }
+  std::lock_guard<std::mutex> lock(mu);
+  if (!at[dev]) {
+    void* p = nullptr;
+    if (cudaGetSymbolAddress(&p, g_dense_err) != cudaSuccess) {
+      cudaGetLastError();
+      return nullptr;
+    }
+    at[dev] = static_cast<uint32_t*>(p);
+  }
+  return at[dev];
+}
+
+// A row-major matrix (planes of them, if planes > 0) as a tensor map with boxes
+// of 128 bytes of a row x box_rows rows, 128-byte swizzle, zeros outside.
+bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long inner, long long rows, long long ld,
+            int planes, int box_rows) {
+  const size_t es = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
+                              static_cast<cuuint64_t>(std::max(planes, 1))};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * es, static_cast<cuuint64_t>(ld) * es * rows};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return encoder()(map, type, planes > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, step,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool aligned(const void* p, long long ld, size_t es) {
+  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<long long>(es) % 16 == 0;
+}
+
+}  // namespace
+
+DenseTcPlan dense_tc_plan(const DenseGemm& g, int sm) {
+  DenseTcPlan best = {};
+  const int kb = static_cast<int>((static_cast<long long>(g.K) + dtc::kBK - 1) / dtc::kBK) * g.segs;
+  const int products = dense_products(g);
+  double best_t = 0.0;
+  for (int cg = 2; cg >= 1; --cg) {
+    const int nt = cg == 2 ? 256 : 128;
+    const long long slots = sm / cg;
+    for (int split = 1; split <= 16; ++split) {
+      // a gated product whose k is split runs as two products (its planes meet in the second launch)
+      const int cols = g.dual && split == 1 ? nt / 2 : nt;
+      const long long tiles = ((g.M + 128LL * cg - 1) / (128 * cg)) * ((static_cast<long long>(g.N) + cols - 1) / cols) *
+                              (g.dual && split > 1 ? 2 : g.batch);
+      if (split > 1 && kb / split < 4) break;
+      const int range = (kb + split - 1) / split;
+      const int ranges = (kb + range - 1) / range;
+      if (ranges != split) continue;
+      const long long units = tiles * split;
+      if (split > 1 && units > 2 * slots) break;
+      // clocks: 64 terms of a tile are 512 (pair) or 300 (one SM; its shared memory is the bound) clocks; a tile's
+      // start and end, and the ranges' planes through memory at some 3000 bytes per clock with a second launch
+      const double per = cg == 2 ? 512.0 : 300.0;
+      double t = static_cast<double>((units + slots - 1) / slots) * (range * per + 800.0) + 2500.0;
+      if (split > 1) t += 4000.0 + 2.0 * split * products * 4.0 * g.M * g.N / 3000.0;
+      if (!best.cg || t < best_t) {
+        best_t = t;
+        best.cg = cg; best.nt = nt; best.split = split; best.kb_range = range;
+        best.tiles = tiles;
+        best.blocks = static_cast<int>(std::min(units, slots)) * cg;
+      }
+    }
+  }
+  return best;
+}
+
+cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dtype, cudaStream_t s) {
+  if (!encoder()) return cudaErrorNotSupported;
+  DenseGemm g = given;
+  if (g.dual && t.split > 1) {
+    g.dual = 0;
+    g.batch = 2;
+    g.a[1] = g.a[0];
+  }
+  DenseTcArgs p;
+  DenseTcMaps maps;
+  memset(&p, 0, sizeof(p));
+  memset(&maps, 0, sizeof(maps));
+  p.M = g.M; p.N = g.N;
+  p.segs = g.segs; p.batch = g.batch; p.dual = g.dual; p.a_mn = g.a_mn; p.b_mn = g.b_mn;
+  p.kb_seg = static_cast<int>((static_cast<long long>(g.K) + dtc::kBK - 1) / dtc::kBK);
+  p.kb_total = p.kb_seg * g.segs;
+  p.kb_range = t.kb_range;
+  p.split = t.split;
+  const int cols = g.dual ? t.nt / 2 : t.nt;
+  p.mtiles = static_cast<int>((g.M + 128LL * t.cg - 1) / (128 * t.cg));
+  p.ntiles = static_cast<int>((static_cast<long long>(g.N) + cols - 1) / cols);
+  p.tiles = p.mtiles * p.ntiles * g.batch;
+  p.units = p.tiles * t.split;
+  p.group = 8;
+  p.epi = g.epi;
+  p.part = g.part;
+  p.err = error_word();
+  if (!p.err) return cudaErrorNotSupported;
+  const CUtensorMapDataType type = dtype == CONV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
+  const int b_rows = g.dual && t.cg == 1 ? t.nt / 2 : t.nt / t.cg;
+  const int as = std::max(g.segs, g.batch), bs = g.segs > 1 || g.batch > 1 || g.dual ? 2 : 1;
+  bool ok = true;
+  for (int i = 0; i < as; ++i)
+    ok = ok && (g.a_mn ? encode(&maps.a[i], type, g.a[i], g.M, g.K, g.lda, 0, 64)
+                       : encode(&maps.a[i], type, g.a[i], g.K, g.M, g.lda, 0, 128));
+  for (int i = 0; i < bs; ++i)
+    ok = ok && (g.b_mn ? encode(&maps.b[i], type, g.b[i], g.N, g.K, g.ldb, 0, 64)
+                       : encode(&maps.b[i], type, g.b[i], g.K, g.N, g.ldb, 0, b_rows));
+  const int mode = t.split > 1 ? EPI_PARTIAL : g.epi.mode;
+  if (mode == EPI_PARTIAL) {
+    const int planes = t.split * dense_products(g);
+    p.tma_pre = aligned(g.part, g.N, 4);
+    if (p.tma_pre) ok = ok && encode(&maps.pre[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.part, g.N, g.M, g.N, planes, 32);
+  } else {
+    const bool two = mode == EPI_GATED_BWD || g.batch > 1;
+    p.tma_y = aligned(g.epi.y, g.epi.ldy, 2) && (!two || aligned(g.epi.y2, g.epi.ldy, 2));
+    if (p.tma_y) {
+      ok = ok && encode(&maps.y[0], type, g.epi.y, g.N, g.M, g.epi.ldy, 0, 32);
+      if (two) ok = ok && encode(&maps.y[1], type, g.epi.y2, g.N, g.M, g.epi.ldy, 0, 32);
+    }
+    if (mode != EPI_GATED_BWD && g.epi.pre) {
+      p.tma_pre = aligned(g.epi.pre, g.epi.ldp, 4);
+      if (p.tma_pre) {
+        ok = ok && encode(&maps.pre[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.epi.pre, g.N, g.M, g.epi.ldp, 0, 32);
+        if (mode == EPI_GATED)
+          ok = ok && encode(&maps.pre[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.epi.pre2, g.N, g.M, g.epi.ldp, 0, 32);
+      }
+    }
+  }
+  if (!ok) return cudaErrorInvalidValue;
+  return dtype == CONV_F16 ? launch_dense_tc_f16(t, mode, p, maps, s) : launch_dense_tc_bf16(t, mode, p, maps, s);
+}
+
+cudaError_t dense_error_word(uint32_t* word, int reset) {
+  cudaError_t err = cudaDeviceSynchronize();
+  if (err != cudaSuccess) return err;
+  err = cudaMemcpyFromSymbol(word, g_dense_err, sizeof(uint32_t));
+  if (err != cudaSuccess || !reset) return err;
+  const uint32_t zero = 0;
+  return cudaMemcpyToSymbol(g_dense_err, &zero, sizeof(uint32_t));
+}
+
+}  // namespace conv

@@ -1,0 +1,9 @@
+// dense_tc_bf16.cu -- the tensor-core products of bfloat16 operands.
+#include "dense_tc_launch.cuh"
+
+namespace conv {
+cudaError_t launch_dense_tc_bf16(const DenseTcPlan& t, int mode, const DenseTcArgs& args, const DenseTcMaps& maps,
+                                 cudaStream_t s) {
+  return dtc::by_tile<__nv_bfloat16>(t, mode, args, maps, s);
+}
+}  // namespace conv
