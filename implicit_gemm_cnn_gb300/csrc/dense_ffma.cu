@@ -218,47 +218,95 @@ __global__ void __launch_bounds__(256) dense_repack(const uint16_t* in, long lon
   }
 }
 
-// dz and the column sums of a row block: a thread takes two columns of every
-// eighth row of the block; the eight partial sums are added in order.
-template <typename T>
+// dz and the column sums of a row block, bound by the bytes (dy, pre in; dz out).  A warp takes 32 * V columns of every
+// eighth row of the block (V columns per lane: 16 bytes of 16-bit values, or of float32), four rows in flight; the
+// eight warps' partial sums are added in order.  VEC: every row of dy, pre and dz begins on a 16-byte boundary.
+template <typename T, bool VEC>
 __global__ void __launch_bounds__(256) dense_dz(const T* dy, long long ld_dy, const float* pre, T* dz, long long ld_dz,
                                                 float* part, int rows_per_block, long long rows, long long cols,
                                                 int act, float alpha, float beta) {
   constexpr bool FAST = sizeof(T) == 2;
-  __shared__ float2 sums[8][32];
+  constexpr int V = VEC ? 16 / sizeof(T) : 2;
+  constexpr int U = 4;
+  __shared__ float sums[8][32 * V];
   const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
-  const long long c = static_cast<long long>(blockIdx.x) * 64 + tx * 2;
+  const long long c = (static_cast<long long>(blockIdx.x) * 32 + tx) * V;
   const long long r0 = static_cast<long long>(blockIdx.y) * rows_per_block;
   const long long r1 = min(r0 + rows_per_block, rows);
-  const bool ok0 = c < cols, ok1 = c + 1 < cols;
-  float2 sum = make_float2(0.0f, 0.0f);
-  for (long long r = r0 + ty; r < r1; r += 8) {
-    float v[2] = {0.0f, 0.0f};
-    if (ok0) v[0] = to_f32(dy[r * ld_dy + c]);
-    if (ok1) v[1] = to_f32(dy[r * ld_dy + c + 1]);
-    if (act != ACT_IDENTITY) {
-      float t[2] = {ok0 ? pre[r * cols + c] : 0.0f, ok1 ? pre[r * cols + c + 1] : 0.0f}, d[2];
-      dense_activate_grad<FAST, 2>(t, d, act, alpha, beta);
-      v[0] *= d[0];
-      v[1] *= d[1];
+  const int n = static_cast<int>(min(static_cast<long long>(V), cols - c));  // columns that exist
+  const bool wide = VEC && n == V;
+  float sum[V];
+#pragma unroll
+  for (int j = 0; j < V; ++j) sum[j] = 0.0f;
+  for (long long r = r0 + ty; r < r1; r += 8 * U) {
+    T raw[U][V];
+    float t[U][V];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long row = r + 8 * u;
+      if (row >= r1) continue;
+      const T* src = dy + row * ld_dy + c;
+      const float* arg = pre + row * cols + c;
+      if (wide) {
+        if constexpr (VEC) {
+          *reinterpret_cast<uint4*>(raw[u]) = __ldcs(reinterpret_cast<const uint4*>(src));
+          if (act != ACT_IDENTITY) {
+#pragma unroll
+            for (int q = 0; q < V / 4; ++q)
+              *reinterpret_cast<float4*>(&t[u][4 * q]) = __ldcs(reinterpret_cast<const float4*>(arg) + q);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+          if (j < n) {
+            raw[u][j] = src[j];
+            if (act != ACT_IDENTITY) t[u][j] = arg[j];
+          }
+      }
     }
-    if (dz) {
-      if (ok0) dz[r * ld_dz + c] = from_f32<T>(v[0]);
-      if (ok1) dz[r * ld_dz + c + 1] = from_f32<T>(v[1]);
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const long long row = r + 8 * u;
+      if (row >= r1) continue;
+      float v[V];
+#pragma unroll
+      for (int j = 0; j < V; ++j) v[j] = j < n ? to_f32(raw[u][j]) : 0.0f;
+      if (act != ACT_IDENTITY) {
+        float a[V], d[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) a[j] = j < n ? t[u][j] : 0.0f;
+        dense_activate_grad<FAST, V>(a, d, act, alpha, beta);
+#pragma unroll
+        for (int j = 0; j < V; ++j) v[j] = j < n ? v[j] * d[j] : 0.0f;
+      }
+      if (dz) {
+        T out[V];
+#pragma unroll
+        for (int j = 0; j < V; ++j) out[j] = from_f32<T>(v[j]);
+        T* dst = dz + row * ld_dz + c;
+        if (wide) {
+          if constexpr (VEC) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(out);
+        } else {
+#pragma unroll
+          for (int j = 0; j < V; ++j)
+            if (j < n) dst[j] = out[j];
+        }
+      }
+#pragma unroll
+      for (int j = 0; j < V; ++j) sum[j] += v[j];
     }
-    sum.x += v[0];
-    sum.y += v[1];
   }
   if (!part) return;
-  sums[ty][tx] = sum;
-  __syncthreads();
-  if (ty == 0) {
-    float2 t = sums[0][tx];
 #pragma unroll
-    for (int i = 1; i < 8; ++i) { t.x += sums[i][tx].x; t.y += sums[i][tx].y; }
-    float* p = part + static_cast<long long>(blockIdx.y) * cols + c;
-    if (ok0) p[0] = t.x;
-    if (ok1) p[1] = t.y;
+  for (int j = 0; j < V; ++j) sums[ty][tx * V + j] = sum[j];
+  __syncthreads();
+  for (int i = threadIdx.x; i < 32 * V; i += 256) {
+    float s = sums[0][i];
+#pragma unroll
+    for (int w = 1; w < 8; ++w) s += sums[w][i];
+    const long long col = static_cast<long long>(blockIdx.x) * 32 * V + i;
+    if (col < cols) part[static_cast<long long>(blockIdx.y) * cols + col] = s;
   }
 }
 template <typename T>
@@ -288,9 +336,13 @@ template <typename T>
 cudaError_t dz_go(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, void* dbias, float* part,
                   int blocks, long long rows, long long cols, int act, float alpha, float beta, cudaStream_t s) {
   const int per = static_cast<int>((rows + blocks - 1) / blocks);
-  const dim3 grid(static_cast<unsigned>((cols + 63) / 64), static_cast<unsigned>((rows + per - 1) / per));
-  dense_dz<T><<<grid, 256, 0, s>>>(static_cast<const T*>(dy), ld_dy, pre, static_cast<T*>(dz), ld_dz,
-                                   dbias ? part : nullptr, per, rows, cols, act, alpha, beta);
+  auto on16 = [](const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && bytes % 16 == 0; };
+  const bool vec = on16(dy, ld_dy * sizeof(T)) && on16(pre, cols * 4) && on16(dz, ld_dz * sizeof(T));
+  const long long strip = 32 * (vec ? 16 / static_cast<long long>(sizeof(T)) : 2);
+  const dim3 grid(static_cast<unsigned>((cols + strip - 1) / strip), static_cast<unsigned>((rows + per - 1) / per));
+  auto kern = vec ? dense_dz<T, true> : dense_dz<T, false>;
+  kern<<<grid, 256, 0, s>>>(static_cast<const T*>(dy), ld_dy, pre, static_cast<T*>(dz), ld_dz, dbias ? part : nullptr, per,
+                            rows, cols, act, alpha, beta);
   cudaError_t err = cudaGetLastError();
   if (err != cudaSuccess || !dbias) return err;
   dense_colsum<T><<<static_cast<unsigned>((cols + 255) / 256), 256, 0, s>>>(part, static_cast<T*>(dbias),
@@ -349,9 +401,9 @@ cudaError_t launch_dense_repack(const void* in, long long ld_in, void* out, long
 }
 
 int dense_col_blocks(long long rows, long long cols, int sm) {
-  // row blocks of at least kColRowsMin rows, about 16 blocks per SM in all
-  const long long strips = (cols + 63) / 64;
-  const long long want = std::max<long long>(1, 16LL * sm / strips);
+  // row blocks of at least kColRowsMin rows, about 8 blocks per SM in all
+  const long long strips = (cols + 255) / 256;
+  const long long want = std::max<long long>(1, 8LL * sm / strips);
   return static_cast<int>(std::max<long long>(1, std::min<long long>({want, (rows + kColRowsMin - 1) / kColRowsMin, 65535})));
 }
 

@@ -11,10 +11,10 @@
 
 namespace conv {
 
-cudaError_t launch_dense_tc_f16(const DenseTcPlan& t, int mode, const DenseTcArgs& args, const DenseTcMaps& maps,
-                                cudaStream_t s);
-cudaError_t launch_dense_tc_bf16(const DenseTcPlan& t, int mode, const DenseTcArgs& args, const DenseTcMaps& maps,
-                                 cudaStream_t s);
+cudaError_t launch_dense_tc_f16(const DenseTcPlan& t, int mode, int a_mn, int b_mn, const DenseTcArgs& args,
+                                const DenseTcMaps& maps, cudaStream_t s);
+cudaError_t launch_dense_tc_bf16(const DenseTcPlan& t, int mode, int a_mn, int b_mn, const DenseTcArgs& args,
+                                 const DenseTcMaps& maps, cudaStream_t s);
 
 namespace {
 
@@ -57,17 +57,31 @@ uint32_t* error_word() {
 }
 
 // A row-major matrix (planes of them, if planes > 0) as a tensor map with boxes
-// of 128 bytes of a row x box_rows rows, 128-byte swizzle, zeros outside.
+// of `box_bytes` (128 or 64) of a row x box_rows rows, swizzled over as many bytes, zeros outside.
 bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long inner, long long rows, long long ld,
-            int planes, int box_rows) {
+            int planes, int box_rows, int box_bytes = 128) {
   const size_t es = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
   const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
                               static_cast<cuuint64_t>(std::max(planes, 1))};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * es, static_cast<cuuint64_t>(ld) * es * rows};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows), 1};
+  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / es), static_cast<cuuint32_t>(box_rows), 1};
   const cuuint32_t step[3] = {1, 1, 1};
   return encoder()(map, type, planes > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, step,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+// An mn-major operand's matrix (rows of `inner` values, inner a multiple of 64) as a map of 64-wide column blocks: one
+// copy brings `blocks` of them, one after another.
+bool encode_blocks(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long inner, long long rows,
+                   long long ld, int blocks) {
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(inner / 64)};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, 128};
+  const cuuint32_t box[3] = {64, 64, static_cast<cuuint32_t>(blocks)};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return encoder()(map, type, 3, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 bool aligned(const void* p, long long ld, size_t es) {
@@ -76,35 +90,38 @@ bool aligned(const void* p, long long ld, size_t es) {
 
 }  // namespace
 
+// The tile and the k ranges of least time by this model, in clocks, fitted to full waves of 4096-term sums (bfloat16,
+// 1.85 GHz): 64 terms of a pair's tile take 165 + 1.73 nt (608 at nt = 256, 386 at 128: 512 and 256 are the MMAs
+// alone), of one SM's 128 columns 415 (its stage is as many bytes as the pair's of 256); a tile adds 600, a launch
+// 6000, the ranges' planes pass through L2 twice at some 3000 bytes a clock, with a launch of their own.
 DenseTcPlan dense_tc_plan(const DenseGemm& g, int sm) {
   DenseTcPlan best = {};
   const int kb = static_cast<int>((static_cast<long long>(g.K) + dtc::kBK - 1) / dtc::kBK) * g.segs;
   const int products = dense_products(g);
   double best_t = 0.0;
   for (int cg = 2; cg >= 1; --cg) {
-    const int nt = cg == 2 ? 256 : 128;
     const long long slots = sm / cg;
-    for (int split = 1; split <= 16; ++split) {
-      // a gated product whose k is split runs as two products (its planes meet in the second launch)
-      const int cols = g.dual && split == 1 ? nt / 2 : nt;
-      const long long tiles = ((g.M + 128LL * cg - 1) / (128 * cg)) * ((static_cast<long long>(g.N) + cols - 1) / cols) *
-                              (g.dual && split > 1 ? 2 : g.batch);
-      if (split > 1 && kb / split < 4) break;
-      const int range = (kb + split - 1) / split;
-      const int ranges = (kb + range - 1) / range;
-      if (ranges != split) continue;
-      const long long units = tiles * split;
-      if (split > 1 && units > 2 * slots) break;
-      // clocks: 64 terms of a tile are 512 (pair) or 300 (one SM; its shared memory is the bound) clocks; a tile's
-      // start and end, and the ranges' planes through memory at some 3000 bytes per clock with a second launch
-      const double per = cg == 2 ? 512.0 : 300.0;
-      double t = static_cast<double>((units + slots - 1) / slots) * (range * per + 800.0) + 2500.0;
-      if (split > 1) t += 4000.0 + 2.0 * split * products * 4.0 * g.M * g.N / 3000.0;
-      if (!best.cg || t < best_t) {
-        best_t = t;
-        best.cg = cg; best.nt = nt; best.split = split; best.kb_range = range;
-        best.tiles = tiles;
-        best.blocks = static_cast<int>(std::min(units, slots)) * cg;
+    for (int nt = cg == 2 ? 256 : 128; nt >= 64; nt -= 32) {
+      if (g.dual && nt % 64) continue;
+      for (int split = 1; split <= 16; ++split) {
+        if (split > 1 && kb / split < 4) break;
+        // a gated product whose k is split runs as two products (its planes meet in the second launch)
+        const int cols = g.dual && split == 1 ? nt / 2 : nt;
+        const long long tiles = ((g.M + 128LL * cg - 1) / (128 * cg)) * ((static_cast<long long>(g.N) + cols - 1) / cols) *
+                                (g.dual && split > 1 ? 2 : g.batch);
+        const int range = (kb + split - 1) / split;
+        if ((kb + range - 1) / range != split) continue;  // every range holds terms
+        const long long units = tiles * split;
+        if (split > 1 && units > 2 * slots) break;
+        const double per = cg == 2 ? 165.0 + 1.73 * nt : 190.0 + 1.76 * nt;
+        double t = static_cast<double>((units + slots - 1) / slots) * (range * per + 600.0) + 6000.0;
+        if (split > 1) t += 4000.0 + 2.0 * split * products * 4.0 * g.M * g.N / 3000.0;
+        if (!best.cg || t < best_t) {
+          best_t = t;
+          best.cg = cg; best.nt = nt; best.split = split; best.kb_range = range;
+          best.tiles = tiles;
+          best.blocks = static_cast<int>(std::min(units, slots)) * cg;
+        }
       }
     }
   }
@@ -124,7 +141,8 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
   memset(&p, 0, sizeof(p));
   memset(&maps, 0, sizeof(maps));
   p.M = g.M; p.N = g.N;
-  p.segs = g.segs; p.batch = g.batch; p.dual = g.dual; p.a_mn = g.a_mn; p.b_mn = g.b_mn;
+  p.segs = g.segs; p.batch = g.batch;
+  p.nt = t.nt;
   p.kb_seg = static_cast<int>((static_cast<long long>(g.K) + dtc::kBK - 1) / dtc::kBK);
   p.kb_total = p.kb_seg * g.segs;
   p.kb_range = t.kb_range;
@@ -134,7 +152,7 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
   p.ntiles = static_cast<int>((static_cast<long long>(g.N) + cols - 1) / cols);
   p.tiles = p.mtiles * p.ntiles * g.batch;
   p.units = p.tiles * t.split;
-  p.group = 8;
+  p.group = 16;  // 8 to 19 rows of tiles measured alike, 1 and 32 some 5% slower
   p.epi = g.epi;
   p.part = g.part;
   p.err = error_word();
@@ -142,12 +160,15 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
   const CUtensorMapDataType type = dtype == CONV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int b_rows = g.dual && t.cg == 1 ? t.nt / 2 : t.nt / t.cg;
   const int as = std::max(g.segs, g.batch), bs = g.segs > 1 || g.batch > 1 || g.dual ? 2 : 1;
+  // one copy per operand and stage where the blocks of 64 divide the matrix and the block's share of the tile
+  p.a_3d = g.a_mn && g.M % 64 == 0;
+  p.b_3d = g.b_mn && g.N % 64 == 0 && b_rows % 64 == 0;
   bool ok = true;
   for (int i = 0; i < as; ++i)
-    ok = ok && (g.a_mn ? encode(&maps.a[i], type, g.a[i], g.M, g.K, g.lda, 0, 64)
+    ok = ok && (p.a_3d ? encode_blocks(&maps.a[i], type, g.a[i], g.M, g.K, g.lda, 2) : g.a_mn ? encode(&maps.a[i], type, g.a[i], g.M, g.K, g.lda, 0, 64)
                        : encode(&maps.a[i], type, g.a[i], g.K, g.M, g.lda, 0, 128));
   for (int i = 0; i < bs; ++i)
-    ok = ok && (g.b_mn ? encode(&maps.b[i], type, g.b[i], g.N, g.K, g.ldb, 0, 64)
+    ok = ok && (p.b_3d ? encode_blocks(&maps.b[i], type, g.b[i], g.N, g.K, g.ldb, b_rows / 64) : g.b_mn ? encode(&maps.b[i], type, g.b[i], g.N, g.K, g.ldb, 0, 64)
                        : encode(&maps.b[i], type, g.b[i], g.K, g.N, g.ldb, 0, b_rows));
   const int mode = t.split > 1 ? EPI_PARTIAL : g.epi.mode;
   if (mode == EPI_PARTIAL) {
@@ -158,20 +179,23 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
     const bool two = mode == EPI_GATED_BWD || g.batch > 1;
     p.tma_y = aligned(g.epi.y, g.epi.ldy, 2) && (!two || aligned(g.epi.y2, g.epi.ldy, 2));
     if (p.tma_y) {
-      ok = ok && encode(&maps.y[0], type, g.epi.y, g.N, g.M, g.epi.ldy, 0, 32);
-      if (two) ok = ok && encode(&maps.y[1], type, g.epi.y2, g.N, g.M, g.epi.ldy, 0, 32);
+      ok = ok && encode(&maps.y[0], type, g.epi.y, g.N, g.M, g.epi.ldy, 0, 32, 64);
+      if (two) ok = ok && encode(&maps.y[1], type, g.epi.y2, g.N, g.M, g.epi.ldy, 0, 32, 64);
     }
-    if (mode != EPI_GATED_BWD && g.epi.pre) {
+    if (mode == EPI_GATED_BWD && !(p.tma_y && aligned(g.epi.pre, g.epi.ldp, 4) && aligned(g.epi.pre2, g.epi.ldp, 4)))
+      return cudaErrorInvalidValue;  // the library's own layout
+    if (g.epi.pre) {
       p.tma_pre = aligned(g.epi.pre, g.epi.ldp, 4);
       if (p.tma_pre) {
         ok = ok && encode(&maps.pre[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.epi.pre, g.N, g.M, g.epi.ldp, 0, 32);
-        if (mode == EPI_GATED)
+        if (mode != EPI_LINEAR)
           ok = ok && encode(&maps.pre[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.epi.pre2, g.N, g.M, g.epi.ldp, 0, 32);
       }
     }
   }
   if (!ok) return cudaErrorInvalidValue;
-  return dtype == CONV_F16 ? launch_dense_tc_f16(t, mode, p, maps, s) : launch_dense_tc_bf16(t, mode, p, maps, s);
+  return dtype == CONV_F16 ? launch_dense_tc_f16(t, mode, g.a_mn, g.b_mn, p, maps, s)
+                           : launch_dense_tc_bf16(t, mode, g.a_mn, g.b_mn, p, maps, s);
 }
 
 cudaError_t dense_error_word(uint32_t* word, int reset) {

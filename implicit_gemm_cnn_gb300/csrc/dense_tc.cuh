@@ -1,7 +1,7 @@
 // dense_tc.cuh -- the dense products of 16-bit operands on the fifth-generation
 // tensor cores (tcgen05, accumulators in tensor memory, operands by TMA).
 //
-// A tile of D = A B^T is 128 * CG rows by NT columns (CG = 2: a pair of SMs, one
+// A tile of D = A B^T is 128 * CG rows by nt columns (CG = 2: a pair of SMs, one
 // cluster, works on one tile; each holds 128 rows of A and half of B, and one
 // cta_group::2 MMA per 16 terms multiplies both).  Persistent blocks walk over
 // the tiles:
@@ -28,13 +28,15 @@ namespace conv {
 
 struct DenseTcMaps {
   CUtensorMap a[2], b[2];
-  CUtensorMap y[2];    // outputs, boxes of 64 columns x 32 rows
-  CUtensorMap pre[2];  // float32 outputs (g, u or the activation's argument, or the ranges' planes): 32 x 32
+  CUtensorMap y[2];    // outputs, boxes of 32 columns x 32 rows
+  CUtensorMap pre[2];  // float32 g and u, the activation's argument, or the ranges' planes: 32 x 32
 };
 
 struct DenseTcArgs {
   int M, N;
-  int segs, batch, dual, a_mn, b_mn;
+  int nt;                   // MMA columns of a tile: a multiple of 32 (64 gated), at most the kernel's NT
+  int segs, batch;
+  int a_3d, b_3d;           // mn-major: all of a stage's 64-wide boxes in one copy
   int kb_seg;               // 64-term blocks of a segment
   int kb_total, kb_range;   // of the sum; of a k range
   int split;
@@ -49,20 +51,30 @@ namespace dtc {
 using namespace tcx;
 
 constexpr int kBK = 64;
-constexpr int kBufBytes = 4096;  // a 32-row staging tile of 128-byte rows
+constexpr int kBufBytes = 4096;  // a staging tile: 32 rows of 32 float32, or two of 32 16-bit values
 
-template <int CG, int NT>
+template <int CG, int NT, int MODE>
 struct Cfg {
   static constexpr int kEpiWarps = NT >= 256 ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
-  static constexpr int kBRows = NT / CG;
   static constexpr int kABytes = 128 * 128;
-  static constexpr int kStageBytes = kABytes + kBRows * 128;
-  static constexpr int kStaging = kEpiWarps * 2 * kBufBytes;
-  static constexpr int kStages = (232448 - 2048 - kStaging) / kStageBytes > 8 ? 8 : (232448 - 2048 - kStaging) / kStageBytes;
-  static constexpr int kSmem = kStages * kStageBytes + kStaging + 2048;  // 1024 to align, 1024 for barriers
-  static constexpr int kTmemCols = 2 * NT < 32 ? 32 : 2 * NT;
+  static constexpr int kStageBytes = kABytes + NT / CG * 128;
+  static constexpr int kWarpBufs = MODE == EPI_GATED_BWD ? 3 : 1;  // g, u and the outputs; or the outputs alone
+  static constexpr int kStaging = kEpiWarps * kWarpBufs * kBufBytes;
+  static constexpr int kFit = (232448 - 2048 - kStaging) / kStageBytes;
+  static constexpr int kStages = kFit > 8 ? 8 : kFit;
+  static constexpr int kSmem = kStages * kStageBytes + kStaging + 2032;  // 1024 to align, the rest for barriers
 };
+
+// A wait of a whole warp: one lane polls (32 polling lanes, of eight warps, take shared-memory cycles from the MMAs).
+__device__ __forceinline__ bool warp_wait(uint32_t* err, uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                          uint32_t code, bool ignore_abort = false, uint32_t sleep_ns = 0,
+                                          unsigned long long limit_ns = kWaitNs) {
+  int ok = 1;
+  if (threadIdx.x % 32 == 0) ok = wait_phase(err, bar, parity, abort_flag, code, ignore_abort, sleep_ns, limit_ns);
+  ok = __shfl_sync(0xffffffffu, ok, 0);
+  return ok != 0;
+}
 
 __device__ __forceinline__ uint32_t cluster_rank() {
   uint32_t r;
@@ -71,6 +83,13 @@ __device__ __forceinline__ uint32_t cluster_rank() {
 }
 __device__ __forceinline__ void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\nbarrier.cluster.wait.acquire.aligned;\n" ::: "memory");
+}
+// One lane of a converged warp.  (A branch on the lane's number would do, but not tell the compiler that one lane alone
+// is inside: it then guards every TMA and MMA instruction against several.)
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n .reg .pred e;\n elect.sync _|e, 0xffffffff;\n selp.u32 %0, 1, 0, e;\n}\n" : "=r"(p));
+  return p != 0;
 }
 // The shared-memory address of the same variable in block `rank` of the cluster.
 __device__ __forceinline__ uint32_t map_rank(uint32_t addr, uint32_t rank) {
@@ -94,6 +113,19 @@ __device__ __forceinline__ void load_2d(uint32_t dst, const void* map, int c0, i
         "l"(map), "r"(c0), "r"(c1), "r"(bar)
         : "memory");
 }
+template <int CG>
+__device__ __forceinline__ void load_3d(uint32_t dst, const void* map, int c0, int c1, int c2, uint32_t bar) {
+  if constexpr (CG == 2)
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2 [%0], [%1, {%2, "
+        "%3, %4}], [%5];\n" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+  else
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+        : "memory");
+}
 __device__ __forceinline__ void store_2d(const void* map, uint32_t src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(c0),
                "r"(c1), "r"(src)
@@ -104,28 +136,35 @@ __device__ __forceinline__ void store_3d(const void* map, uint32_t src, int c0, 
                "r"(c0), "r"(c1), "r"(c2), "r"(src)
                : "memory");
 }
-// One MMA, by one lane of the converged warp; and the arrival on `bar` (of
-// every block of the pair) when all MMAs issued so far are done.
-template <int CG>
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  if constexpr (CG == 2)
-    asm volatile(
-        "{\n .reg .pred p, e;\n elect.sync _|e, 0xffffffff;\n setp.ne.b32 p, %4, 0;\n"
-        " @e tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n}\n" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(acc)
-        : "memory");
-  else
-    mma_f16_elect(d, a, b, idesc, acc);
+// The MMAs of one 64-term stage, then the arrival on `bar` (of every block of the pair) when they are done.
+template <int CG, int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc, uint32_t bar) {
+#define CONV_MMA_STAGE(GROUP, COMMIT)                                                                    \
+  asm volatile(                                                                                          \
+      "{\n .reg .pred p, q;\n .reg .b64 a1, a2, a3, b1, b2, b3;\n .reg .b16 m;\n"                        \
+      " setp.ne.b32 p, %6, 0;\n setp.eq.b32 q, 0, 0;\n mov.b16 m, 3;\n"    \
+      " add.s64 a1, %1, %3;\n add.s64 b1, %2, %4;\n add.s64 a2, a1, %3;\n add.s64 b2, b1, %4;\n"         \
+      " add.s64 a3, a2, %3;\n add.s64 b3, b2, %4;\n"                                                     \
+      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], %1, %2, %5, p;\n"                            \
+      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], a1, b1, %5, q;\n"                            \
+      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], a2, b2, %5, q;\n"                            \
+      " tcgen05.mma.cta_group::" GROUP ".kind::f16 [%0], a3, b3, %5, q;\n"                            \
+      " tcgen05.commit.cta_group::" GROUP ".mbarrier::arrive::one.shared::cluster" COMMIT ";\n}\n" ::"r"(d), \
+      "l"(a), "l"(b), "n"(A_STEP), "n"(B_STEP), "r"(idesc), "r"(acc), "r"(bar)                           \
+      : "memory")
+  if constexpr (CG == 2) CONV_MMA_STAGE("2", ".multicast::cluster.b64 [%7], m");
+  else CONV_MMA_STAGE("1", ".b64 [%7]");
+#undef CONV_MMA_STAGE
 }
 template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar) {
   if constexpr (CG == 2)
     asm volatile(
-        "{\n .reg .pred e;\n .reg .b16 m;\n elect.sync _|e, 0xffffffff;\n mov.b16 m, 3;\n"
-        " @e tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(bar)
+        "{\n .reg .b16 m;\n mov.b16 m, 3;\n"
+        " tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], m;\n}\n" ::"r"(bar)
         : "memory");
   else
-    mma_commit_elect(bar);
+    mma_commit(bar);
 }
 template <int CG>
 __device__ __forceinline__ void alloc_tmem(uint32_t slot, uint32_t cols) {
@@ -179,32 +218,24 @@ __device__ __forceinline__ uint32_t pack_pair(float lo, float hi) {
     return *reinterpret_cast<const uint32_t*>(&h);
   }
 }
-// 32 consecutive 16-bit values as float32; `n` of them exist.
+// 32 consecutive 16-bit values, packed; `n` of them exist (n <= 0: none).
 template <typename T>
-__device__ __forceinline__ void load_row32(const T* p, bool vec, int n, float (&v)[32]) {
+__device__ __forceinline__ void load_row32(const T* p, bool vec, int n, uint32_t (&w)[16]) {
   if (vec && n >= 32) {
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint4 w = __ldg(reinterpret_cast<const uint4*>(p) + q);
-      const uint32_t r[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        v[q * 8 + 2 * i] = to_f32(*reinterpret_cast<const T*>(&r[i]));
-        v[q * 8 + 2 * i + 1] = to_f32(reinterpret_cast<const T*>(&r[i])[1]);
-      }
-    }
+    for (int q = 0; q < 4; ++q) *reinterpret_cast<uint4*>(w + 4 * q) = __ldg(reinterpret_cast<const uint4*>(p) + q);
   } else {
+    const uint16_t* h = reinterpret_cast<const uint16_t*>(p);
 #pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = i < n ? to_f32(p[i]) : 0.0f;
+    for (int i = 0; i < 16; ++i) w[i] = pack2(2 * i < n ? h[2 * i] : 0, 2 * i + 1 < n ? h[2 * i + 1] : 0);
   }
 }
-__device__ __forceinline__ void load_row32f(const float* p, bool vec, int n, float (&v)[32]) {
-  if (vec && n >= 32) {
+template <typename T>
+__device__ __forceinline__ void add_row32(float (&v)[32], const uint32_t (&w)[16]) {
 #pragma unroll
-    for (int q = 0; q < 8; ++q) *reinterpret_cast<float4*>(v + 4 * q) = __ldg(reinterpret_cast<const float4*>(p) + q);
-  } else {
-#pragma unroll
-    for (int i = 0; i < 32; ++i) v[i] = i < n ? p[i] : 0.0f;
+  for (int i = 0; i < 16; ++i) {
+    v[2 * i] += to_f32(*reinterpret_cast<const T*>(&w[i]));
+    v[2 * i + 1] += to_f32(reinterpret_cast<const T*>(&w[i])[1]);
   }
 }
 
@@ -228,11 +259,12 @@ __device__ __forceinline__ Tile tile_of(const DenseTcArgs& p, int u) {
   return t;
 }
 
-template <typename T, int CG, int NT, int MODE>
-__global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
+template <typename T, int CG, int NT, int MODE, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
     dense_tc(const __grid_constant__ DenseTcArgs p, const __grid_constant__ DenseTcMaps maps) {
-  using C = Cfg<CG, NT>;
-  constexpr int kOutCols = MODE == EPI_GATED ? NT / 2 : NT;  // output columns of a tile
+  using C = Cfg<CG, NT, MODE>;
+  const int nt = p.nt, out_cols = MODE == EPI_GATED ? nt / 2 : nt;  // a tile's columns of the output
+  const int b_rows = nt / CG;                                      // rows of B in this block
   extern __shared__ uint8_t smem_raw[];
   __shared__ volatile int abort_flag;
   __shared__ uint32_t tmem_slot;
@@ -244,7 +276,8 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
   auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
   auto acc_full = [&](int b) { return bars + 8u * (2 * C::kStages + b); };
   auto acc_empty = [&](int b) { return bars + 8u * (2 * C::kStages + 2 + b); };
-  const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
+  auto in_full = [&](int w) { return bars + 8u * (2 * C::kStages + 4 + w); };  // a warp's g and u
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
 
   if (warp == 0 && lane == 0) {
@@ -256,150 +289,171 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
       mbar_init(acc_full(b), 1);
       mbar_init(acc_empty(b), C::kEpiWarps * CG);
     }
+    if (MODE == EPI_GATED_BWD)
+      for (int w = 0; w < C::kEpiWarps; ++w) mbar_init(in_full(w), 1);
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     fence_proxy_async();
   }
-  if (warp == 1) alloc_tmem<CG>(smem_u32(&tmem_slot), C::kTmemCols);
+  if (warp == 1) alloc_tmem<CG>(smem_u32(&tmem_slot), 2 * NT);
   tc_fence_before();
   if constexpr (CG == 2) cluster_sync_all(); else __syncthreads();
   tc_fence_after();
-  const uint32_t tmem = tmem_slot;
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
+  // The two issuing loops are one thread's: every instruction of theirs counts (a stage's MMAs take 512 clocks at most).
+  // Operand orders are compiled in, addresses are carried from stage to stage.
   if (warp == 0) {
-    if (lane == 0) {
-      int it = 0;
+    if (elect_one()) {
+      // bytes of a stage, both blocks' together: whole boxes, past the matrices' ends too
+      const int b_boxes = (b_rows + 63) / 64;
+      const uint32_t stage_bytes = CG * (C::kABytes + (B_MN ? b_boxes * 8192 : b_rows * 128));
+      const uint32_t bar0 = CG == 2 ? map_rank(full(0), 0) : full(0);  // the first block's
+      const bool a_3d = A_MN && p.a_3d, b_3d = B_MN && p.b_3d;
+      int s = 0, left = 0;
+      uint32_t parity = 1;
       bool ok = true;
       for (int u = first; u < p.units && ok; u += step) {
         const Tile t = tile_of(p, u);
         const int kb0 = t.range * p.kb_range, kb1 = min(kb0 + p.kb_range, p.kb_total);
         const int m0 = t.m * (128 * CG) + static_cast<int>(rank) * 128;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % C::kStages;
-          if (!wait_phase(p.err, empty(s), ((it / C::kStages) & 1) ^ 1, &abort_flag, 1u)) { ok = false; break; }
-          const uint32_t bar = CG == 2 ? map_rank(full(s), 0) : full(s);
-          if (rank == 0) mbar_arrive_expect_tx(full(s), CG * C::kStageBytes);
+        const int n0 = MODE == EPI_GATED ? t.n * out_cols : t.n * nt + static_cast<int>(rank) * b_rows;
+        for (int kb = kb0; kb < kb1 && ok;) {
           const int seg = kb >= p.kb_seg ? 1 : 0;
-          const int k0 = (kb - seg * p.kb_seg) * kBK;
           const int op = p.segs > 1 ? seg : t.batch;
-          const uint32_t a = base + s * C::kStageBytes, b = a + C::kABytes;
-          if (p.a_mn) {
-            load_2d<CG>(a, &maps.a[op], m0, k0, bar);
-            load_2d<CG>(a + 8192, &maps.a[op], m0 + 64, k0, bar);
-          } else {
-            load_2d<CG>(a, &maps.a[op], k0, m0, bar);
-          }
-          if constexpr (MODE == EPI_GATED) {
-            if constexpr (CG == 2) {  // the first block's half of B is the gate's, the second's the up projection's
-              load_2d<CG>(b, &maps.b[rank], k0, t.n * kOutCols, bar);
-            } else {
-              load_2d<CG>(b, &maps.b[0], k0, t.n * kOutCols, bar);
-              load_2d<CG>(b + kOutCols * 128, &maps.b[1], k0, t.n * kOutCols, bar);
+          const CUtensorMap* am = &maps.a[op];
+          const CUtensorMap* bm = &maps.b[MODE == EPI_GATED && CG == 2 ? rank : op];
+          int k0 = (kb - seg * p.kb_seg) * kBK;
+          const int end = seg ? kb1 : min(kb1, p.kb_seg);
+          for (; kb < end; ++kb, k0 += kBK) {
+            if (!mbar_try_wait(empty(s), parity) && !wait_phase(p.err, empty(s), parity, &abort_flag, 1u)) {
+              ok = false;
+              break;
             }
-          } else {
-            const int n0 = t.n * NT + static_cast<int>(rank) * C::kBRows;
-            if (p.b_mn) {
-#pragma unroll
-              for (int i = 0; i < C::kBRows / 64; ++i) load_2d<CG>(b + i * 8192, &maps.b[op], n0 + 64 * i, k0, bar);
+            const uint32_t bar = bar0 + 8u * s;
+            if (rank == 0) mbar_arrive_expect_tx(bar0 + 8u * s, stage_bytes);
+            const uint32_t a = base + s * C::kStageBytes, b = a + C::kABytes;
+            if constexpr (A_MN) {
+              if (a_3d) load_3d<CG>(a, am, 0, k0, m0 / 64, bar);
+              else {
+                load_2d<CG>(a, am, m0, k0, bar);
+                load_2d<CG>(a + 8192, am, m0 + 64, k0, bar);
+              }
             } else {
-              load_2d<CG>(b, &maps.b[op], k0, n0, bar);
+              load_2d<CG>(a, am, k0, m0, bar);
             }
+            if constexpr (MODE == EPI_GATED) {
+              // of a pair, the first block's half of B is the gate's, the second's the up projection's
+              load_2d<CG>(b, bm, k0, n0, bar);
+              if constexpr (CG == 1) load_2d<CG>(b + out_cols * 128, &maps.b[1], k0, n0, bar);
+            } else if constexpr (B_MN) {
+              if (b_3d) load_3d<CG>(b, bm, 0, k0, n0 / 64, bar);
+              else
+                for (int i = 0; i < b_boxes; ++i) load_2d<CG>(b + i * 8192, bm, n0 + 64 * i, k0, bar);
+            } else {
+              load_2d<CG>(b, bm, k0, n0, bar);
+            }
+            if (++s == C::kStages) { s = 0; parity ^= 1; }
           }
         }
       }
       // every stage handed out has been released (no arrival is under way when the block ends)
-      for (int i = 0; i < C::kStages && ok; ++i, ++it)
-        ok = wait_phase(p.err, empty(it % C::kStages), ((it / C::kStages) & 1) ^ 1, &abort_flag, 1u);
+      for (left = C::kStages; left > 0 && ok; --left) {
+        ok = wait_phase(p.err, empty(s), parity, &abort_flag, 1u);
+        if (++s == C::kStages) { s = 0; parity ^= 1; }
+      }
       if (!ok)  // copies in flight end within microseconds; the block does not return before
         for (int i = 0; i < 1000; ++i) __nanosleep(10000);
     }
   } else if (warp == 1) {
-    if (rank == 0) {
+    if (rank == 0 && elect_one()) {
       // D float32, A and B of type T, transposes, N / 8, M / 16
       const uint32_t kind = std::is_same<T, __nv_bfloat16>::value ? 1u : 0u;
-      const uint32_t idesc = (1u << 4) | (kind << 7) | (kind << 10) | (static_cast<uint32_t>(p.a_mn) << 15) |
-                             (static_cast<uint32_t>(p.b_mn) << 16) | (static_cast<uint32_t>(NT >> 3) << 17) |
+      const uint32_t idesc = (1u << 4) | (kind << 7) | (kind << 10) | (static_cast<uint32_t>(A_MN) << 15) |
+                             (static_cast<uint32_t>(B_MN) << 16) | (static_cast<uint32_t>(nt >> 3) << 17) |
                              (static_cast<uint32_t>(128 * CG >> 4) << 24);
       // 128-byte swizzle.  k-major: 8-row groups 1024 bytes apart, 16 terms are 32 bytes of a row.  mn-major: 64-wide
       // blocks 8192 bytes apart (the leading offset), groups of 8 terms 1024 apart, 16 terms are 2048 bytes.
-      const uint32_t a_step = p.a_mn ? 2048 >> 4 : 32 >> 4, b_step = p.b_mn ? 2048 >> 4 : 32 >> 4;
-      const uint64_t a_hi = smem_desc(0, p.a_mn ? 8192 : 16, 1024, 2), b_hi = smem_desc(0, p.b_mn ? 8192 : 16, 1024, 2);
-      int it = 0, tile_it = 0;
+      constexpr int kAStep = A_MN ? 2048 >> 4 : 32 >> 4, kBStep = B_MN ? 2048 >> 4 : 32 >> 4;
+      const uint64_t a0 = smem_desc(base, A_MN ? 8192 : 16, 1024, 2);
+      const uint64_t b0 = smem_desc(base + C::kABytes, B_MN ? 8192 : 16, 1024, 2);
+      int s = 0, tile_it = 0;
+      uint32_t parity = 0;
       bool ok = true;
       for (int u = first; u < p.units && ok; u += step, ++tile_it) {
-        const int range = u / p.tiles;
-        const int kb0 = range * p.kb_range, kb1 = min(kb0 + p.kb_range, p.kb_total);
+        const int kb0 = u / p.tiles * p.kb_range, kbs = min(p.kb_range, p.kb_total - kb0);
         const int buf = tile_it & 1;
         if (!wait_phase(p.err, acc_empty(buf), ((tile_it >> 1) & 1) ^ 1, &abort_flag, 2u)) break;
-        __syncwarp();
         tc_fence_after();
         const uint32_t d = tmem + buf * NT;
-        for (int kb = kb0; kb < kb1; ++kb, ++it) {
-          const int s = it % C::kStages;
-          if (!wait_phase(p.err, full(s), (it / C::kStages) & 1, &abort_flag, 4u)) { ok = false; break; }
-          __syncwarp();
+        for (int kb = 0; kb < kbs; ++kb) {
+          if (!mbar_try_wait(full(s), parity) && !wait_phase(p.err, full(s), parity, &abort_flag, 4u)) {
+            ok = false;
+            break;
+          }
           tc_fence_after();
-          const uint32_t a = base + s * C::kStageBytes, b = a + C::kABytes;
-          const uint64_t ad = a_hi | (a >> 4), bd = b_hi | (b >> 4);
-#pragma unroll
-          for (int k = 0; k < kBK / 16; ++k)
-            mma<CG>(d, ad + k * a_step, bd + k * b_step, idesc, kb > kb0 || k > 0);
-          commit<CG>(empty(s));
+          const uint64_t off = static_cast<uint64_t>(s) * (C::kStageBytes >> 4);
+          mma_stage<CG, kAStep, kBStep>(d, a0 + off, b0 + off, idesc, kb, empty(s));
+          if (++s == C::kStages) { s = 0; parity ^= 1; }
         }
         if (ok) commit<CG>(acc_full(buf));
       }
       if (abort_flag)
         for (int i = 0; i < 1000; ++i) __nanosleep(10000);
-      __syncwarp();
     }
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     constexpr int kParts = C::kEpiWarps / 4;       // warps that share a quarter's columns
-    constexpr int kCols = kOutCols / kParts;       // output columns of this warp
-    static_assert(kCols % 64 == 0, "whole staging tiles");
-    const uint32_t mine = staging + (warp - 2) * 2 * kBufBytes;
+    const uint32_t mine = staging + (warp - 2) * C::kWarpBufs * kBufBytes;
     const DenseEpi& e = p.epi;
-    int ring = 0;
-    // the next staging tile, free of its last store
-    auto acquire = [&]() {
-      if (lane == 0) bulk_wait_read<1>();
+    // The outputs' staging tile: one float32 piece, or two 16-bit ones in turn.  A piece waits until the stores that
+    // read its place have done so: the last but one's if both are 16-bit, else the last one's.
+    const uint32_t out_buf = mine + (C::kWarpBufs - 1) * kBufBytes;
+    int turn = 0;
+    bool last_wide = true;
+    auto acquire = [&](bool wide) {
+      if (lane == 0) {
+        if (wide || last_wide) bulk_wait_read<0>();
+        else bulk_wait_read<1>();
+      }
+      last_wide = wide;
       __syncwarp();
-      const uint32_t b = mine + (ring & 1) * kBufBytes;
-      ++ring;
-      return b;
+      turn ^= wide ? 0 : 1;
+      return wide ? out_buf : out_buf + turn * (kBufBytes / 2);
     };
     auto publish = [&]() {
       fence_proxy_async();
       __syncwarp();
     };
-    // 64 16-bit columns (32 words) of this lane's row
-    auto put16 = [&](const uint32_t (&w)[32], const CUtensorMap* map, T* y, int n, int m_warp) {
-      if (p.tma_y) {
-        const uint32_t b = acquire();
+    // 32 16-bit columns of this lane's row into a staging tile of 64-byte rows (64-byte swizzle)
+    auto stage16 = [&](uint32_t b, const uint32_t (&w)[16]) {
 #pragma unroll
-        for (int q = 0; q < 8; ++q)
-          sts_v4(b + lane * 128 + ((q ^ (lane & 7)) << 4), make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
-        publish();
-        if (lane == 0) {
-          store_2d(map, b, n, m_warp);
-          bulk_commit();
-        }
-      } else if (m_warp + lane < p.M) {
-        T* row = y + static_cast<long long>(m_warp + lane) * e.ldy + n;
+      for (int q = 0; q < 4; ++q)
+        sts_v4(b + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
+    };
+    auto plain16 = [&](const uint32_t (&w)[16], T* y, int n, int m_warp) {
+      if (m_warp + lane < p.M) {
+        uint16_t* row = reinterpret_cast<uint16_t*>(y + static_cast<long long>(m_warp + lane) * e.ldy + n);
 #pragma unroll
-        for (int j = 0; j < 64; ++j)
-          if (n + j < p.N) {
-            const uint16_t v = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
-            row[j] = *reinterpret_cast<const T*>(&v);
-          }
+        for (int j = 0; j < 32; ++j)
+          if (n + j < p.N) row[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+      }
+    };
+    auto put16 = [&](const uint32_t (&w)[16], const CUtensorMap* map, T* y, int n, int m_warp) {
+      if (!p.tma_y) return plain16(w, y, n, m_warp);
+      const uint32_t b = acquire(false);
+      stage16(b, w);
+      publish();
+      if (lane == 0) {
+        store_2d(map, b, n, m_warp);
+        bulk_commit();
       }
     };
     // 32 float32 columns of this lane's row (plane >= 0: of the ranges' planes)
     auto put32 = [&](const float (&v)[32], const CUtensorMap* map, float* out, long long ld, int n, int m_warp, int plane) {
-      if (n >= p.N) return;
       if (p.tma_pre) {
-        const uint32_t b = acquire();
+        const uint32_t b = acquire(true);
 #pragma unroll
         for (int q = 0; q < 8; ++q)
           sts_v4(b + lane * 128 + ((q ^ (lane & 7)) << 4),
@@ -419,116 +473,123 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
           if (n + j < p.N) row[j] = v[j];
       }
     };
-    const bool vec_r = e.residual && e.ldr % 8 == 0 && reinterpret_cast<uintptr_t>(e.residual) % 16 == 0;
+    const bool vec_r = e.ldr % 8 == 0 && reinterpret_cast<uintptr_t>(e.residual) % 16 == 0;
     const bool vec_b = reinterpret_cast<uintptr_t>(e.bias) % 16 == 0;
-    const bool vec_p = e.ldp % 4 == 0 && reinterpret_cast<uintptr_t>(e.pre) % 16 == 0 &&
-                       reinterpret_cast<uintptr_t>(e.pre2) % 16 == 0;
-    int tile_it = 0;
+    const int chunks = out_cols / 32, per_warp = (chunks + kParts - 1) / kParts;
+    const int c0 = half * per_warp, c1 = min(c0 + per_warp, chunks);
+    int tile_it = 0, fetched = 0;
     for (int u = first; u < p.units; u += step, ++tile_it) {
       const Tile t = tile_of(p, u);
       const int buf = tile_it & 1;
-      if (!wait_phase(p.err, acc_full(buf), (tile_it >> 1) & 1, &abort_flag, 8u, false, 64,
-                      kWaitNs + 1000ull * p.kb_range))  // a stage takes below a microsecond
+      const int m_warp = t.m * (128 * CG) + static_cast<int>(rank) * 128 + quarter * 32;
+      const int m = m_warp + lane, n_tile = t.n * out_cols;
+      // pieces that exist: this warp's rows, and columns below N
+      const int c_end = m_warp < p.M ? min(c1, (p.N - n_tile + 31) / 32) : c0;
+      // g and u of a piece, loaded while the one before is worked on
+      auto fetch = [&](int c) {
+        if (lane == 0) {
+          mbar_arrive_expect_tx(in_full(warp - 2), 2 * kBufBytes);
+          load_2d<1>(mine, &maps.pre[0], n_tile + 32 * c, m_warp, in_full(warp - 2));
+          load_2d<1>(mine + kBufBytes, &maps.pre[1], n_tile + 32 * c, m_warp, in_full(warp - 2));
+        }
+      };
+      if (MODE == EPI_GATED_BWD && c0 < c_end) fetch(c0);
+      uint32_t res[16];
+      const T* res_row = static_cast<const T*>(e.residual) + static_cast<long long>(m) * e.ldr + n_tile;
+      auto fetch_residual = [&](int c) {
+        load_row32(res_row + 32 * c, vec_r, m < p.M && c < c_end ? p.N - n_tile - 32 * c : 0, res);
+      };
+      if (MODE == EPI_LINEAR && e.residual) fetch_residual(c0);
+      if (!warp_wait(p.err, acc_full(buf), (tile_it >> 1) & 1, &abort_flag, 8u, false, 128,
+                      kWaitNs + 1000ull * p.kb_range)) {  // a stage takes below a microsecond
+        if (MODE == EPI_GATED_BWD && c0 < c_end)  // the copies under way land before the block ends
+          warp_wait(p.err, in_full(warp - 2), fetched & 1, &abort_flag, 16u, true);
         break;
+      }
+      __syncwarp();
       tc_fence_after();
       const uint32_t acc = tmem + buf * NT + (static_cast<uint32_t>(quarter * 32) << 16);
-      const int m_warp = t.m * (128 * CG) + static_cast<int>(rank) * 128 + quarter * 32;
-      const int m = m_warp + lane;
-      const int col0 = half * kCols;
 #pragma unroll 1
-      for (int c = 0; c < kCols; c += 64) {
-        const int n = t.n * kOutCols + col0 + c;
-        const bool dead = n >= p.N || m_warp >= p.M;  // nothing of this piece exists
-        uint32_t w0[32], w1[32];
-#pragma unroll
-        for (int sub = 0; sub < 2; ++sub) {
-          float v[32];
-          tmem_ld32(acc + col0 + c + sub * 32, v);
-          const int ns = n + sub * 32, left = p.N - ns;  // columns that exist
-          const bool row_ok = m < p.M && left > 0;
-          if constexpr (MODE == EPI_PARTIAL) {
-            tmem_arrived(v);
-            if (!dead) put32(v, &maps.pre[0], p.part, p.N, ns, m_warp, t.range * (p.dual ? 2 : p.batch) + t.batch);
-          } else if constexpr (MODE == EPI_GATED) {
-            float g[32];
-            tmem_ld32(acc + NT / 2 + col0 + c + sub * 32, g);
-            tmem_arrived(v);
-            tmem_arrived(g);
-            if (dead) continue;
-            if (e.pre) {
-              put32(v, &maps.pre[0], e.pre, e.ldp, ns, m_warp, -1);
-              put32(g, &maps.pre[1], e.pre2, e.ldp, ns, m_warp, -1);
-            }
-            dense_activate<true, 32>(v, e.act, e.alpha, e.beta);
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w0[sub * 16 + i] = pack_pair<T>(v[2 * i] * g[2 * i], v[2 * i + 1] * g[2 * i + 1]);
-          } else if constexpr (MODE == EPI_GATED_BWD) {
-            float g[32], gr[32], uu[32];
-            const long long at = static_cast<long long>(m) * e.ldp + ns;
-            if (row_ok) {
-              load_row32f(e.pre + at, vec_p, left, g);
-              load_row32f(e.pre2 + at, vec_p, left, uu);
-            } else {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) g[i] = uu[i] = 0.0f;
-            }
-            dense_activate_grad<true, 32>(g, gr, e.act, e.alpha, e.beta);
-            tmem_arrived(v);
-            if (dead) continue;
-#pragma unroll
-            for (int i = 0; i < 16; ++i) {
-              w0[sub * 16 + i] = pack_pair<T>(v[2 * i] * uu[2 * i] * gr[2 * i], v[2 * i + 1] * uu[2 * i + 1] * gr[2 * i + 1]);
-              w1[sub * 16 + i] = pack_pair<T>(v[2 * i] * g[2 * i], v[2 * i + 1] * g[2 * i + 1]);
-            }
-          } else {
-            float r[32];
-            if (e.residual) {
-              if (row_ok) load_row32(static_cast<const T*>(e.residual) + static_cast<long long>(m) * e.ldr + ns, vec_r, left, r);
-              else {
-#pragma unroll
-                for (int i = 0; i < 32; ++i) r[i] = 0.0f;
-              }
-            }
-            tmem_arrived(v);
-            if (dead) continue;
-            if (e.bias) {
-              float bv[32];
-              load_row32(static_cast<const T*>(e.bias) + ns, vec_b, left, bv);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] += bv[i];
-            }
-            if (e.residual && !e.residual_last) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] += r[i];
-            }
-            if (e.pre) put32(v, &maps.pre[0], e.pre, e.ldp, ns, m_warp, -1);
-            dense_activate<true, 32>(v, e.act, e.alpha, e.beta);
-            if (e.residual && e.residual_last) {
-#pragma unroll
-              for (int i = 0; i < 32; ++i) v[i] += r[i];
-            }
-#pragma unroll
-            for (int i = 0; i < 16; ++i) w0[sub * 16 + i] = pack_pair<T>(v[2 * i], v[2 * i + 1]);
+      for (int c = c0; c < c_end; ++c) {
+        const int n = n_tile + 32 * c, left = p.N - n;
+        float v[32];
+        uint32_t w[16];
+        tmem_ld32(acc + 32 * c, v);
+        if constexpr (MODE == EPI_PARTIAL) {
+          tmem_arrived(v);
+          put32(v, &maps.pre[0], p.part, p.N, n, m_warp, t.range * p.batch + t.batch);
+        } else if constexpr (MODE == EPI_GATED) {
+          float g[32];
+          tmem_ld32(acc + nt / 2 + 32 * c, g);
+          tmem_arrived(v);
+          tmem_arrived(g);
+          if (e.pre) {
+            put32(v, &maps.pre[0], e.pre, e.ldp, n, m_warp, -1);
+            put32(g, &maps.pre[1], e.pre2, e.ldp, n, m_warp, -1);
           }
-        }
-        if (c + 64 >= kCols) {  // the accumulator has been read: the next but one tile may have it
-          tc_fence_before();
+          dense_activate<true, 32>(v, e.act, e.alpha, e.beta);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = pack_pair<T>(v[2 * i] * g[2 * i], v[2 * i + 1] * g[2 * i + 1]);
+          put16(w, &maps.y[0], static_cast<T*>(e.y), n, m_warp);
+        } else if constexpr (MODE == EPI_GATED_BWD) {
+          float g[32], slope[32];
+          if (!warp_wait(p.err, in_full(warp - 2), fetched & 1, &abort_flag, 16u, true)) break;
+          ++fetched;
           __syncwarp();
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 f = *reinterpret_cast<const float4*>(__cvta_shared_to_generic(mine + lane * 128 + ((q ^ (lane & 7)) << 4)));
+            g[4 * q] = f.x; g[4 * q + 1] = f.y; g[4 * q + 2] = f.z; g[4 * q + 3] = f.w;
+          }
+          dense_activate_grad<true, 32>(g, slope, e.act, e.alpha, e.beta);
+          tmem_arrived(v);
+          uint32_t w2[16];
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float4 f = *reinterpret_cast<const float4*>(
+                __cvta_shared_to_generic(mine + kBufBytes + lane * 128 + ((q ^ (lane & 7)) << 4)));
+            w[2 * q] = pack_pair<T>(v[4 * q] * f.x * slope[4 * q], v[4 * q + 1] * f.y * slope[4 * q + 1]);
+            w[2 * q + 1] = pack_pair<T>(v[4 * q + 2] * f.z * slope[4 * q + 2], v[4 * q + 3] * f.w * slope[4 * q + 3]);
+            w2[2 * q] = pack_pair<T>(v[4 * q] * g[4 * q], v[4 * q + 1] * g[4 * q + 1]);
+            w2[2 * q + 1] = pack_pair<T>(v[4 * q + 2] * g[4 * q + 2], v[4 * q + 3] * g[4 * q + 3]);
+          }
+          __syncwarp();  // g and u have been read
+          if (c + 1 < c_end) fetch(c + 1);
+          const uint32_t b = acquire(true);
+          stage16(b, w);
+          stage16(b + kBufBytes / 2, w2);
+          publish();
           if (lane == 0) {
-            if constexpr (CG == 2) mbar_arrive_cluster(map_rank(acc_empty(buf), 0));
-            else mbar_arrive(acc_empty(buf));
+            store_2d(&maps.y[0], b, n, m_warp);
+            store_2d(&maps.y[1], b + kBufBytes / 2, n, m_warp);
+            bulk_commit();
           }
-        }
-        if constexpr (MODE != EPI_PARTIAL) {
-          if (!dead) {
-            if constexpr (MODE == EPI_GATED_BWD) {
-              put16(w0, &maps.y[0], static_cast<T*>(e.y), n, m_warp);
-              put16(w1, &maps.y[1], static_cast<T*>(e.y2), n, m_warp);
-            } else {
-              put16(w0, &maps.y[t.batch], static_cast<T*>(t.batch ? e.y2 : e.y), n, m_warp);
-            }
+        } else {
+          uint32_t bias[16];
+          if (e.bias) load_row32(static_cast<const T*>(e.bias) + n, vec_b, left, bias);
+          tmem_arrived(v);
+          if (e.bias) add_row32<T>(v, bias);
+          if (e.residual && !e.residual_last) {
+            add_row32<T>(v, res);
+            fetch_residual(c + 1);
           }
+          if (e.pre) put32(v, &maps.pre[0], e.pre, e.ldp, n, m_warp, -1);
+          dense_activate<true, 32>(v, e.act, e.alpha, e.beta);
+          if (e.residual && e.residual_last) {
+            add_row32<T>(v, res);
+            fetch_residual(c + 1);
+          }
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = pack_pair<T>(v[2 * i], v[2 * i + 1]);
+          put16(w, &maps.y[t.batch], static_cast<T*>(t.batch ? e.y2 : e.y), n, m_warp);
         }
+      }
+      // the accumulator has been read: the next but one tile may have it
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) {
+        if constexpr (CG == 2) mbar_arrive_cluster(map_rank(acc_empty(buf), 0));
+        else mbar_arrive(acc_empty(buf));
       }
     }
     if (lane == 0) bulk_wait_all();
@@ -540,7 +601,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
   if constexpr (CG == 2) cluster_sync_all(); else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    free_tmem<CG>(tmem, C::kTmemCols);
+    free_tmem<CG>(tmem, 2 * NT);
   }
 }
 
