@@ -83,7 +83,7 @@ conv_status validate(const conv_gated_problem* p, GatedShape* s) {
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
 
 // ---- one product: which kernel, and its scratch ------------------------------
-enum Variant { V_FFMA = 0, V_TC = 1 };
+enum Variant { V_FFMA = 0, V_TC = 1, V_FEW = 2 };
 struct Product {
   Variant variant;
   DenseFfmaPlan ffma;
@@ -94,10 +94,12 @@ struct Product {
 };
 
 // `g` without addresses.  `tc`: 16-bit operands with rows a tensor-core copy can take.
-Product plan_product(const DenseGemm& g, bool tc, uint32_t flags, int sm) {
-  (void)flags;
+Product plan_product(const DenseGemm& g, bool tc, bool few, int sm) {
   Product r = {};
-  if (tc) {
+  if (few) {
+    r.variant = V_FEW;
+    r.split = 1;
+  } else if (tc) {
     r.variant = V_TC;
     r.tc = dense_tc_plan(g, sm);
     r.split = r.tc.split;
@@ -111,7 +113,9 @@ Product plan_product(const DenseGemm& g, bool tc, uint32_t flags, int sm) {
   return r;
 }
 
-cudaError_t launch_product(const Product& r, DenseGemm g, int dtype, void* part, cudaStream_t s) {
+// `follows`: the kernel before in the stream is this call's own.
+cudaError_t launch_product(const Product& r, DenseGemm g, int dtype, void* part, bool follows, cudaStream_t s) {
+  if (r.variant == V_FEW) return launch_dense_few(g, dtype, follows, s);
   g.split = r.split;
   g.part = static_cast<float*>(part);
   cudaError_t err;
@@ -127,7 +131,9 @@ cudaError_t launch_product(const Product& r, DenseGemm g, int dtype, void* part,
 
 void describe_product(const Product& r, const DenseGemm& g, int sm, char* buf, size_t len) {
   const long long k = static_cast<long long>(g.segs) * g.K;
-  if (r.variant == V_TC)
+  if (r.variant == V_FEW)
+    snprintf(buf, len, "few_rows tile=%dx16 split=1 products=%d sums over %lld sms=%d launches=1", g.M, dense_products(g), k, sm);
+  else if (r.variant == V_TC)
     snprintf(buf, len, "tcgen05 tile=%dx%d sms_per_tile=%d tiles=%lld split=%d products=%d sums over %lld sms=%d launches=%d",
              128 * r.tc.cg, r.tc.nt, r.tc.cg, r.tc.tiles, r.split, dense_products(g), k, sm, r.launches);
   else
@@ -185,13 +191,17 @@ DenseGemm make_gemm(long long m, long long n, long long k, int a_mn, int b_mn, l
 struct Mode {
   bool copies;   // every 16-bit operand is copied
   bool tc;       // the tensor-core kernels may run
+  bool few;      // the kernel for few rows may run (it takes any alignment)
 };
 Mode mode_of(uint32_t flags, int dtype) {
   Mode m;
   m.tc = dtype != CONV_F32 && !(flags & CONV_LINEAR_FLAG_FORCE_FFMA);
   m.copies = m.tc && (flags & CONV_LINEAR_FLAG_UNALIGNED);
+  m.few = !(flags & (CONV_LINEAR_FLAG_FORCE_FFMA | CONV_LINEAR_FLAG_NO_FEW_ROWS));
   return m;
 }
+
+bool few_rows(long long rows, int dtype) { return rows >= 1 && rows <= dense_few_rows(dtype); }
 
 struct LinearPlan {
   Copy x, w, dy;
@@ -206,7 +216,8 @@ struct LinearPlan {
 LinearPlan plan_linear(const conv_linear_problem* p, const LinearShape& sh, const Mode& mode, int sm) {
   LinearPlan r = {};
   Layout l;
-  const int dt = mode.tc ? p->dtype : CONV_F32;  // what copies go by
+  const bool few = mode.few && few_rows(p->rows, p->dtype);
+  const int dt = mode.tc && !few ? p->dtype : CONV_F32;  // what copies go by
   r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
   r.w = l.copy(dt, mode.copies, p->c_out, p->c_in, sh.ldw);
   r.fwd = make_gemm(p->rows, p->c_out, p->c_in, 0, 0, r.x.ld, r.w.ld);
@@ -214,7 +225,7 @@ LinearPlan plan_linear(const conv_linear_problem* p, const LinearShape& sh, cons
   e.act = p->act; e.alpha = p->act_alpha; e.beta = p->act_beta;
   e.residual_last = (p->flags & CONV_LINEAR_FLAG_RESIDUAL_LAST) != 0;
   e.ldr = sh.ldr; e.ldy = sh.ldy; e.ldp = p->c_out;
-  if (p->rows > 0) r.pfwd = plan_product(r.fwd, mode.tc, p->flags, sm);
+  if (p->rows > 0) r.pfwd = plan_product(r.fwd, mode.tc, few, sm);
   r.part_off = l.take(r.pfwd.part_bytes);
   r.total = l.total;
   return r;
@@ -239,10 +250,10 @@ LinearPlan plan_linear_backward(const conv_linear_problem* p, const LinearShape&
     r.col_off = l.take(static_cast<size_t>(r.col_blocks) * p->c_out * sizeof(float));
     r.dx = make_gemm(p->rows, p->c_in, p->c_out, 0, 1, r.ldz, r.w.ld);
     r.dx.epi.ldy = p->c_in;
-    r.pdx = plan_product(r.dx, mode.tc, p->flags, sm);
+    r.pdx = plan_product(r.dx, mode.tc, false, sm);
     r.dw = make_gemm(p->c_out, p->c_in, p->rows, 1, 1, r.ldz, r.x.ld);
     r.dw.epi.ldy = p->c_in;
-    r.pdw = plan_product(r.dw, mode.tc, p->flags, sm);
+    r.pdw = plan_product(r.dw, mode.tc, false, sm);
   }
   r.part_off = l.take(std::max(r.pdx.part_bytes, r.pdw.part_bytes));
   r.total = l.total;
@@ -285,7 +296,7 @@ auto plan_for(uint32_t flags, int dtype, std::initializer_list<const void*> oper
     m.copies = true;
     auto r = plan(m);
     if (r.total <= have) return r;
-    m.copies = m.tc = false;
+    m.copies = m.tc = false;  // (the kernel for few rows stays)
   }
   return plan(m);
 }
@@ -320,7 +331,8 @@ GatedSaved gated_saved(const conv_gated_problem* p, const GatedShape& sh) {
 GatedPlan plan_gated(const conv_gated_problem* p, const GatedShape& sh, const Mode& mode, int sm, bool saved) {
   GatedPlan r = {};
   Layout l;
-  const int dt = mode.tc ? p->dtype : CONV_F32;
+  const bool few = mode.few && few_rows(p->rows, p->dtype);
+  const int dt = mode.tc && !few ? p->dtype : CONV_F32;
   r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
   r.wg = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
   r.wu = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
@@ -332,10 +344,10 @@ GatedPlan plan_gated(const conv_gated_problem* p, const GatedShape& sh, const Mo
     r.up.epi.mode = EPI_GATED;
     r.up.epi.act = p->act; r.up.epi.alpha = p->act_alpha; r.up.epi.beta = p->act_beta;
     r.up.epi.ldy = sh.ldh; r.up.epi.ldp = sh.ldh;
-    r.pup = plan_product(r.up, mode.tc, p->flags, sm);
+    r.pup = plan_product(r.up, mode.tc, few, sm);
     r.down = make_gemm(p->rows, p->c_out, p->hidden, 0, 0, sh.ldh, r.wd.ld);
     r.down.epi.ldr = sh.ldr; r.down.epi.ldy = sh.ldy;
-    r.pdown = plan_product(r.down, mode.tc, p->flags, sm);
+    r.pdown = plan_product(r.down, mode.tc, few, sm);
   }
   r.part_off = l.take(std::max(r.pup.part_bytes, r.pdown.part_bytes));
   r.total = l.total;
@@ -359,18 +371,18 @@ GatedPlan plan_gated_backward(const conv_gated_problem* p, const GatedShape& sh,
     r.dh.epi.mode = EPI_GATED_BWD;
     r.dh.epi.act = p->act; r.dh.epi.alpha = p->act_alpha; r.dh.epi.beta = p->act_beta;
     r.dh.epi.ldy = sh.ldh; r.dh.epi.ldp = sh.ldh;
-    r.pdh = plan_product(r.dh, mode.tc, p->flags, sm);
+    r.pdh = plan_product(r.dh, mode.tc, false, sm);
     r.dx = make_gemm(p->rows, p->c_in, p->hidden, 0, 1, sh.ldh, r.wg.ld);
     r.dx.segs = 2;
     r.dx.epi.ldy = p->c_in;
-    r.pdx = plan_product(r.dx, mode.tc, p->flags, sm);
+    r.pdx = plan_product(r.dx, mode.tc, false, sm);
     r.dwgu = make_gemm(p->hidden, p->c_in, p->rows, 1, 1, sh.ldh, r.x.ld);
     r.dwgu.batch = 2;
     r.dwgu.epi.ldy = p->c_in;
-    r.pdwgu = plan_product(r.dwgu, mode.tc, p->flags, sm);
+    r.pdwgu = plan_product(r.dwgu, mode.tc, false, sm);
     r.dwd = make_gemm(p->c_out, p->hidden, p->rows, 1, 1, r.dy.ld, sh.ldh);
     r.dwd.epi.ldy = p->hidden;
-    r.pdwd = plan_product(r.dwd, mode.tc, p->flags, sm);
+    r.pdwd = plan_product(r.dwd, mode.tc, false, sm);
   }
   r.part_off = l.take(std::max({r.pdh.part_bytes, r.pdx.part_bytes, r.pdwgu.part_bytes, r.pdwd.part_bytes}));
   r.total = l.total;
@@ -380,29 +392,32 @@ GatedPlan plan_gated_backward(const conv_gated_problem* p, const GatedShape& sh,
 // The pointer checks of conv_clip_grads.
 conv_status clip_check(int64_t count, const void* const* in, void* const* out, const int64_t* sizes,
                        const int32_t* dtypes, const float* norm, const void* scratch, size_t have, size_t need) {
-  // ranges sorted by address: an output touches no other range but its own input's, exactly
-  struct R { uintptr_t lo, hi; int64_t tensor; bool out; };
-  std::vector<R> ranges;
-  ranges.reserve(static_cast<size_t>(count) * 2 + 2);
+  // ranges by address: an output touches no other range but its own input's, exactly
+  struct R { uintptr_t lo, hi; bool out; };
+  auto below = [](const R& a, const R& b) { return a.lo < b.lo; };
+  std::vector<R> ins, outs, ranges;
+  ins.reserve(static_cast<size_t>(count));
+  outs.reserve(static_cast<size_t>(count) + 2);
   for (int64_t i = 0; i < count; ++i) {
     if (dtypes[i] < CONV_F32 || dtypes[i] > CONV_BF16) return CONV_ERR_DTYPE;
     if (sizes[i] == 0) continue;
     const size_t es = elem_size(dtypes[i]), n = static_cast<size_t>(sizes[i]) * es;
-    const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]);
-    if (!a || (out && !out[i])) return CONV_ERR_NULL;
-    if (a % es) return CONV_ERR_ARG;
-    ranges.push_back({a, a + n, i, false});
-    if (out) {
-      const uintptr_t b = reinterpret_cast<uintptr_t>(out[i]);
-      if (b % es) return CONV_ERR_ARG;
-      if (b != a) ranges.push_back({b, b + n, i, true});
-      else ranges.back().out = true;
-    }
+    const uintptr_t a = reinterpret_cast<uintptr_t>(in[i]), b = out ? reinterpret_cast<uintptr_t>(out[i]) : 0;
+    if (!a || (out && !b)) return CONV_ERR_NULL;
+    if (a % es || b % es) return CONV_ERR_ARG;
+    if (a != b) ins.push_back({a, a + n, false});
+    if (b) outs.push_back({b, b + n, true});
   }
   if (scratch_bad(scratch, have, need)) return CONV_ERR_SCRATCH;
-  ranges.push_back({reinterpret_cast<uintptr_t>(scratch), reinterpret_cast<uintptr_t>(scratch) + need, -1, true});
-  ranges.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, -2, true});
-  std::sort(ranges.begin(), ranges.end(), [](const R& a, const R& b) { return a.lo < b.lo; });
+  // (buffers mostly come in order already)
+  if (!std::is_sorted(ins.begin(), ins.end(), below)) std::sort(ins.begin(), ins.end(), below);
+  outs.push_back({reinterpret_cast<uintptr_t>(scratch), reinterpret_cast<uintptr_t>(scratch) + need, true});
+  outs.push_back({reinterpret_cast<uintptr_t>(norm), reinterpret_cast<uintptr_t>(norm) + 4, true});
+  std::sort(outs.end() - 2, outs.end(), below);
+  if (!std::is_sorted(outs.begin(), outs.end() - 2, below)) std::sort(outs.begin(), outs.end() - 2, below);
+  std::inplace_merge(outs.begin(), outs.end() - 2, outs.end(), below);
+  ranges.resize(ins.size() + outs.size());
+  std::merge(ins.begin(), ins.end(), outs.begin(), outs.end(), ranges.begin(), below);
   // the furthest end so far of any range, and of the written ones
   uintptr_t end = 0, end_out = 0;
   for (const R& r : ranges) {
@@ -493,7 +508,7 @@ conv_status conv_linear_forward(const conv_linear_problem* p, const void* x, con
   g.epi.residual = p->has_residual ? residual : nullptr;
   g.epi.y = y;
   g.epi.pre = pre;
-  CONV_TRY(launch_product(r.pfwd, g, p->dtype, base + r.part_off, s));
+  CONV_TRY(launch_product(r.pfwd, g, p->dtype, base + r.part_off, false, s));
   return CONV_OK;
 }
 
@@ -555,14 +570,14 @@ conv_status conv_linear_backward(const conv_linear_problem* p, const void* x, co
     g.a[0] = z;
     CONV_TRY(resolve(r.w, w, base, &g.b[0], s));
     g.epi.y = dx;
-    CONV_TRY(launch_product(r.pdx, g, p->dtype, base + r.part_off, s));
+    CONV_TRY(launch_product(r.pdx, g, p->dtype, base + r.part_off, false, s));
   }
   if (dw) {
     DenseGemm g = r.dw;
     g.a[0] = z;
     CONV_TRY(resolve(r.x, x, base, &g.b[0], s));
     g.epi.y = dw;
-    CONV_TRY(launch_product(r.pdw, g, p->dtype, base + r.part_off, s));
+    CONV_TRY(launch_product(r.pdw, g, p->dtype, base + r.part_off, false, s));
   }
   return CONV_OK;
 }
@@ -637,13 +652,13 @@ conv_status conv_gated_forward(const conv_gated_problem* p, const void* x, const
     g.epi.pre = reinterpret_cast<float*>(kept + keep.g_off);
     g.epi.pre2 = reinterpret_cast<float*>(kept + keep.u_off);
   }
-  CONV_TRY(launch_product(r.pup, g, p->dtype, base + r.part_off, s));
+  CONV_TRY(launch_product(r.pup, g, p->dtype, base + r.part_off, false, s));
   g = r.down;
   g.a[0] = h;
   CONV_TRY(resolve(r.wd, w_down, base, &g.b[0], s));
   g.epi.residual = p->has_residual ? residual : nullptr;
   g.epi.y = y;
-  CONV_TRY(launch_product(r.pdown, g, p->dtype, base + r.part_off, s));
+  CONV_TRY(launch_product(r.pdown, g, p->dtype, base + r.part_off, !r.wd.on, s));
   return CONV_OK;
 }
 
@@ -707,7 +722,7 @@ conv_status conv_gated_backward(const conv_gated_problem* p, const void* x, cons
     g.epi.pre2 = reinterpret_cast<float*>(const_cast<char*>(kept + keep.u_off));
     g.epi.y = base + r.dg_off;
     g.epi.y2 = base + r.du_off;
-    CONV_TRY(launch_product(r.pdh, g, p->dtype, part, s));
+    CONV_TRY(launch_product(r.pdh, g, p->dtype, part, false, s));
   }
   if (dx) {
     DenseGemm g = r.dx;
@@ -716,7 +731,7 @@ conv_status conv_gated_backward(const conv_gated_problem* p, const void* x, cons
     CONV_TRY(resolve(r.wg, w_gate, base, &g.b[0], s));
     CONV_TRY(resolve(r.wu, w_up, base, &g.b[1], s));
     g.epi.y = dx;
-    CONV_TRY(launch_product(r.pdx, g, p->dtype, part, s));
+    CONV_TRY(launch_product(r.pdx, g, p->dtype, part, false, s));
   }
   if (dwgu) {
     DenseGemm g = r.dwgu;
@@ -731,14 +746,14 @@ conv_status conv_gated_backward(const conv_gated_problem* p, const void* x, cons
       g.batch = 1;
       if (!dw_gate) g.a[0] = g.a[1], g.epi.y = dw_up;
     }
-    CONV_TRY(launch_product(q, g, p->dtype, part, s));
+    CONV_TRY(launch_product(q, g, p->dtype, part, false, s));
   }
   if (dw_down) {
     DenseGemm g = r.dwd;
     g.a[0] = dyc;
     g.b[0] = kept + keep.h_off;
     g.epi.y = dw_down;
-    CONV_TRY(launch_product(r.pdwd, g, p->dtype, part, s));
+    CONV_TRY(launch_product(r.pdwd, g, p->dtype, part, false, s));
   }
   return CONV_OK;
 }

@@ -219,15 +219,15 @@ __global__ void __launch_bounds__(256) dense_repack(const uint16_t* in, long lon
 }
 
 // dz and the column sums of a row block, bound by the bytes (dy, pre in; dz out).  A warp takes 32 * V columns of every
-// eighth row of the block (V columns per lane: 16 bytes of 16-bit values, or of float32), four rows in flight; the
+// eighth row of the block (V columns per lane: 16 bytes of 16-bit values, or of float32), two rows in flight; the
 // eight warps' partial sums are added in order.  VEC: every row of dy, pre and dz begins on a 16-byte boundary.
 template <typename T, bool VEC>
-__global__ void __launch_bounds__(256) dense_dz(const T* dy, long long ld_dy, const float* pre, T* dz, long long ld_dz,
+__global__ void __launch_bounds__(256, 3) dense_dz(const T* dy, long long ld_dy, const float* pre, T* dz, long long ld_dz,
                                                 float* part, int rows_per_block, long long rows, long long cols,
                                                 int act, float alpha, float beta) {
   constexpr bool FAST = sizeof(T) == 2;
   constexpr int V = VEC ? 16 / sizeof(T) : 2;
-  constexpr int U = 4;
+  constexpr int U = 2;
   __shared__ float sums[8][32 * V];
   const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
   const long long c = (static_cast<long long>(blockIdx.x) * 32 + tx) * V;

@@ -29,6 +29,12 @@ DenseTcPlan dense_tc_plan(const DenseGemm& g, int sm);
 cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype, cudaStream_t s);
 cudaError_t dense_error_word(uint32_t* word, int reset);
 
+// Few rows (dense_few.cu): at most 16 (8 of float32), any alignment.  `follows`:
+// the kernel before in the stream is this call's own, and writes no weights: the
+// launch overlaps its end, the first weights' loads included.
+constexpr int dense_few_rows(int dtype) { return dtype == CONV_F32 ? 8 : 16; }
+cudaError_t launch_dense_few(const DenseGemm& g, int dtype, bool follows, cudaStream_t s);
+
 // Adds the k ranges' planes in order and applies the epilogue.
 cudaError_t launch_dense_reduce(const DenseGemm& g, int dtype, cudaStream_t s);
 

@@ -88,13 +88,11 @@ bool aligned(const void* p, long long ld, size_t es) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<long long>(es) % 16 == 0;
 }
 
-}  // namespace
-
 // The tile and the k ranges of least time by this model, in clocks, fitted to full waves of 4096-term sums (bfloat16,
 // 1.85 GHz): 64 terms of a pair's tile take 165 + 1.73 nt (608 at nt = 256, 386 at 128: 512 and 256 are the MMAs
 // alone), of one SM's 128 columns 415 (its stage is as many bytes as the pair's of 256); a tile adds 600, a launch
 // 6000, the ranges' planes pass through L2 twice at some 3000 bytes a clock, with a launch of their own.
-DenseTcPlan dense_tc_plan(const DenseGemm& g, int sm) {
+DenseTcPlan search(const DenseGemm& g, int sm) {
   DenseTcPlan best = {};
   const int kb = static_cast<int>((static_cast<long long>(g.K) + dtc::kBK - 1) / dtc::kBK) * g.segs;
   const int products = dense_products(g);
@@ -126,6 +124,37 @@ DenseTcPlan dense_tc_plan(const DenseGemm& g, int sm) {
     }
   }
   return best;
+}
+
+// The plans of the shapes used last (a search takes microseconds, a small product too).
+struct PlanKey {
+  int M, N, K, segs, batch, dual, sm;
+  bool operator==(const PlanKey& o) const {
+    return M == o.M && N == o.N && K == o.K && segs == o.segs && batch == o.batch && dual == o.dual && sm == o.sm;
+  }
+};
+std::mutex g_plan_mu;
+struct {
+  PlanKey key;
+  DenseTcPlan plan;
+} g_plans[256];
+
+}  // namespace
+
+DenseTcPlan dense_tc_plan(const DenseGemm& g, int sm) {
+  const PlanKey key{g.M, g.N, g.K, g.segs, g.batch, g.dual, sm};
+  uint32_t h = 2166136261u;
+  for (int v : {key.M, key.N, key.K, key.segs, key.batch, key.dual}) h = (h ^ static_cast<uint32_t>(v)) * 16777619u;
+  auto& slot = g_plans[(h ^ (h >> 15)) % 256];
+  {
+    std::lock_guard<std::mutex> lock(g_plan_mu);
+    if (slot.key == key) return slot.plan;  // (an empty slot's sm is 0)
+  }
+  const DenseTcPlan plan = search(g, sm);
+  std::lock_guard<std::mutex> lock(g_plan_mu);
+  slot.key = key;
+  slot.plan = plan;
+  return plan;
 }
 
 cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dtype, cudaStream_t s) {

@@ -8,6 +8,7 @@ outputs and scratch with torch."""
 from __future__ import annotations
 
 import ctypes
+from array import array
 
 from . import ACTIVATIONS, DTYPES, _check, _dtype_name, _ptr, load
 
@@ -194,6 +195,9 @@ def _rows(t, width, what):
         raise ValueError(f"{what} must be [..., {width}], not {tuple(shape)}")
     if width > 1 and strides[-1] != 1:
         raise ValueError(f"{what}: the elements of a row must be adjacent")
+    if n == 2 and strides[0] >= width:
+        rows, stride = shape[0], strides[0]
+        return rows, stride if rows > 1 else 0
     rows, stride = 1, 0
     for i in range(n - 2, -1, -1):
         if shape[i] == 1:
@@ -211,54 +215,98 @@ def _rows(t, width, what):
 
 
 def _same(x, others):
-    for what, t in others:
-        if t is not None and (t.dtype != x.dtype or t.device != x.device):
-            raise ValueError(f"{what} must share x's element type and device")
-    if x.device.type != "cuda":
+    """The operands' device number; ValueError unless they share x's type and device."""
+    dtype, index = x.dtype, x.get_device()
+    for t in others:
+        if t is not None and (t.dtype != dtype or t.get_device() != index):
+            raise ValueError("operands must share x's element type and device")
+    if index < 0:
         raise ValueError("operands must be CUDA tensors")
+    return index
 
 
 class _On:
-    """The stream of a call.  Memory that torch allocates for the call belongs to
-    that stream, so that it is not handed out again while the call's kernels
-    still run; the call runs on the operands' device."""
+    """A call on another stream than the current one, or another device.  Memory
+    that torch allocates for the call belongs to that stream, so that it is not
+    handed out again while the call's kernels still run."""
 
     __slots__ = ("handle", "ctx")
 
-    def __init__(self, device, stream):
+    def __init__(self, index, stream):
         import torch
-        self.ctx = None
         if stream is None:
-            if device.index is not None and device.index != torch.cuda.current_device():
-                self.ctx = torch.cuda.device(device)
-            self.handle = torch.cuda.current_stream(device).cuda_stream
+            self.ctx = torch.cuda.device(index)
+            self.handle = torch.cuda.current_stream(index).cuda_stream
         else:
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=device)
+            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=index)
             self.ctx = torch.cuda.stream(s)
             self.handle = s.cuda_stream
 
     def __enter__(self):
-        if self.ctx is not None:
-            self.ctx.__enter__()
+        self.ctx.__enter__()
         return self.handle
 
     def __exit__(self, *exc):
-        if self.ctx is not None:
-            self.ctx.__exit__(*exc)
+        self.ctx.__exit__(*exc)
 
 
-def _unaligned(tensors) -> bool:
-    return any(t is not None and t.data_ptr() % 16 for t in tensors)
+class _Here:
+    """A call on the current stream of the current device."""
+
+    __slots__ = ("handle",)
+
+    def __enter__(self):
+        return self.handle
+
+    def __exit__(self, *exc):
+        pass
 
 
-def _scratch(need, given, device):
-    """(tensor or None, bytes)"""
+def _on(index, stream):
     import torch
+    if stream is not None or index != torch.cuda.current_device():
+        return _On(index, stream)
+    here = _Here()
+    here.handle = torch.cuda.current_stream(index).cuda_stream
+    return here
+
+
+# Problems and their scratch sizes by shape, so that a call of a shape seen before marshals nothing anew.
+_linear_cache: dict = {}
+_gated_cache: dict = {}
+
+
+def _linear_problem(back, *key):
+    found = _linear_cache.get((back, key))
+    if found is None:
+        p = LinearProblem(*key)
+        need = (conv_linear_backward_scratch_bytes if back else conv_linear_scratch_bytes)(p)
+        if len(_linear_cache) >= 4096:
+            _linear_cache.clear()
+        found = _linear_cache[(back, key)] = (p, ctypes.byref(p), need)
+    return found
+
+
+def _gated_problem(back, *key):
+    found = _gated_cache.get((back, key))
+    if found is None:
+        p = GatedProblem(*key)
+        need = (conv_gated_backward_scratch_bytes if back else conv_gated_scratch_bytes)(p)
+        if len(_gated_cache) >= 4096:
+            _gated_cache.clear()
+        found = _gated_cache[(back, key)] = (p, ctypes.byref(p), need, conv_gated_saved_bytes(p))
+    return found
+
+
+def _scratch(need, given, x):
+    """(tensor or None, its address, bytes)"""
     if given is not None:
-        return given, given.numel() * given.element_size()
+        return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
-        return None, 0
-    return torch.empty(need, dtype=torch.uint8, device=device), need
+        return None, None, 0
+    import torch
+    t = torch.empty(need, dtype=torch.uint8, device=x.device)
+    return t, t.data_ptr(), need
 
 
 def _dense_out(out, shape, like, what):
@@ -278,38 +326,48 @@ def linear(x, w, bias=None, residual=None, *, act="identity", alpha=0.0, beta=0.
     Rows may be strided.  ``residual_last``: y = act(x w^T + bias) + residual.
     With ``save``, returns (y, pre): pre is the activation's argument in float32
     for ``linear_backward`` (None for the identity, which needs none)."""
-    import torch
-    dt = _dtype_name(x)
+    dt = DTYPES[_dtype_name(x)]
     if w.dim() != 2:
         raise ValueError("w must be [c_out, c_in]")
     c_out, c_in = w.shape
-    _same(x, (("w", w), ("bias", bias), ("residual", residual), ("out", out)))
+    index = _same(x, (w, bias, residual, out))
     rows, ldx = _rows(x, c_in, "x")
-    _, ldw = _rows(w, c_in, "w")
-    y_shape = x.shape[:-1] + (c_out,)
+    ldw = _rows(w, c_in, "w")[1]
+    xs = x.shape
+    y_shape = (xs[0], c_out) if len(xs) == 2 else (*xs[:-1], c_out)
     ldr = ldy = 0
-    if bias is not None and (bias.dim() != 1 or bias.shape[0] != c_out or not bias.is_contiguous()):
-        raise ValueError("bias must be a contiguous [c_out]")
+    xp, wp, bp, rp = x.data_ptr(), w.data_ptr(), None, None
+    if bias is not None:
+        if bias.dim() != 1 or bias.shape[0] != c_out or not bias.is_contiguous():
+            raise ValueError("bias must be a contiguous [c_out]")
+        bp = bias.data_ptr()
     if residual is not None:
         if residual.shape != y_shape:
             raise ValueError("residual must have y's shape")
         ldr = _rows(residual, c_out, "residual")[1]
+        rp = residual.data_ptr()
     if out is not None:
         if out.shape != y_shape:
             raise ValueError("out must have y's shape")
         ldy = _rows(out, c_out, "out")[1]
     if residual_last:
         flags |= FLAG_LINEAR_RESIDUAL_LAST
-    if dt != "f32" and _unaligned((x, w)):
+    if (xp | wp) & 15 and dt:
         flags |= FLAG_LINEAR_UNALIGNED
-    with _On(x.device, stream) as handle:
+    with _on(index, stream) as handle:
         if out is None:
-            out = torch.empty(y_shape, dtype=x.dtype, device=x.device)
-        pre = torch.empty(y_shape, dtype=torch.float32, device=x.device) if save and act != "identity" else None
-        p = LinearProblem(rows, c_in, c_out, ldx, ldw, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, DTYPES[dt],
-                          0 if bias is None else 1, 0 if residual is None else 1, flags)
-        buf, n = _scratch(conv_linear_scratch_bytes(p) if scratch is None else 0, scratch, x.device)
-        conv_linear_forward(p, x, w, bias, residual, out, pre, buf, n, handle)
+            out = x.new_empty(y_shape)
+        pre = None
+        if save and act != "identity":
+            import torch
+            pre = torch.empty(y_shape, dtype=torch.float32, device=x.device)
+        _, ref, need = _linear_problem(False, rows, c_in, c_out, ldx, ldw, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, dt,
+                                       0 if bp is None else 1, 0 if rp is None else 1, flags)
+        buf, at, n = _scratch(need, scratch, x)
+        status = _load().conv_linear_forward(ref, xp, wp, bp, rp, out.data_ptr(), None if pre is None else pre.data_ptr(),
+                                             at, n, handle or None)
+        if status:
+            _check(status, "conv_linear_forward")
     return (out, pre) if save else out
 
 
@@ -320,11 +378,11 @@ def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, 
     dresidual), None where not wanted.  ``pre`` is what linear(..., save=True)
     returned; act, alpha, beta and residual_last are that call's."""
     import torch
-    dt = _dtype_name(x)
+    dt = DTYPES[_dtype_name(x)]
     if w.dim() != 2:
         raise ValueError("w must be [c_out, c_in]")
     c_out, c_in = w.shape
-    _same(x, (("w", w), ("dy", dy)))
+    index = _same(x, (w, dy))
     rows, ldx = _rows(x, c_in, "x")
     _, ldw = _rows(w, c_in, "w")
     if dy.shape != x.shape[:-1] + (c_out,):
@@ -339,17 +397,19 @@ def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, 
         pre = None
     if residual_last:
         flags |= FLAG_LINEAR_RESIDUAL_LAST
-    if dt != "f32" and _unaligned((x if need_dw else None, w if need_dx else None, dy if pre is None else None)):
+    xp, wp, dyp = x.data_ptr(), w.data_ptr(), dy.data_ptr()
+    if dt and ((xp if need_dw else 0) | (wp if need_dx else 0) | (dyp if pre is None else 0)) & 15:
         flags |= FLAG_LINEAR_UNALIGNED
-    with _On(x.device, stream) as handle:
+    with _on(index, stream) as handle:
         dx = _dense_out(dx, x.shape, x, "dx") if need_dx else None
         dw = _dense_out(dw, w.shape, x, "dw") if need_dw else None
         dbias = torch.empty(c_out, dtype=x.dtype, device=x.device) if need_dbias else None
         dres = torch.empty(dy.shape, dtype=x.dtype, device=x.device) if need_dresidual else None
-        p = LinearProblem(rows, c_in, c_out, ldx, ldw, 0, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, DTYPES[dt], 0, 0,
-                          flags)
-        buf, n = _scratch(conv_linear_backward_scratch_bytes(p) if scratch is None else 0, scratch, x.device)
-        conv_linear_backward(p, x, w, pre, dy, dx, dw, dbias, dres, buf, n, handle)
+        _, ref, need = _linear_problem(True, rows, c_in, c_out, ldx, ldw, 0, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, dt,
+                                       0, 0, flags)
+        buf, at, n = _scratch(need, scratch, x)
+        _check(_load().conv_linear_backward(ref, xp, wp, _ptr(pre), dyp, _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dres), at, n,
+                                            handle or None), "conv_linear_backward")
     return dx, dw, dbias, dres
 
 
@@ -370,8 +430,8 @@ def gated_ffn(x, w_gate, w_up, w_down, residual=None, *, act="silu", alpha=0.0, 
     residual and y [..., c_out].  With ``save``, returns (y, saved) for
     ``gated_ffn_backward``."""
     import torch
-    dt = _dtype_name(x)
-    _same(x, (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down), ("residual", residual), ("out", out)))
+    dt = DTYPES[_dtype_name(x)]
+    index = _same(x, (w_gate, w_up, w_down, residual, out))
     c_in, hidden, c_out = _gated(x, w_gate, w_up, w_down)
     rows, ldx = _rows(x, c_in, "x")
     y_shape = x.shape[:-1] + (c_out,)
@@ -384,16 +444,19 @@ def gated_ffn(x, w_gate, w_up, w_down, residual=None, *, act="silu", alpha=0.0, 
         if out.shape != y_shape:
             raise ValueError("out must have y's shape")
         ldy = _rows(out, c_out, "out")[1]
-    if dt != "f32" and _unaligned((x, w_gate, w_up, w_down)):
+    ptrs = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr()
+    if dt and (ptrs[0] | ptrs[1] | ptrs[2] | ptrs[3]) & 15:
         flags |= FLAG_LINEAR_UNALIGNED
-    with _On(x.device, stream) as handle:
+    with _on(index, stream) as handle:
         if out is None:
-            out = torch.empty(y_shape, dtype=x.dtype, device=x.device)
-        p = GatedProblem(rows, c_in, hidden, c_out, ldx, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, DTYPES[dt],
-                         0 if residual is None else 1, flags)
-        saved = torch.empty(conv_gated_saved_bytes(p), dtype=torch.uint8, device=x.device) if save else None
-        buf, n = _scratch(conv_gated_scratch_bytes(p) if scratch is None else 0, scratch, x.device)
-        conv_gated_forward(p, x, w_gate, w_up, w_down, residual, out, saved, buf, n, handle)
+            out = x.new_empty(y_shape)
+        _, ref, need, kept = _gated_problem(False, rows, c_in, hidden, c_out, ldx, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha,
+                                            beta, dt, 0 if residual is None else 1, flags)
+        saved = torch.empty(kept, dtype=torch.uint8, device=x.device) if save else None
+        buf, at, n = _scratch(need, scratch, x)
+        status = _load().conv_gated_forward(ref, *ptrs, _ptr(residual), out.data_ptr(), _ptr(saved), at, n, handle or None)
+        if status:
+            _check(status, "conv_gated_forward")
     return (out, saved) if save else out
 
 
@@ -404,24 +467,27 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=
     save=True) returned; act, alpha and beta are that call's.  The residual's
     gradient is dy."""
     import torch
-    dt = _dtype_name(x)
-    _same(x, (("w_gate", w_gate), ("w_up", w_up), ("w_down", w_down), ("dy", dy)))
+    dt = DTYPES[_dtype_name(x)]
+    index = _same(x, (w_gate, w_up, w_down, dy))
     c_in, hidden, c_out = _gated(x, w_gate, w_up, w_down)
     rows, ldx = _rows(x, c_in, "x")
     if dy.shape != x.shape[:-1] + (c_out,):
         raise ValueError("dy must have y's shape")
     ldy = _rows(dy, c_out, "dy")[1]
-    if dt != "f32" and _unaligned((x, w_gate, w_up, w_down, dy)):
+    ptrs = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr()
+    if dt and (ptrs[0] | ptrs[1] | ptrs[2] | ptrs[3] | dy.data_ptr()) & 15:
         flags |= FLAG_LINEAR_UNALIGNED
-    p = GatedProblem(rows, c_in, hidden, c_out, ldx, 0, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, DTYPES[dt], 0, flags)
-    if saved.dtype != torch.uint8 or saved.device != x.device or saved.numel() != conv_gated_saved_bytes(p):
-        raise ValueError("saved must be what gated_ffn(..., save=True) returned for this problem")
-    with _On(x.device, stream) as handle:
+    with _on(index, stream) as handle:
+        _, ref, need, kept = _gated_problem(True, rows, c_in, hidden, c_out, ldx, 0, ldy, LINEAR_ACTIVATIONS[act], alpha,
+                                            beta, dt, 0, flags)
+        if saved.dtype != torch.uint8 or saved.get_device() != index or saved.numel() != kept:
+            raise ValueError("saved must be what gated_ffn(..., save=True) returned for this problem")
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
         dws = [torch.empty(w.shape, dtype=x.dtype, device=x.device) if need_dw else None
                for w in (w_gate, w_up, w_down)]
-        buf, n = _scratch(conv_gated_backward_scratch_bytes(p) if scratch is None else 0, scratch, x.device)
-        conv_gated_backward(p, x, w_gate, w_up, w_down, saved, dy, dx, *dws, buf, n, handle)
+        buf, at, n = _scratch(need, scratch, x)
+        _check(_load().conv_gated_backward(ref, *ptrs, saved.data_ptr(), dy.data_ptr(), _ptr(dx), *[_ptr(t) for t in dws],
+                                           at, n, handle or None), "conv_gated_backward")
     return (dx, *dws)
 
 
@@ -432,35 +498,42 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, scratch=None, stream=
     of the element types."""
     import torch
     grads = list(grads)
-    outs = grads if out is None else list(out)
-    if len(outs) != len(grads):
-        raise ValueError("out must have one tensor per gradient")
-    if not grads:
-        raise ValueError("no gradients")
-    device = grads[0].device
-    if device.type != "cuda":
-        raise ValueError("operands must be CUDA tensors")
     n = len(grads)
+    if n == 0:
+        raise ValueError("no gradients")
+    # one pass over the list per property (a model has hundreds of tensors; their kernels take microseconds)
+    tensor = torch.Tensor
+    outs = grads if out is None else list(out)
+    if len(outs) != n:
+        raise ValueError("out must have one tensor per gradient")
     names = {torch.float32: 0, torch.float16: 1, torch.bfloat16: 2}
-    for g, o in zip(grads, outs):
-        if g.dtype not in names:
-            raise TypeError(f"unsupported element type {g.dtype}")
-        if not g.is_contiguous() or g.device != device:
-            raise ValueError("gradients must be contiguous and on one device")
-        if o is not g and (o.dtype != g.dtype or o.shape != g.shape or o.device != device or not o.is_contiguous()):
-            raise ValueError("out must be contiguous tensors of the gradients' shapes and element types")
-    vps = ctypes.c_void_p * n
-    sizes = (ctypes.c_int64 * n)(*[g.numel() for g in grads])
-    ins = vps(*[g.data_ptr() for g in grads])
-    to = ins if out is None else vps(*[o.data_ptr() for o in outs])
-    types = (ctypes.c_int32 * n)(*[names[g.dtype] for g in grads])
-    with _On(device, stream) as handle:
-        norm = torch.empty((), dtype=torch.float32, device=device)
+    types = [g.dtype for g in grads]
+    sizes = list(map(tensor.numel, grads))
+    index = grads[0].get_device()
+    if index < 0:
+        raise ValueError("operands must be CUDA tensors")
+    if set(map(tensor.get_device, grads)) != {index} or not all(map(tensor.is_contiguous, grads)):
+        raise ValueError("gradients must be contiguous and on one device")
+    if out is not None and ([o.dtype for o in outs] != types or list(map(tensor.numel, outs)) != sizes or
+                            set(map(tensor.get_device, outs)) != {index} or not all(map(tensor.is_contiguous, outs))):
+        raise ValueError("out must be contiguous tensors of the gradients' sizes and element types")
+    try:
+        types = array("i", [names[t] for t in types])
+    except KeyError as e:
+        raise TypeError(f"unsupported element type {e}") from None
+    sizes = array("q", sizes)
+    ins = array("Q", map(tensor.data_ptr, grads))
+    to = ins if out is None else array("Q", map(tensor.data_ptr, outs))
+    lib = _load()
+    with _on(index, stream) as handle:
+        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        at_sizes = sizes.buffer_info()[0]
         if scratch is None:
             need = ctypes.c_size_t()
-            _check(_load().conv_clip_scratch_bytes(n, sizes, ctypes.byref(need)), "conv_clip_scratch_bytes")
-            scratch = torch.empty(need.value, dtype=torch.uint8, device=device)
-        _check(_load().conv_clip_grads(n, ins, to, sizes, types, float(max_norm), float(eps), norm.data_ptr(),
-                                       scratch.data_ptr(), scratch.numel() * scratch.element_size(), handle or None),
-               "conv_clip_grads")
+            _check(lib.conv_clip_scratch_bytes(n, ctypes.cast(at_sizes, ctypes.POINTER(ctypes.c_int64)), ctypes.byref(need)),
+                   "conv_clip_scratch_bytes")
+            scratch = torch.empty(need.value, dtype=torch.uint8, device=grads[0].device)
+        _check(lib.conv_clip_grads(n, ins.buffer_info()[0], to.buffer_info()[0], at_sizes, types.buffer_info()[0],
+                                   float(max_norm), float(eps), norm.data_ptr(), scratch.data_ptr(),
+                                   scratch.numel() * scratch.element_size(), handle or None), "conv_clip_grads")
     return norm
