@@ -65,7 +65,7 @@ def _load() -> ctypes.CDLL:
             "conv_gated_saved_bytes": [gp, P(sz)],
             "conv_gated_forward": [gp] + [vp] * 8 + [sz, vp],
             "conv_gated_backward": [gp] + [vp] * 11 + [sz, vp],
-            "conv_clip_scratch_bytes": [i64, P(i64), P(sz)],
+            "conv_clip_scratch_bytes": [i64, vp, P(sz)],
             "conv_clip_grads": [i64, vp, vp, vp, vp, f, f, vp, vp, sz, vp],
             "conv_linear_device_error": [P(ctypes.c_uint32), i32],
         }.items():
@@ -262,12 +262,19 @@ class _Here:
         pass
 
 
+_raw_stream = None
+
+
 def _on(index, stream):
+    global _raw_stream
     import torch
     if stream is not None or index != torch.cuda.current_device():
         return _On(index, stream)
+    if _raw_stream is None:
+        _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+            lambda i: torch.cuda.current_stream(i).cuda_stream)
     here = _Here()
-    here.handle = torch.cuda.current_stream(index).cuda_stream
+    here.handle = _raw_stream(index)
     return here
 
 
@@ -298,15 +305,32 @@ def _gated_problem(back, *key):
     return found
 
 
-def _scratch(need, given, x):
-    """(tensor or None, its address, bytes)"""
+# Scratch of up to _KEPT bytes is kept per stream: the calls of a stream run one after another, and an allocation from
+# torch's pool takes longer than a small call's own work.  A larger one, and one under graph capture (whose memory belongs
+# to the graph), is the call's own.
+_KEPT = 32 << 20
+_kept: dict = {}
+
+
+def _scratch(need, given, index, handle):
+    """(tensor or None, its address, bytes); runs under the call's stream."""
     if given is not None:
         return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
         return None, None, 0
     import torch
-    t = torch.empty(need, dtype=torch.uint8, device=x.device)
-    return t, t.data_ptr(), need
+    if need > _KEPT or torch.cuda.is_current_stream_capturing():
+        t = torch.empty(need, dtype=torch.uint8, device=index)
+        return t, t.data_ptr(), need
+    t, at, size = _kept.get((index, handle), (None, 0, 0))
+    if size < need:
+        size = max(need, 1 << 20)
+        t = torch.empty(size, dtype=torch.uint8, device=index)
+        at = t.data_ptr()
+        if len(_kept) >= 64:
+            _kept.clear()
+        _kept[(index, handle)] = (t, at, size)
+    return t, at, size
 
 
 def _dense_out(out, shape, like, what):
@@ -355,15 +379,17 @@ def linear(x, w, bias=None, residual=None, *, act="identity", alpha=0.0, beta=0.
     if (xp | wp) & 15 and dt:
         flags |= FLAG_LINEAR_UNALIGNED
     with _on(index, stream) as handle:
+        import torch
         if out is None:
-            out = x.new_empty(y_shape)
+            # (empty_like is the quicker of the two)
+            out = torch.empty_like(residual) if rp is not None and ldr in (0, c_out) and residual.is_contiguous() else \
+                torch.empty(y_shape, dtype=x.dtype, device=x.device)
         pre = None
         if save and act != "identity":
-            import torch
             pre = torch.empty(y_shape, dtype=torch.float32, device=x.device)
         _, ref, need = _linear_problem(False, rows, c_in, c_out, ldx, ldw, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, dt,
                                        0 if bp is None else 1, 0 if rp is None else 1, flags)
-        buf, at, n = _scratch(need, scratch, x)
+        buf, at, n = _scratch(need, scratch, index, handle)
         status = _load().conv_linear_forward(ref, xp, wp, bp, rp, out.data_ptr(), None if pre is None else pre.data_ptr(),
                                              at, n, handle or None)
         if status:
@@ -407,7 +433,7 @@ def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, 
         dres = torch.empty(dy.shape, dtype=x.dtype, device=x.device) if need_dresidual else None
         _, ref, need = _linear_problem(True, rows, c_in, c_out, ldx, ldw, 0, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, dt,
                                        0, 0, flags)
-        buf, at, n = _scratch(need, scratch, x)
+        buf, at, n = _scratch(need, scratch, index, handle)
         _check(_load().conv_linear_backward(ref, xp, wp, _ptr(pre), dyp, _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dres), at, n,
                                             handle or None), "conv_linear_backward")
     return dx, dw, dbias, dres
@@ -449,11 +475,12 @@ def gated_ffn(x, w_gate, w_up, w_down, residual=None, *, act="silu", alpha=0.0, 
         flags |= FLAG_LINEAR_UNALIGNED
     with _on(index, stream) as handle:
         if out is None:
-            out = x.new_empty(y_shape)
+            out = torch.empty_like(residual) if residual is not None and residual.is_contiguous() else \
+                torch.empty(y_shape, dtype=x.dtype, device=x.device)
         _, ref, need, kept = _gated_problem(False, rows, c_in, hidden, c_out, ldx, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha,
                                             beta, dt, 0 if residual is None else 1, flags)
         saved = torch.empty(kept, dtype=torch.uint8, device=x.device) if save else None
-        buf, at, n = _scratch(need, scratch, x)
+        buf, at, n = _scratch(need, scratch, index, handle)
         status = _load().conv_gated_forward(ref, *ptrs, _ptr(residual), out.data_ptr(), _ptr(saved), at, n, handle or None)
         if status:
             _check(status, "conv_gated_forward")
@@ -485,7 +512,7 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
         dws = [torch.empty(w.shape, dtype=x.dtype, device=x.device) if need_dw else None
                for w in (w_gate, w_up, w_down)]
-        buf, at, n = _scratch(need, scratch, x)
+        buf, at, n = _scratch(need, scratch, index, handle)
         _check(_load().conv_gated_backward(ref, *ptrs, saved.data_ptr(), dy.data_ptr(), _ptr(dx), *[_ptr(t) for t in dws],
                                            at, n, handle or None), "conv_gated_backward")
     return (dx, *dws)
@@ -526,14 +553,11 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, scratch=None, stream=
     to = ins if out is None else array("Q", map(tensor.data_ptr, outs))
     lib = _load()
     with _on(index, stream) as handle:
-        norm = torch.empty((), dtype=torch.float32, device=grads[0].device)
+        norm = torch.empty((), dtype=torch.float32, device=index)
         at_sizes = sizes.buffer_info()[0]
-        if scratch is None:
-            need = ctypes.c_size_t()
-            _check(lib.conv_clip_scratch_bytes(n, ctypes.cast(at_sizes, ctypes.POINTER(ctypes.c_int64)), ctypes.byref(need)),
-                   "conv_clip_scratch_bytes")
-            scratch = torch.empty(need.value, dtype=torch.uint8, device=grads[0].device)
+        need = ctypes.c_size_t()
+        _check(lib.conv_clip_scratch_bytes(n, at_sizes, ctypes.byref(need)), "conv_clip_scratch_bytes")
+        buf, at, size = _scratch(need.value, scratch, index, handle)
         _check(lib.conv_clip_grads(n, ins.buffer_info()[0], to.buffer_info()[0], at_sizes, types.buffer_info()[0],
-                                   float(max_norm), float(eps), norm.data_ptr(), scratch.data_ptr(),
-                                   scratch.numel() * scratch.element_size(), handle or None), "conv_clip_grads")
+                                   max_norm, eps, norm.data_ptr(), at, size, handle or None), "conv_clip_grads")
     return norm
