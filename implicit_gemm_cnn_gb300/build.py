@@ -22,7 +22,7 @@ INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(BUILD, "libconv.so")
 SOURCES = ["conv_api.cu", "conv_ffma.cu", "conv_depthwise.cu", "conv_tc.cu", "conv_tcw.cu", "conv_integer.cu", "conv_transpose.cu", "conv_winograd.cu", "conv_pointwise.cu",
-           "dense_api.cu", "dense_ffma.cu", "dense_few.cu", "dense_tc.cu", "dense_tc_f16.cu", "dense_tc_bf16.cu", "clip.cu"]
+           "dense_api.cu", "dense_ffma.cu", "dense_few.cu", "dense_tc.cu", "dense_tc_f16.cu", "dense_tc_bf16.cu", "dense_tc32.cu", "clip.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 
 

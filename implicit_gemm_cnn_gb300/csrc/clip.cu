@@ -34,9 +34,6 @@ struct ClipTable {
   int count;
 };
 
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-
 template <int CAP>
 __device__ __forceinline__ int find_tensor(const ClipTable<CAP>& t, int chunk) {
   int lo = 0, hi = t.count;  // first[lo] <= chunk < first[hi]
@@ -172,6 +169,7 @@ __device__ __forceinline__ double block_sum(double v) {
 
 template <int CAP>
 __global__ void __launch_bounds__(kThreads) clip_norm(const __grid_constant__ ClipTable<CAP> t, double* part) {
+  griddep_wait();
   griddep_launch();
   double acc = 0.0;
   const int chunks = t.first[t.count];
@@ -231,6 +229,7 @@ template <int CAP>
 __global__ void __launch_bounds__(kThreads) clip_scale(const __grid_constant__ ClipTable<CAP> t, const double* part,
                                                        int parts, float max_norm, float eps, float* norm) {
   griddep_wait();
+  griddep_launch();
   double s = 0.0;
   for (int i = threadIdx.x; i < parts; i += kThreads) s += part[i];
   const double total = sqrt(block_sum(s));
@@ -287,8 +286,8 @@ cudaError_t run(long long count, const void* const* in, void* const* out, const 
   do {
     at = fill(&t, at, count, in, out, sizes, dtypes);
     const int blocks = blocks_of();
-    clip_norm<CAP><<<blocks, kThreads, 0, s>>>(t, part + parts);
-    const cudaError_t err = cudaGetLastError();
+    const cudaError_t err = launch_overlapped(clip_norm<CAP>, dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, s, t,
+                                              part + parts);
     if (err != cudaSuccess) return err;
     parts += blocks;
     ++launches;
@@ -300,18 +299,8 @@ cudaError_t run(long long count, const void* const* in, void* const* out, const 
     at = fill(&t, 0, count, in, out, sizes, dtypes);
   }
   for (bool first = true;; first = false) {
-    // the first launch overlaps its start with the norm pass's end, and waits for it
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(blocks_of()));
-    cfg.blockDim = dim3(kThreads);
-    cfg.stream = s;
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = attr;
-    cfg.numAttrs = first ? 1 : 0;
-    const cudaError_t err = cudaLaunchKernelEx(&cfg, clip_scale<CAP>, t, static_cast<const double*>(part), parts,
-                                               max_norm, eps, first ? norm : static_cast<float*>(nullptr));
+    const cudaError_t err = launch_overlapped(clip_scale<CAP>, dim3(static_cast<unsigned>(blocks_of())), kThreads, 0, 1, s, t,
+                                              part, parts, max_norm, eps, first ? norm : static_cast<float*>(nullptr));
     if (err != cudaSuccess) return err;
     if (!out || at >= count) break;
     at = fill(&t, at, count, in, out, sizes, dtypes);

@@ -94,14 +94,14 @@ struct Product {
 };
 
 // `g` without addresses.  `tc`: 16-bit operands with rows a tensor-core copy can take.
-Product plan_product(const DenseGemm& g, bool tc, bool few, int sm) {
+Product plan_product(const DenseGemm& g, int dtype, bool tc, bool few, int sm) {
   Product r = {};
   if (few) {
     r.variant = V_FEW;
     r.split = 1;
   } else if (tc) {
     r.variant = V_TC;
-    r.tc = dense_tc_plan(g, sm);
+    r.tc = dense_tc_plan(g, dtype, sm);
     r.split = r.tc.split;
   } else {
     r.variant = V_FFMA;
@@ -129,21 +129,21 @@ cudaError_t launch_product(const Product& r, DenseGemm g, int dtype, void* part,
   return err;
 }
 
-void describe_product(const Product& r, const DenseGemm& g, int sm, char* buf, size_t len) {
+void describe_product(const Product& r, const DenseGemm& g, bool f32, int sm, char* buf, size_t len) {
   const long long k = static_cast<long long>(g.segs) * g.K;
   if (r.variant == V_FEW)
     snprintf(buf, len, "few_rows tile=%dx16 split=1 products=%d sums over %lld sms=%d launches=1", g.M, dense_products(g), k, sm);
   else if (r.variant == V_TC)
-    snprintf(buf, len, "tcgen05 tile=%dx%d sms_per_tile=%d tiles=%lld split=%d products=%d sums over %lld sms=%d launches=%d",
-             128 * r.tc.cg, r.tc.nt, r.tc.cg, r.tc.tiles, r.split, dense_products(g), k, sm, r.launches);
+    snprintf(buf, len, "%s tile=%dx%d sms_per_tile=%d tiles=%lld split=%d products=%d sums over %lld sms=%d launches=%d",
+             f32 ? "tcgen05_bf16x3" : "tcgen05", 128 * r.tc.cg, r.tc.nt, r.tc.cg, r.tc.tiles, r.split, dense_products(g), k, sm, r.launches);
   else
     snprintf(buf, len, "ffma tile=%dx%d split=%d products=%d sums over %lld sms=%d launches=%d", r.ffma.bm, r.ffma.bn,
              r.split, dense_products(g), k, sm, r.launches);
 }
 
-// A 16-bit operand's copy into aligned rows, where its rows need one.
+// An operand's copy: a 16-bit one's into aligned rows, where its rows need one; the three planes of a float32 one.
 struct Copy {
-  bool on;
+  bool on, planes;
   long long rows, cols, ld_in, ld;
   size_t off, bytes;
 };
@@ -154,25 +154,33 @@ struct Layout {
     total = align256(total + bytes);
     return at;
   }
-  Copy copy(int dtype, bool unaligned, long long rows, long long cols, long long ld) {
+  // `tc`: for the tensor cores (the other kernels take operands as they are)
+  Copy copy(bool tc, int dtype, bool unaligned, long long rows, long long cols, long long ld) {
     Copy c = {};
-    c.on = dtype != CONV_F32 && (unaligned || ld % 8 != 0) && rows > 0;
+    c.planes = dtype == CONV_F32;
+    c.on = tc && (c.planes || unaligned || ld % 8 != 0) && rows > 0;
     c.rows = rows; c.cols = cols; c.ld_in = ld;
     c.ld = c.on ? round8(cols) : ld;
     if (c.on) {
-      c.bytes = static_cast<size_t>(rows) * c.ld * 2;
+      c.bytes = static_cast<size_t>(rows) * c.ld * (c.planes ? 6 : 2);
       c.off = take(c.bytes);
     }
     return c;
   }
 };
-// The operand as the product reads it: the copy (enqueued here), or itself.
-cudaError_t resolve(const Copy& c, const void* in, char* scratch, const void** out, cudaStream_t s) {
-  *out = in;
-  if (!c.on) return cudaSuccess;
-  *out = scratch + c.off;
-  return launch_dense_repack(in, c.ld_in, scratch + c.off, c.ld, c.rows, c.cols, s);
-}
+// Operands as the products read them: their copies, or themselves.  add() several, then enqueue() their copies together.
+struct Copies {
+  CopyJob job[kCopyJobs];
+  int count = 0;
+  bool planes = false;
+  const void* add(const Copy& c, const void* in, char* scratch) {
+    if (!c.on) return in;
+    planes = c.planes;
+    job[count++] = {in, scratch + c.off, c.ld_in, c.ld, c.rows, c.cols};
+    return scratch + c.off;
+  }
+  cudaError_t enqueue(cudaStream_t s) const { return launch_dense_copies(job, count, planes, s); }
+};
 
 DenseGemm make_gemm(long long m, long long n, long long k, int a_mn, int b_mn, long long lda, long long ldb) {
   DenseGemm g;
@@ -195,37 +203,37 @@ struct Mode {
 };
 Mode mode_of(uint32_t flags, int dtype) {
   Mode m;
-  m.tc = dtype != CONV_F32 && !(flags & CONV_LINEAR_FLAG_FORCE_FFMA);
-  m.copies = m.tc && (flags & CONV_LINEAR_FLAG_UNALIGNED);
+  m.tc = !(flags & CONV_LINEAR_FLAG_FORCE_FFMA);
+  m.copies = m.tc && dtype != CONV_F32 && (flags & CONV_LINEAR_FLAG_UNALIGNED);
   m.few = !(flags & (CONV_LINEAR_FLAG_FORCE_FFMA | CONV_LINEAR_FLAG_NO_FEW_ROWS));
   return m;
 }
 
-bool few_rows(long long rows, int dtype) { return rows >= 1 && rows <= dense_few_rows(dtype); }
+bool few_rows(long long rows) { return rows >= 1 && rows <= kFewRows; }
 
 struct LinearPlan {
-  Copy x, w, dy;
+  Copy x, w, z;
   DenseGemm fwd, dx, dw;
   Product pfwd, pdx, pdw;
   size_t part_off, dz_off, col_off, total;
   long long ldz;
   int col_blocks;
-  bool dz;   // dz is written (an activation); else dy stands for it
+  bool dz, dz_planes;   // dz is written (an activation), as float32 operands' planes; else dy stands for it
 };
 
 LinearPlan plan_linear(const conv_linear_problem* p, const LinearShape& sh, const Mode& mode, int sm) {
   LinearPlan r = {};
   Layout l;
-  const bool few = mode.few && few_rows(p->rows, p->dtype);
-  const int dt = mode.tc && !few ? p->dtype : CONV_F32;  // what copies go by
-  r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
-  r.w = l.copy(dt, mode.copies, p->c_out, p->c_in, sh.ldw);
+  const bool few = mode.few && few_rows(p->rows);
+  const bool tc = mode.tc && !few;
+  r.x = l.copy(tc, p->dtype, mode.copies, p->rows, p->c_in, sh.ldx);
+  r.w = l.copy(tc, p->dtype, mode.copies, p->c_out, p->c_in, sh.ldw);
   r.fwd = make_gemm(p->rows, p->c_out, p->c_in, 0, 0, r.x.ld, r.w.ld);
   DenseEpi& e = r.fwd.epi;
   e.act = p->act; e.alpha = p->act_alpha; e.beta = p->act_beta;
   e.residual_last = (p->flags & CONV_LINEAR_FLAG_RESIDUAL_LAST) != 0;
   e.ldr = sh.ldr; e.ldy = sh.ldy; e.ldp = p->c_out;
-  if (p->rows > 0) r.pfwd = plan_product(r.fwd, mode.tc, few, sm);
+  if (p->rows > 0) r.pfwd = plan_product(r.fwd, p->dtype, mode.tc, few, sm);
   r.part_off = l.take(r.pfwd.part_bytes);
   r.total = l.total;
   return r;
@@ -234,26 +242,25 @@ LinearPlan plan_linear(const conv_linear_problem* p, const LinearShape& sh, cons
 LinearPlan plan_linear_backward(const conv_linear_problem* p, const LinearShape& sh, const Mode& mode, int sm) {
   LinearPlan r = {};
   Layout l;
-  const int dt = mode.tc ? p->dtype : CONV_F32;
-  r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
-  r.w = l.copy(dt, mode.copies, p->c_out, p->c_in, sh.ldw);
+  const bool tc = mode.tc;
+  r.x = l.copy(tc, p->dtype, mode.copies, p->rows, p->c_in, sh.ldx);
+  r.w = l.copy(tc, p->dtype, mode.copies, p->c_out, p->c_in, sh.ldw);
   r.dz = p->act != CONV_ACT_IDENTITY;
-  if (r.dz) {
-    r.ldz = round8(p->c_out);
-    r.dz_off = l.take(static_cast<size_t>(p->rows) * r.ldz * elem_size(p->dtype));
-  } else {
-    r.dy = l.copy(dt, mode.copies, p->rows, p->c_out, sh.ldy);
-    r.ldz = r.dy.ld;
-  }
+  // dz as it is written (or dy, which stands for it), then as the products read it
+  r.dz_planes = tc && p->dtype == CONV_F32;
+  r.ldz = r.dz ? round8(p->c_out) : sh.ldy;
+  if (r.dz) r.dz_off = l.take(static_cast<size_t>(p->rows) * r.ldz * (r.dz_planes ? 6 : elem_size(p->dtype)));
+  else r.z = l.copy(tc, p->dtype, mode.copies, p->rows, p->c_out, r.ldz);
+  const long long ldz = r.dz ? r.ldz : r.z.ld;
   if (p->rows > 0) {
     r.col_blocks = dense_col_blocks(p->rows, p->c_out, sm);
     r.col_off = l.take(static_cast<size_t>(r.col_blocks) * p->c_out * sizeof(float));
-    r.dx = make_gemm(p->rows, p->c_in, p->c_out, 0, 1, r.ldz, r.w.ld);
+    r.dx = make_gemm(p->rows, p->c_in, p->c_out, 0, 1, ldz, r.w.ld);
     r.dx.epi.ldy = p->c_in;
-    r.pdx = plan_product(r.dx, mode.tc, false, sm);
-    r.dw = make_gemm(p->c_out, p->c_in, p->rows, 1, 1, r.ldz, r.x.ld);
+    r.pdx = plan_product(r.dx, p->dtype, mode.tc, false, sm);
+    r.dw = make_gemm(p->c_out, p->c_in, p->rows, 1, 1, ldz, r.x.ld);
     r.dw.epi.ldy = p->c_in;
-    r.pdw = plan_product(r.dw, mode.tc, false, sm);
+    r.pdw = plan_product(r.dw, p->dtype, mode.tc, false, sm);
   }
   r.part_off = l.take(std::max(r.pdx.part_bytes, r.pdw.part_bytes));
   r.total = l.total;
@@ -292,7 +299,7 @@ auto plan_for(uint32_t flags, int dtype, std::initializer_list<const void*> oper
   Mode m = mode_of(flags, dtype);
   bool all = true;
   for (const void* p : operands) all = all && aligned16(p);
-  if (m.tc && !all && !m.copies) {
+  if (m.tc && dtype != CONV_F32 && !all && !m.copies) {
     m.copies = true;
     auto r = plan(m);
     if (r.total <= have) return r;
@@ -308,7 +315,7 @@ auto plan_for(uint32_t flags, int dtype, std::initializer_list<const void*> oper
 
 // ---- gated ------------------------------------------------------------------
 struct GatedPlan {
-  Copy x, wg, wu, wd, dy;
+  Copy x, wg, wu, wd, dy, h, dg, du;
   DenseGemm up, down;                 // forward
   DenseGemm dh, dx, dwgu, dwd;        // backward
   Product pup, pdown, pdh, pdx, pdwgu, pdwd;
@@ -331,23 +338,24 @@ GatedSaved gated_saved(const conv_gated_problem* p, const GatedShape& sh) {
 GatedPlan plan_gated(const conv_gated_problem* p, const GatedShape& sh, const Mode& mode, int sm, bool saved) {
   GatedPlan r = {};
   Layout l;
-  const bool few = mode.few && few_rows(p->rows, p->dtype);
-  const int dt = mode.tc && !few ? p->dtype : CONV_F32;
-  r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
-  r.wg = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
-  r.wu = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
-  r.wd = l.copy(dt, mode.copies, p->c_out, p->hidden, p->hidden);
+  const bool few = mode.few && few_rows(p->rows);
+  const bool tc = mode.tc && !few;
+  r.x = l.copy(tc, p->dtype, mode.copies, p->rows, p->c_in, sh.ldx);
+  r.wg = l.copy(tc, p->dtype, mode.copies, p->hidden, p->c_in, p->c_in);
+  r.wu = l.copy(tc, p->dtype, mode.copies, p->hidden, p->c_in, p->c_in);
+  r.wd = l.copy(tc, p->dtype, mode.copies, p->c_out, p->hidden, p->hidden);
   if (!saved) r.h_off = l.take(static_cast<size_t>(p->rows) * sh.ldh * elem_size(p->dtype));
+  r.h = l.copy(tc, p->dtype, false, p->rows, p->hidden, sh.ldh);
   if (p->rows > 0) {
     r.up = make_gemm(p->rows, p->hidden, p->c_in, 0, 0, r.x.ld, r.wg.ld);
     r.up.dual = 1;
     r.up.epi.mode = EPI_GATED;
     r.up.epi.act = p->act; r.up.epi.alpha = p->act_alpha; r.up.epi.beta = p->act_beta;
     r.up.epi.ldy = sh.ldh; r.up.epi.ldp = sh.ldh;
-    r.pup = plan_product(r.up, mode.tc, few, sm);
-    r.down = make_gemm(p->rows, p->c_out, p->hidden, 0, 0, sh.ldh, r.wd.ld);
+    r.pup = plan_product(r.up, p->dtype, mode.tc, few, sm);
+    r.down = make_gemm(p->rows, p->c_out, p->hidden, 0, 0, r.h.ld, r.wd.ld);
     r.down.epi.ldr = sh.ldr; r.down.epi.ldy = sh.ldy;
-    r.pdown = plan_product(r.down, mode.tc, few, sm);
+    r.pdown = plan_product(r.down, p->dtype, mode.tc, few, sm);
   }
   r.part_off = l.take(std::max(r.pup.part_bytes, r.pdown.part_bytes));
   r.total = l.total;
@@ -357,32 +365,35 @@ GatedPlan plan_gated(const conv_gated_problem* p, const GatedShape& sh, const Mo
 GatedPlan plan_gated_backward(const conv_gated_problem* p, const GatedShape& sh, const Mode& mode, int sm) {
   GatedPlan r = {};
   Layout l;
-  const int dt = mode.tc ? p->dtype : CONV_F32;
-  r.x = l.copy(dt, mode.copies, p->rows, p->c_in, sh.ldx);
-  r.wg = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
-  r.wu = l.copy(dt, mode.copies, p->hidden, p->c_in, p->c_in);
-  r.wd = l.copy(dt, mode.copies, p->c_out, p->hidden, p->hidden);
-  r.dy = l.copy(dt, mode.copies, p->rows, p->c_out, sh.ldy);
+  const bool tc = mode.tc;
+  r.x = l.copy(tc, p->dtype, mode.copies, p->rows, p->c_in, sh.ldx);
+  r.wg = l.copy(tc, p->dtype, mode.copies, p->hidden, p->c_in, p->c_in);
+  r.wu = l.copy(tc, p->dtype, mode.copies, p->hidden, p->c_in, p->c_in);
+  r.wd = l.copy(tc, p->dtype, mode.copies, p->c_out, p->hidden, p->hidden);
+  r.dy = l.copy(tc, p->dtype, mode.copies, p->rows, p->c_out, sh.ldy);
   const size_t n = static_cast<size_t>(p->rows) * sh.ldh * elem_size(p->dtype);
   r.dg_off = l.take(n);
   r.du_off = l.take(n);
+  r.dg = l.copy(tc, p->dtype, false, p->rows, p->hidden, sh.ldh);
+  r.du = l.copy(tc, p->dtype, false, p->rows, p->hidden, sh.ldh);
+  r.h = l.copy(tc, p->dtype, false, p->rows, p->hidden, sh.ldh);
   if (p->rows > 0) {
     r.dh = make_gemm(p->rows, p->hidden, p->c_out, 0, 1, r.dy.ld, r.wd.ld);
     r.dh.epi.mode = EPI_GATED_BWD;
     r.dh.epi.act = p->act; r.dh.epi.alpha = p->act_alpha; r.dh.epi.beta = p->act_beta;
     r.dh.epi.ldy = sh.ldh; r.dh.epi.ldp = sh.ldh;
-    r.pdh = plan_product(r.dh, mode.tc, false, sm);
-    r.dx = make_gemm(p->rows, p->c_in, p->hidden, 0, 1, sh.ldh, r.wg.ld);
+    r.pdh = plan_product(r.dh, p->dtype, mode.tc, false, sm);
+    r.dx = make_gemm(p->rows, p->c_in, p->hidden, 0, 1, r.dg.ld, r.wg.ld);
     r.dx.segs = 2;
     r.dx.epi.ldy = p->c_in;
-    r.pdx = plan_product(r.dx, mode.tc, false, sm);
-    r.dwgu = make_gemm(p->hidden, p->c_in, p->rows, 1, 1, sh.ldh, r.x.ld);
+    r.pdx = plan_product(r.dx, p->dtype, mode.tc, false, sm);
+    r.dwgu = make_gemm(p->hidden, p->c_in, p->rows, 1, 1, r.dg.ld, r.x.ld);
     r.dwgu.batch = 2;
     r.dwgu.epi.ldy = p->c_in;
-    r.pdwgu = plan_product(r.dwgu, mode.tc, false, sm);
-    r.dwd = make_gemm(p->c_out, p->hidden, p->rows, 1, 1, r.dy.ld, sh.ldh);
+    r.pdwgu = plan_product(r.dwgu, p->dtype, mode.tc, false, sm);
+    r.dwd = make_gemm(p->c_out, p->hidden, p->rows, 1, 1, r.dy.ld, r.h.ld);
     r.dwd.epi.ldy = p->hidden;
-    r.pdwd = plan_product(r.dwd, mode.tc, false, sm);
+    r.pdwd = plan_product(r.dwd, p->dtype, mode.tc, false, sm);
   }
   r.part_off = l.take(std::max({r.pdh.part_bytes, r.pdx.part_bytes, r.pdwgu.part_bytes, r.pdwd.part_bytes}));
   r.total = l.total;
@@ -466,10 +477,10 @@ conv_status conv_linear_describe_plan(const conv_linear_problem* p, int32_t pass
   const Mode mode = mode_of(p->flags, p->dtype);
   if (pass == 0) {
     const LinearPlan r = plan_linear(p, sh, mode, sm_count);
-    describe_product(r.pfwd, r.fwd, sm_count, buf, len);
+    describe_product(r.pfwd, r.fwd, p->dtype == CONV_F32, sm_count, buf, len);
   } else {
     const LinearPlan r = plan_linear_backward(p, sh, mode, sm_count);
-    describe_product(pass == 1 ? r.pdx : r.pdw, pass == 1 ? r.dx : r.dw, sm_count, buf, len);
+    describe_product(pass == 1 ? r.pdx : r.pdw, pass == 1 ? r.dx : r.dw, p->dtype == CONV_F32, sm_count, buf, len);
   }
   return CONV_OK;
 }
@@ -502,8 +513,10 @@ conv_status conv_linear_forward(const conv_linear_problem* p, const void* x, con
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   char* base = static_cast<char*>(scratch);
   DenseGemm g = r.fwd;
-  CONV_TRY(resolve(r.x, x, base, &g.a[0], s));
-  CONV_TRY(resolve(r.w, w, base, &g.b[0], s));
+  Copies copies;
+  g.a[0] = copies.add(r.x, x, base);
+  g.b[0] = copies.add(r.w, w, base);
+  CONV_TRY(copies.enqueue(s));
   g.epi.bias = p->has_bias ? bias : nullptr;
   g.epi.residual = p->has_residual ? residual : nullptr;
   g.epi.y = y;
@@ -550,32 +563,37 @@ conv_status conv_linear_backward(const conv_linear_problem* p, const void* x, co
   if (ranges.clash()) return CONV_ERR_ALIAS;
   char* base = static_cast<char*>(scratch);
   const bool last = (p->flags & CONV_LINEAR_FLAG_RESIDUAL_LAST) != 0;
-  // dz, and its column sums
-  void* dz = r.dz && (dx || dw) ? base + r.dz_off : nullptr;
-  if (dz || dbias)
-    CONV_TRY(launch_dense_dz(dy, sh.ldy, pre, dz, r.ldz, dbias, reinterpret_cast<float*>(base + r.col_off), r.col_blocks,
-                             p->rows, p->c_out, p->act, p->act_alpha, p->act_beta, p->dtype, s));
+  // dz (as the products read it), and its column sums
+  const bool products = dx || dw;
+  Copies copies;
+  const void* z = nullptr;
+  if (products) z = r.dz ? base + r.dz_off : copies.add(r.z, dy, base);
+  const void* xc = dw ? copies.add(r.x, x, base) : nullptr;
+  const void* wc = dx ? copies.add(r.w, w, base) : nullptr;
+  CONV_TRY(copies.enqueue(s));
+  if ((products && r.dz) || dbias)
+    CONV_TRY(launch_dense_dz(dy, sh.ldy, pre, products && r.dz ? base + r.dz_off : nullptr, r.ldz, r.dz_planes, dbias,
+                             reinterpret_cast<float*>(base + r.col_off), r.col_blocks, p->rows, p->c_out, p->act,
+                             p->act_alpha, p->act_beta, p->dtype, s));
   if (dresidual) {
     if (act && !last)
-      CONV_TRY(launch_dense_dz(dy, sh.ldy, pre, dresidual, p->c_out, nullptr, nullptr, r.col_blocks, p->rows, p->c_out,
+      CONV_TRY(launch_dense_dz(dy, sh.ldy, pre, dresidual, p->c_out, false, nullptr, nullptr, r.col_blocks, p->rows, p->c_out,
                                p->act, p->act_alpha, p->act_beta, p->dtype, s));
     else
       CONV_TRY(cudaMemcpy2DAsync(dresidual, p->c_out * es, dy, sh.ldy * es, p->c_out * es, p->rows,
                                  cudaMemcpyDeviceToDevice, s));
   }
-  const void* z = dz;
-  if (!r.dz && (dx || dw)) CONV_TRY(resolve(r.dy, dy, base, &z, s));
   if (dx) {
     DenseGemm g = r.dx;
     g.a[0] = z;
-    CONV_TRY(resolve(r.w, w, base, &g.b[0], s));
+    g.b[0] = wc;
     g.epi.y = dx;
     CONV_TRY(launch_product(r.pdx, g, p->dtype, base + r.part_off, false, s));
   }
   if (dw) {
     DenseGemm g = r.dw;
     g.a[0] = z;
-    CONV_TRY(resolve(r.x, x, base, &g.b[0], s));
+    g.b[0] = xc;
     g.epi.y = dw;
     CONV_TRY(launch_product(r.pdw, g, p->dtype, base + r.part_off, false, s));
   }
@@ -644,9 +662,12 @@ conv_status conv_gated_forward(const conv_gated_problem* p, const void* x, const
   char* kept = static_cast<char*>(saved);
   void* h = saved ? kept + keep.h_off : base + r.h_off;
   DenseGemm g = r.up;
-  CONV_TRY(resolve(r.x, x, base, &g.a[0], s));
-  CONV_TRY(resolve(r.wg, w_gate, base, &g.b[0], s));
-  CONV_TRY(resolve(r.wu, w_up, base, &g.b[1], s));
+  Copies copies, hidden;
+  g.a[0] = copies.add(r.x, x, base);
+  g.b[0] = copies.add(r.wg, w_gate, base);
+  g.b[1] = copies.add(r.wu, w_up, base);
+  const void* down = copies.add(r.wd, w_down, base);
+  CONV_TRY(copies.enqueue(s));
   g.epi.y = h;
   if (saved) {
     g.epi.pre = reinterpret_cast<float*>(kept + keep.g_off);
@@ -654,11 +675,12 @@ conv_status conv_gated_forward(const conv_gated_problem* p, const void* x, const
   }
   CONV_TRY(launch_product(r.pup, g, p->dtype, base + r.part_off, false, s));
   g = r.down;
-  g.a[0] = h;
-  CONV_TRY(resolve(r.wd, w_down, base, &g.b[0], s));
+  g.a[0] = hidden.add(r.h, h, base);
+  CONV_TRY(hidden.enqueue(s));
+  g.b[0] = down;
   g.epi.residual = p->has_residual ? residual : nullptr;
   g.epi.y = y;
-  CONV_TRY(launch_product(r.pdown, g, p->dtype, base + r.part_off, !r.wd.on, s));
+  CONV_TRY(launch_product(r.pdown, g, p->dtype, base + r.part_off, true, s));
   return CONV_OK;
 }
 
@@ -712,34 +734,43 @@ conv_status conv_gated_backward(const conv_gated_problem* p, const void* x, cons
   char* base = static_cast<char*>(scratch);
   const char* kept = static_cast<const char*>(saved);
   void* part = base + r.part_off;
-  const void* dyc = dy;
-  CONV_TRY(resolve(r.dy, dy, base, &dyc, s));
+  Copies copies, grads;
+  const void* dyc = copies.add(r.dy, dy, base);
+  const void* wdc = dgu ? copies.add(r.wd, w_down, base) : nullptr;
+  const void* wgc = dx ? copies.add(r.wg, w_gate, base) : nullptr;
+  const void* wuc = dx ? copies.add(r.wu, w_up, base) : nullptr;
+  const void* xc = dwgu ? copies.add(r.x, x, base) : nullptr;
+  const void* hc = dw_down ? copies.add(r.h, kept + keep.h_off, base) : nullptr;
+  CONV_TRY(copies.enqueue(s));
+  const void *dg = nullptr, *du = nullptr;
   if (dgu) {
     DenseGemm g = r.dh;
     g.a[0] = dyc;
-    CONV_TRY(resolve(r.wd, w_down, base, &g.b[0], s));
+    g.b[0] = wdc;
     g.epi.pre = reinterpret_cast<float*>(const_cast<char*>(kept + keep.g_off));
     g.epi.pre2 = reinterpret_cast<float*>(const_cast<char*>(kept + keep.u_off));
     g.epi.y = base + r.dg_off;
     g.epi.y2 = base + r.du_off;
     CONV_TRY(launch_product(r.pdh, g, p->dtype, part, false, s));
+    dg = grads.add(r.dg, base + r.dg_off, base);
+    du = grads.add(r.du, base + r.du_off, base);
+    CONV_TRY(grads.enqueue(s));
   }
   if (dx) {
     DenseGemm g = r.dx;
-    g.a[0] = base + r.dg_off;
-    g.a[1] = base + r.du_off;
-    CONV_TRY(resolve(r.wg, w_gate, base, &g.b[0], s));
-    CONV_TRY(resolve(r.wu, w_up, base, &g.b[1], s));
+    g.a[0] = dg;
+    g.a[1] = du;
+    g.b[0] = wgc;
+    g.b[1] = wuc;
     g.epi.y = dx;
     CONV_TRY(launch_product(r.pdx, g, p->dtype, part, false, s));
   }
   if (dwgu) {
     DenseGemm g = r.dwgu;
     Product q = r.pdwgu;
-    CONV_TRY(resolve(r.x, x, base, &g.b[0], s));
-    g.b[1] = g.b[0];
-    g.a[0] = base + r.dg_off;
-    g.a[1] = base + r.du_off;
+    g.b[0] = g.b[1] = xc;
+    g.a[0] = dg;
+    g.a[1] = du;
     g.epi.y = dw_gate;
     g.epi.y2 = dw_up;
     if (!dw_gate || !dw_up) {  // one of the two: its planes fit where both would
@@ -751,7 +782,7 @@ conv_status conv_gated_backward(const conv_gated_problem* p, const void* x, cons
   if (dw_down) {
     DenseGemm g = r.dwd;
     g.a[0] = dyc;
-    g.b[0] = kept + keep.h_off;
+    g.b[0] = hc;
     g.epi.y = dw_down;
     CONV_TRY(launch_product(r.pdwd, g, p->dtype, part, false, s));
   }

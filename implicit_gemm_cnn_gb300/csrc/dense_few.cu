@@ -24,9 +24,6 @@ constexpr int kWarps = 8;
 constexpr int kThreads = 32 * kWarps;
 constexpr int kOuts = 16;   // output features of a block
 
-__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
-__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
-
 // 16 bytes read once.
 __device__ __forceinline__ uint4 load_once(const void* p) {
   uint4 r;
@@ -87,7 +84,7 @@ __device__ __forceinline__ void finish(const DenseGemm& g, const float* red, int
 
 // NB: 8-row groups of x (1 or 2).  A piece is 32 * CH terms.
 template <typename T, int NB, bool DUAL, bool VEC>
-__global__ void __launch_bounds__(kThreads, 2) few_mma(const DenseGemm g) {
+__global__ void __launch_bounds__(kThreads, 2) few_mma(const DenseGemm g, const int early) {
   constexpr int P = DUAL ? 2 : 1;
   constexpr int CH = DUAL ? 2 : 4;
   __shared__ float red[P * kWarps * kOuts * NB * 8];
@@ -127,8 +124,10 @@ __global__ void __launch_bounds__(kThreads, 2) few_mma(const DenseGemm g) {
   };
   const long long piece = 32 * CH, step = piece * kWarps;
   long long k = warp * piece;
+  // `early`: the kernel before is the same call's, whose output x is and the weights are not
+  if (!early) griddep_wait();
   if (k < K) load_w(cur, k);
-  griddep_wait();    // (the weights are no other kernel's output; x may be the kernel before's)
+  griddep_wait();
   griddep_launch();
   for (; k < K; k += step) {
     if (k + step < K) load_w(next, k + step);
@@ -165,9 +164,10 @@ __global__ void __launch_bounds__(kThreads, 2) few_mma(const DenseGemm g) {
 // float32: a warp multiplies pieces of 128 terms (four per lane) of the block's outputs with every row.  ROWS: rows
 // compiled for (at least g.M).  Outputs are taken OG at a time, so that their sums stay in registers.
 template <int ROWS, bool DUAL, bool VEC>
-__global__ void __launch_bounds__(kThreads) few_f32(const DenseGemm g) {
+__global__ void __launch_bounds__(kThreads) few_f32(const DenseGemm g, const int early) {
+  (void)early;
   constexpr int P = DUAL ? 2 : 1;
-  constexpr int OG = 8 / P;
+  constexpr int OG = (ROWS > 8 ? 4 : 8) / P;
   __shared__ float red[P * kWarps * kOuts * ROWS];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32;
   const int n0 = blockIdx.x * kOuts;
@@ -226,16 +226,8 @@ __global__ void __launch_bounds__(kThreads) few_f32(const DenseGemm g) {
 
 template <typename K>
 cudaError_t start(K kern, const DenseGemm& g, bool follows, cudaStream_t s) {
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>((g.N + kOuts - 1) / kOuts));
-  cfg.blockDim = dim3(kThreads);
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = follows ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, g);
+  return launch_overlapped(kern, dim3(static_cast<unsigned>((g.N + kOuts - 1) / kOuts)), kThreads, 0, 1, s, g,
+                           follows ? 1 : 0);
 }
 template <typename T, bool DUAL>
 cudaError_t go16(const DenseGemm& g, bool vec, bool follows, cudaStream_t s) {
@@ -260,7 +252,8 @@ cudaError_t launch_dense_few(const DenseGemm& g, int dtype, bool follows, cudaSt
     return g.dual ? go16<__nv_bfloat16, true>(g, vec, follows, s) : go16<__nv_bfloat16, false>(g, vec, follows, s);
   if (g.M <= 1) return g.dual ? go32<1, true>(g, vec, follows, s) : go32<1, false>(g, vec, follows, s);
   if (g.M <= 4) return g.dual ? go32<4, true>(g, vec, follows, s) : go32<4, false>(g, vec, follows, s);
-  return g.dual ? go32<8, true>(g, vec, follows, s) : go32<8, false>(g, vec, follows, s);
+  if (g.M <= 8) return g.dual ? go32<8, true>(g, vec, follows, s) : go32<8, false>(g, vec, follows, s);
+  return g.dual ? go32<16, true>(g, vec, follows, s) : go32<16, false>(g, vec, follows, s);
 }
 
 }  // namespace conv

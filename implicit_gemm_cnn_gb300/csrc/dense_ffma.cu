@@ -59,6 +59,8 @@ template <typename T, int BM, int BN, bool DUAL>
 __global__ void __launch_bounds__(kThreads, BM * BN >= 128 * 128 ? 1 : 2) dense_ffma(const DenseGemm g) {
   constexpr int TM = BM / 16, TN = BN / 16;
   constexpr int BNL = DUAL ? BN / 2 : BN;  // columns of the output tile
+  griddep_wait();
+  griddep_launch();
   __shared__ float As[2][kBK][BM + 4];
   __shared__ float Bs[2][kBK][BN + 4];
   const int tid = threadIdx.x, tx = tid % 16, ty = tid / 16;
@@ -166,6 +168,8 @@ __global__ void __launch_bounds__(kThreads, BM * BN >= 128 * 128 ? 1 : 2) dense_
 // y[m][n] from the planes of the k ranges: four columns per thread.
 template <typename T>
 __global__ void __launch_bounds__(256) dense_reduce(const DenseGemm g) {
+  griddep_wait();
+  griddep_launch();
   const long long quads = (static_cast<long long>(g.N) + 3) / 4;
   const long long idx = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (idx >= quads * g.M) return;
@@ -201,19 +205,78 @@ __global__ void __launch_bounds__(256) dense_reduce(const DenseGemm g) {
   dense_epilogue<T, 4>(g.epi, which, m, col, ok, v, u);
 }
 
-__global__ void __launch_bounds__(256) dense_repack(const uint16_t* in, long long ld_in, uint16_t* out, long long ld_out,
-                                                    long long rows, long long cols) {
-  // a warp copies 256 columns of a row at a time
-  const long long chunks = (cols + 255) / 256;
-  const long long warp = (static_cast<long long>(blockIdx.x) * 256 + threadIdx.x) / 32;
-  const long long warps = static_cast<long long>(gridDim.x) * 8;
-  const int lane = threadIdx.x % 32;
-  for (long long w = warp; w < rows * chunks; w += warps) {
-    const long long r = w / chunks, c0 = w % chunks * 256;
+// The three planes of 4 values: v = p0 + p1 + p2, exactly (for |v| above 2^-110; below, to 2^-133).  An infinity or a
+// NaN is its own first plane; a value that would round up to infinity is cut instead.
+__device__ __forceinline__ void put_planes(const float (&v)[4], __nv_bfloat16* out, long long plane) {
+  uint16_t h[3][4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const long long c = c0 + i * 32 + lane;
-      if (c < cols) out[r * ld_out + c] = in[r * ld_in + c];
+  for (int j = 0; j < 4; ++j) {
+    __nv_bfloat16 p0 = __float2bfloat16_rn(v[j]);
+    const bool finite = fabsf(v[j]) <= 3.402823466e38f;
+    if (finite && __hisinf(p0)) p0 = __float2bfloat16_rz(v[j]);
+    const float r1 = finite ? v[j] - __bfloat162float(p0) : 0.0f;
+    const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
+    const __nv_bfloat16 p2 = __float2bfloat16_rn(r1 - __bfloat162float(p1));
+    h[0][j] = __bfloat16_as_ushort(p0);
+    h[1][j] = __bfloat16_as_ushort(p1);
+    h[2][j] = __bfloat16_as_ushort(p2);
+  }
+#pragma unroll
+  for (int q = 0; q < 3; ++q)
+    *reinterpret_cast<uint2*>(out + q * plane) =
+        make_uint2(h[q][0] | (static_cast<uint32_t>(h[q][1]) << 16), h[q][2] | (static_cast<uint32_t>(h[q][3]) << 16));
+}
+
+// A warp takes 256 columns of a row at a time: 16-bit rows as they are, or float32 rows as three planes (rows of the
+// planes are a multiple of 8 long, so whole groups of four are written).  Blocks walk over the jobs' pieces together.
+struct CopyJobs {
+  CopyJob job[kCopyJobs];
+  long long first[kCopyJobs + 1];
+  int count;
+};
+template <bool PLANES>
+__global__ void __launch_bounds__(256) dense_copies(const __grid_constant__ CopyJobs c) {
+  griddep_wait();
+  griddep_launch();
+  const int lane = threadIdx.x % 32;
+  const long long warps = static_cast<long long>(gridDim.x) * 8;
+  int j = 0;
+  for (long long w = static_cast<long long>(blockIdx.x) * 8 + threadIdx.x / 32; w < c.first[c.count]; w += warps) {
+    while (w >= c.first[j + 1]) ++j;
+    const CopyJob& job = c.job[j];
+    const long long chunks = (job.cols + 255) / 256, i = w - c.first[j];
+    const long long r = i / chunks, c0 = i % chunks * 256;
+    if constexpr (PLANES) {
+      const float* src = static_cast<const float*>(job.in) + r * job.ld_in;
+      __nv_bfloat16* dst = static_cast<__nv_bfloat16*>(job.out) + r * job.ld;
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const long long col = c0 + h * 128 + lane * 4;
+        if (col >= job.cols) continue;
+        float v[4];
+        if (col + 4 <= job.cols && reinterpret_cast<uintptr_t>(src + col) % 16 == 0) {
+          const float4 f = *reinterpret_cast<const float4*>(src + col);
+          v[0] = f.x; v[1] = f.y; v[2] = f.z; v[3] = f.w;
+        } else {
+#pragma unroll
+          for (int k = 0; k < 4; ++k) v[k] = col + k < job.cols ? src[col + k] : 0.0f;
+        }
+        put_planes(v, dst + col, job.rows * job.ld);
+      }
+    } else {
+      const uint16_t* src = static_cast<const uint16_t*>(job.in) + r * job.ld_in;
+      uint16_t* dst = static_cast<uint16_t*>(job.out) + r * job.ld;
+      uint16_t v[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const long long col = c0 + k * 32 + lane;
+        v[k] = col < job.cols ? src[col] : 0;
+      }
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const long long col = c0 + k * 32 + lane;
+        if (col < job.cols) dst[col] = v[k];
+      }
     }
   }
 }
@@ -221,12 +284,14 @@ __global__ void __launch_bounds__(256) dense_repack(const uint16_t* in, long lon
 // dz and the column sums of a row block, bound by the bytes (dy, pre in; dz out).  A warp takes 32 * V columns of every
 // eighth row of the block (V columns per lane: 16 bytes of 16-bit values, or of float32), two rows in flight; the
 // eight warps' partial sums are added in order.  VEC: every row of dy, pre and dz begins on a 16-byte boundary.
-template <typename T, bool VEC>
-__global__ void __launch_bounds__(256, 3) dense_dz(const T* dy, long long ld_dy, const float* pre, T* dz, long long ld_dz,
-                                                float* part, int rows_per_block, long long rows, long long cols,
+template <typename T, bool VEC, bool PLANES>
+__global__ void __launch_bounds__(256, 3) dense_dz(const T* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz,
+                                                   float* part, int rows_per_block, long long rows, long long cols,
                                                 int act, float alpha, float beta) {
   constexpr bool FAST = sizeof(T) == 2;
-  constexpr int V = VEC ? 16 / sizeof(T) : 2;
+  constexpr int V = VEC ? 16 / sizeof(T) : PLANES ? 4 : 2;
+  griddep_wait();
+  griddep_launch();
   constexpr int U = 2;
   __shared__ float sums[8][32 * V];
   const int tx = threadIdx.x % 32, ty = threadIdx.x / 32;
@@ -280,11 +345,13 @@ __global__ void __launch_bounds__(256, 3) dense_dz(const T* dy, long long ld_dy,
 #pragma unroll
         for (int j = 0; j < V; ++j) v[j] = j < n ? v[j] * d[j] : 0.0f;
       }
-      if (dz) {
+      if constexpr (PLANES) {
+        if (dz && n > 0) put_planes(v, static_cast<__nv_bfloat16*>(dz) + row * ld_dz + c, rows * ld_dz);
+      } else if (dz) {
         T out[V];
 #pragma unroll
         for (int j = 0; j < V; ++j) out[j] = from_f32<T>(v[j]);
-        T* dst = dz + row * ld_dz + c;
+        T* dst = static_cast<T*>(dz) + row * ld_dz + c;
         if (wide) {
           if constexpr (VEC) *reinterpret_cast<uint4*>(dst) = *reinterpret_cast<const uint4*>(out);
         } else {
@@ -311,6 +378,8 @@ __global__ void __launch_bounds__(256, 3) dense_dz(const T* dy, long long ld_dy,
 }
 template <typename T>
 __global__ void __launch_bounds__(256) dense_colsum(const float* part, T* out, int blocks, long long cols) {
+  griddep_wait();
+  griddep_launch();
   const long long c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (c >= cols) return;
   float s = 0.0f;
@@ -323,8 +392,7 @@ cudaError_t go(const DenseGemm& g, cudaStream_t s) {
   const int bnl = DUAL ? BN / 2 : BN;
   const dim3 grid(static_cast<unsigned>(((g.N + bnl - 1LL) / bnl) * ((g.M + BM - 1LL) / BM)), 1,
                   static_cast<unsigned>((DUAL ? 1 : g.batch) * g.split));
-  dense_ffma<T, BM, BN, DUAL><<<grid, kThreads, 0, s>>>(g);
-  return cudaGetLastError();
+  return launch_overlapped(dense_ffma<T, BM, BN, DUAL>, grid, kThreads, 0, 1, s, g);
 }
 template <typename T>
 cudaError_t by_tile(const DenseFfmaPlan& p, const DenseGemm& g, cudaStream_t s) {
@@ -333,21 +401,22 @@ cudaError_t by_tile(const DenseFfmaPlan& p, const DenseGemm& g, cudaStream_t s) 
 }
 
 template <typename T>
-cudaError_t dz_go(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, void* dbias, float* part,
-                  int blocks, long long rows, long long cols, int act, float alpha, float beta, cudaStream_t s) {
+cudaError_t dz_go(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, bool planes, void* dbias,
+                  float* part, int blocks, long long rows, long long cols, int act, float alpha, float beta, cudaStream_t s) {
   const int per = static_cast<int>((rows + blocks - 1) / blocks);
   auto on16 = [](const void* p, long long bytes) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && bytes % 16 == 0; };
-  const bool vec = on16(dy, ld_dy * sizeof(T)) && on16(pre, cols * 4) && on16(dz, ld_dz * sizeof(T));
-  const long long strip = 32 * (vec ? 16 / static_cast<long long>(sizeof(T)) : 2);
+  const bool vec = on16(dy, ld_dy * sizeof(T)) && on16(pre, cols * 4) && (planes || on16(dz, ld_dz * sizeof(T)));
+  const long long strip = 32 * (vec ? 16 / static_cast<long long>(sizeof(T)) : planes ? 4 : 2);
   const dim3 grid(static_cast<unsigned>((cols + strip - 1) / strip), static_cast<unsigned>((rows + per - 1) / per));
-  auto kern = vec ? dense_dz<T, true> : dense_dz<T, false>;
-  kern<<<grid, 256, 0, s>>>(static_cast<const T*>(dy), ld_dy, pre, static_cast<T*>(dz), ld_dz, dbias ? part : nullptr, per,
-                            rows, cols, act, alpha, beta);
-  cudaError_t err = cudaGetLastError();
+  auto kern = vec ? dense_dz<T, true, false> : dense_dz<T, false, false>;
+  if constexpr (sizeof(T) == 4) {
+    if (planes) kern = vec ? dense_dz<T, true, true> : dense_dz<T, false, true>;
+  }
+  cudaError_t err = launch_overlapped(kern, grid, 256, 0, 1, s, static_cast<const T*>(dy), ld_dy, pre, dz, ld_dz,
+                                      dbias ? part : nullptr, per, rows, cols, act, alpha, beta);
   if (err != cudaSuccess || !dbias) return err;
-  dense_colsum<T><<<static_cast<unsigned>((cols + 255) / 256), 256, 0, s>>>(part, static_cast<T*>(dbias),
-                                                                         static_cast<int>(grid.y), cols);
-  return cudaGetLastError();
+  return launch_overlapped(dense_colsum<T>, dim3(static_cast<unsigned>((cols + 255) / 256)), 256, 0, 1, s, part,
+                           static_cast<T*>(dbias), static_cast<int>(grid.y), cols);
 }
 
 }  // namespace
@@ -384,20 +453,22 @@ cudaError_t launch_dense_reduce(const DenseGemm& g, int dtype, cudaStream_t s) {
   const long long quads = (static_cast<long long>(g.N) + 3) / 4 * g.M;
   const dim3 grid(static_cast<unsigned>((quads + 255) / 256), static_cast<unsigned>(g.dual ? 1 : g.batch));
   switch (dtype) {
-    case CONV_F32: dense_reduce<float><<<grid, 256, 0, s>>>(g); break;
-    case CONV_F16: dense_reduce<__half><<<grid, 256, 0, s>>>(g); break;
-    default: dense_reduce<__nv_bfloat16><<<grid, 256, 0, s>>>(g); break;
+    case CONV_F32: return launch_overlapped(dense_reduce<float>, grid, 256, 0, 1, s, g);
+    case CONV_F16: return launch_overlapped(dense_reduce<__half>, grid, 256, 0, 1, s, g);
+    default: return launch_overlapped(dense_reduce<__nv_bfloat16>, grid, 256, 0, 1, s, g);
   }
-  return cudaGetLastError();
 }
 
-cudaError_t launch_dense_repack(const void* in, long long ld_in, void* out, long long ld_out, long long rows,
-                                long long cols, cudaStream_t s) {
-  const long long warps = rows * ((cols + 255) / 256);
-  const unsigned blocks = static_cast<unsigned>(std::min<long long>((warps + 7) / 8, 1 << 16));
-  dense_repack<<<blocks, 256, 0, s>>>(static_cast<const uint16_t*>(in), ld_in, static_cast<uint16_t*>(out), ld_out, rows,
-                                      cols);
-  return cudaGetLastError();
+cudaError_t launch_dense_copies(const CopyJob* jobs, int count, bool planes, cudaStream_t s) {
+  if (count == 0) return cudaSuccess;
+  CopyJobs c = {};
+  c.count = count;
+  for (int i = 0; i < count; ++i) {
+    c.job[i] = jobs[i];
+    c.first[i + 1] = c.first[i] + jobs[i].rows * ((jobs[i].cols + 255) / 256);
+  }
+  const unsigned blocks = static_cast<unsigned>(std::min<long long>((c.first[count] + 7) / 8, 1 << 14));
+  return launch_overlapped(planes ? dense_copies<true> : dense_copies<false>, dim3(blocks), 256, 0, 1, s, c);
 }
 
 int dense_col_blocks(long long rows, long long cols, int sm) {
@@ -407,15 +478,11 @@ int dense_col_blocks(long long rows, long long cols, int sm) {
   return static_cast<int>(std::max<long long>(1, std::min<long long>({want, (rows + kColRowsMin - 1) / kColRowsMin, 65535})));
 }
 
-cudaError_t launch_dense_dz(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, void* dbias,
-                            float* part, int blocks, long long rows, long long cols, int act, float alpha, float beta,
-                            int dtype, cudaStream_t s) {
-  switch (dtype) {
-    case CONV_F32: return dz_go<float>(dy, ld_dy, pre, dz, ld_dz, dbias, part, blocks, rows, cols, act, alpha, beta, s);
-    case CONV_F16: return dz_go<__half>(dy, ld_dy, pre, dz, ld_dz, dbias, part, blocks, rows, cols, act, alpha, beta, s);
-    default:
-      return dz_go<__nv_bfloat16>(dy, ld_dy, pre, dz, ld_dz, dbias, part, blocks, rows, cols, act, alpha, beta, s);
-  }
+cudaError_t launch_dense_dz(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, bool planes,
+                            void* dbias, float* part, int blocks, long long rows, long long cols, int act, float alpha,
+                            float beta, int dtype, cudaStream_t s) {
+  auto go = dtype == CONV_F32 ? dz_go<float> : dtype == CONV_F16 ? dz_go<__half> : dz_go<__nv_bfloat16>;
+  return go(dy, ld_dy, pre, dz, ld_dz, planes, dbias, part, blocks, rows, cols, act, alpha, beta, s);
 }
 
 }  // namespace conv

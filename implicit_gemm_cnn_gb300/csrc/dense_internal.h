@@ -8,6 +8,32 @@
 
 namespace conv {
 
+// Programmatic dependent launch: a kernel's start (its set-up, before
+// griddep_wait) overlaps the end of the kernel before it in the stream.  Every
+// dense kernel calls griddep_wait before it touches memory that another kernel
+// writes or reads, so any kernel may stand before it.
+__device__ __forceinline__ void griddep_wait() { asm volatile("griddepcontrol.wait;\n" ::: "memory"); }
+__device__ __forceinline__ void griddep_launch() { asm volatile("griddepcontrol.launch_dependents;\n" ::: "memory"); }
+template <typename... P, typename... A>
+cudaError_t launch_overlapped(void (*kern)(P...), dim3 grid, int threads, size_t smem, int cluster, cudaStream_t s,
+                              A&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(static_cast<unsigned>(threads));
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kern, static_cast<P>(args)...);
+}
+
 // CUDA-core product (dense_ffma.cu): any type, stride and alignment.
 struct DenseFfmaPlan {
   int bm, bn;            // tile
@@ -17,7 +43,8 @@ struct DenseFfmaPlan {
 DenseFfmaPlan dense_ffma_plan(const DenseGemm& g, int sm);
 cudaError_t launch_dense_ffma(const DenseFfmaPlan& p, const DenseGemm& g, int dtype, cudaStream_t s);
 
-// Tensor-core product (dense_tc.cuh): 16-bit operands on 16-byte boundaries.
+// Tensor-core product: 16-bit operands on 16-byte boundaries (dense_tc.cuh), or
+// the three bfloat16 planes of float32 ones (dense_tc32.cu).
 struct DenseTcPlan {
   int cg, nt;       // SMs per tile, MMA columns: tiles of 128 * cg x nt (nt / 2 gated)
   int split;        // k ranges
@@ -25,29 +52,36 @@ struct DenseTcPlan {
   long long tiles;
   int blocks;       // persistent blocks
 };
-DenseTcPlan dense_tc_plan(const DenseGemm& g, int sm);
+DenseTcPlan dense_tc_plan(const DenseGemm& g, int dtype, int sm);
 cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype, cudaStream_t s);
 cudaError_t dense_error_word(uint32_t* word, int reset);
 
-// Few rows (dense_few.cu): at most 16 (8 of float32), any alignment.  `follows`:
+// Few rows (dense_few.cu): at most 16, any alignment.  `follows`:
 // the kernel before in the stream is this call's own, and writes no weights: the
 // launch overlaps its end, the first weights' loads included.
-constexpr int dense_few_rows(int dtype) { return dtype == CONV_F32 ? 8 : 16; }
+constexpr int kFewRows = 16;
 cudaError_t launch_dense_few(const DenseGemm& g, int dtype, bool follows, cudaStream_t s);
 
 // Adds the k ranges' planes in order and applies the epilogue.
 cudaError_t launch_dense_reduce(const DenseGemm& g, int dtype, cudaStream_t s);
 
-// Rows copied to a pitch of `ld_out` elements (16-bit elements).
-cudaError_t launch_dense_repack(const void* in, long long ld_in, void* out, long long ld_out, long long rows,
-                                long long cols, cudaStream_t s);
+// Operands' copies, in one launch: 16-bit rows copied to a pitch of `ld`
+// elements, or (planes) the three bfloat16 planes of float32 rows, rows of ld (a
+// multiple of 8) elements, planes rows * ld elements apart.
+struct CopyJob {
+  const void* in;
+  void* out;
+  long long ld_in, ld, rows, cols;
+};
+constexpr int kCopyJobs = 6;
+cudaError_t launch_dense_copies(const CopyJob* jobs, int count, bool planes, cudaStream_t s);
 
-// dz = dy * act'(pre) in the element type (`dz`, may be nullptr: not wanted)
-// and float32 column sums of the unrounded dz over row blocks
+// dz = dy * act'(pre) in the element type (`dz`, may be nullptr: not wanted;
+// planes: as the three planes of CopyJob) and float32 column sums of the unrounded dz over row blocks
 // (part [blocks][cols]), summed in order into dbias by the second kernel.
 constexpr int kColRowsMin = 64;
 int dense_col_blocks(long long rows, long long cols, int sm);
-cudaError_t launch_dense_dz(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, void* dbias,
+cudaError_t launch_dense_dz(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, bool planes, void* dbias,
                             float* part, int blocks, long long rows, long long cols, int act, float alpha, float beta,
                             int dtype, cudaStream_t s);
 

@@ -16,6 +16,9 @@ cudaError_t launch_dense_tc_f16(const DenseTcPlan& t, int mode, int a_mn, int b_
 cudaError_t launch_dense_tc_bf16(const DenseTcPlan& t, int mode, int a_mn, int b_mn, const DenseTcArgs& args,
                                  const DenseTcMaps& maps, cudaStream_t s);
 
+cudaError_t launch_dense_tc32(int mode, int a_mn, int b_mn, const DenseTcArgs& args, const DenseTcMaps& maps, int blocks,
+                              cudaStream_t s);
+
 namespace {
 
 __device__ uint32_t g_dense_err;
@@ -84,6 +87,16 @@ bool encode_blocks(CUtensorMap* map, CUtensorMapDataType type, const void* base,
                    CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
+// Three bfloat16 planes of a matrix (rows * ld elements apart), boxes of 64 x box_rows of all three.
+bool encode_planes(CUtensorMap* map, const void* base, long long inner, long long rows, long long ld, int box_rows) {
+  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows), 3};
+  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, static_cast<cuuint64_t>(ld) * 2 * rows};
+  const cuuint32_t box[3] = {64, static_cast<cuuint32_t>(box_rows), 3};
+  const cuuint32_t step[3] = {1, 1, 1};
+  return encoder()(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, step,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 bool aligned(const void* p, long long ld, size_t es) {
   return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<long long>(es) % 16 == 0;
 }
@@ -92,15 +105,17 @@ bool aligned(const void* p, long long ld, size_t es) {
 // 1.85 GHz): 64 terms of a pair's tile take 165 + 1.73 nt (608 at nt = 256, 386 at 128: 512 and 256 are the MMAs
 // alone), of one SM's 128 columns 415 (its stage is as many bytes as the pair's of 256); a tile adds 600, a launch
 // 6000, the ranges' planes pass through L2 twice at some 3000 bytes a clock, with a launch of their own.
-DenseTcPlan search(const DenseGemm& g, int sm) {
+// float32 (dense_tc32.cu): one SM's tiles of 64 or 128 columns, six products; a stage of 64 terms takes the MMAs' 12 nt
+// clocks or its 16-byte rows' and hand-overs' 1000, whichever is more.
+DenseTcPlan search(const DenseGemm& g, int f32, int sm) {
   DenseTcPlan best = {};
   const int kb = static_cast<int>((static_cast<long long>(g.K) + dtc::kBK - 1) / dtc::kBK) * g.segs;
   const int products = dense_products(g);
   double best_t = 0.0;
-  for (int cg = 2; cg >= 1; --cg) {
+  for (int cg = f32 ? 1 : 2; cg >= 1; --cg) {
     const long long slots = sm / cg;
     for (int nt = cg == 2 ? 256 : 128; nt >= 64; nt -= 32) {
-      if (g.dual && nt % 64) continue;
+      if ((g.dual || f32) && nt % 64) continue;
       for (int split = 1; split <= 16; ++split) {
         if (split > 1 && kb / split < 4) break;
         // a gated product whose k is split runs as two products (its planes meet in the second launch)
@@ -111,7 +126,7 @@ DenseTcPlan search(const DenseGemm& g, int sm) {
         if ((kb + range - 1) / range != split) continue;  // every range holds terms
         const long long units = tiles * split;
         if (split > 1 && units > 2 * slots) break;
-        const double per = cg == 2 ? 165.0 + 1.73 * nt : 190.0 + 1.76 * nt;
+        const double per = f32 ? std::max(13.0 * nt, 1000.0) : cg == 2 ? 165.0 + 1.73 * nt : 190.0 + 1.76 * nt;
         double t = static_cast<double>((units + slots - 1) / slots) * (range * per + 600.0) + 6000.0;
         if (split > 1) t += 4000.0 + 2.0 * split * products * 4.0 * g.M * g.N / 3000.0;
         if (!best.cg || t < best_t) {
@@ -128,9 +143,10 @@ DenseTcPlan search(const DenseGemm& g, int sm) {
 
 // The plans of the shapes used last (a search takes microseconds, a small product too).
 struct PlanKey {
-  int M, N, K, segs, batch, dual, sm;
+  int M, N, K, segs, batch, dual, f32, sm;
   bool operator==(const PlanKey& o) const {
-    return M == o.M && N == o.N && K == o.K && segs == o.segs && batch == o.batch && dual == o.dual && sm == o.sm;
+    return M == o.M && N == o.N && K == o.K && segs == o.segs && batch == o.batch && dual == o.dual && f32 == o.f32 &&
+           sm == o.sm;
   }
 };
 std::mutex g_plan_mu;
@@ -141,16 +157,17 @@ struct {
 
 }  // namespace
 
-DenseTcPlan dense_tc_plan(const DenseGemm& g, int sm) {
-  const PlanKey key{g.M, g.N, g.K, g.segs, g.batch, g.dual, sm};
+DenseTcPlan dense_tc_plan(const DenseGemm& g, int dtype, int sm) {
+  const int f32 = dtype == CONV_F32;
+  const PlanKey key{g.M, g.N, g.K, g.segs, g.batch, g.dual, f32, sm};
   uint32_t h = 2166136261u;
-  for (int v : {key.M, key.N, key.K, key.segs, key.batch, key.dual}) h = (h ^ static_cast<uint32_t>(v)) * 16777619u;
+  for (int v : {key.M, key.N, key.K, key.segs, key.batch, key.dual, key.f32}) h = (h ^ static_cast<uint32_t>(v)) * 16777619u;
   auto& slot = g_plans[(h ^ (h >> 15)) % 256];
   {
     std::lock_guard<std::mutex> lock(g_plan_mu);
     if (slot.key == key) return slot.plan;  // (an empty slot's sm is 0)
   }
-  const DenseTcPlan plan = search(g, sm);
+  const DenseTcPlan plan = search(g, f32, sm);
   std::lock_guard<std::mutex> lock(g_plan_mu);
   slot.key = key;
   slot.plan = plan;
@@ -186,19 +203,23 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
   p.part = g.part;
   p.err = error_word();
   if (!p.err) return cudaErrorNotSupported;
+  const bool f32 = dtype == CONV_F32;
   const CUtensorMapDataType type = dtype == CONV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int b_rows = g.dual && t.cg == 1 ? t.nt / 2 : t.nt / t.cg;
   const int as = std::max(g.segs, g.batch), bs = g.segs > 1 || g.batch > 1 || g.dual ? 2 : 1;
   // one copy per operand and stage where the blocks of 64 divide the matrix and the block's share of the tile
-  p.a_3d = g.a_mn && g.M % 64 == 0;
-  p.b_3d = g.b_mn && g.N % 64 == 0 && b_rows % 64 == 0;
+  p.a_3d = g.a_mn && g.M % 64 == 0 && !f32;
+  p.b_3d = g.b_mn && g.N % 64 == 0 && b_rows % 64 == 0 && !f32;
   bool ok = true;
-  for (int i = 0; i < as; ++i)
-    ok = ok && (p.a_3d ? encode_blocks(&maps.a[i], type, g.a[i], g.M, g.K, g.lda, 2) : g.a_mn ? encode(&maps.a[i], type, g.a[i], g.M, g.K, g.lda, 0, 64)
-                       : encode(&maps.a[i], type, g.a[i], g.K, g.M, g.lda, 0, 128));
-  for (int i = 0; i < bs; ++i)
-    ok = ok && (p.b_3d ? encode_blocks(&maps.b[i], type, g.b[i], g.N, g.K, g.ldb, b_rows / 64) : g.b_mn ? encode(&maps.b[i], type, g.b[i], g.N, g.K, g.ldb, 0, 64)
-                       : encode(&maps.b[i], type, g.b[i], g.K, g.N, g.ldb, 0, b_rows));
+  auto operand = [&](CUtensorMap* map, const void* base, int mn, bool blocks, long long rows, long long ld, int box_rows,
+                     int box_blocks) {
+    if (f32)
+      return mn ? encode_planes(map, base, rows, g.K, ld, 64) : encode_planes(map, base, g.K, rows, ld, box_rows);
+    if (blocks) return encode_blocks(map, type, base, rows, g.K, ld, box_blocks);
+    return mn ? encode(map, type, base, rows, g.K, ld, 0, 64) : encode(map, type, base, g.K, rows, ld, 0, box_rows);
+  };
+  for (int i = 0; i < as; ++i) ok = ok && operand(&maps.a[i], g.a[i], g.a_mn, p.a_3d, g.M, g.lda, 128, 2);
+  for (int i = 0; i < bs; ++i) ok = ok && operand(&maps.b[i], g.b[i], g.b_mn, p.b_3d, g.N, g.ldb, b_rows, b_rows / 64);
   const int mode = t.split > 1 ? EPI_PARTIAL : g.epi.mode;
   if (mode == EPI_PARTIAL) {
     const int planes = t.split * dense_products(g);
@@ -206,10 +227,12 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
     if (p.tma_pre) ok = ok && encode(&maps.pre[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.part, g.N, g.M, g.N, planes, 32);
   } else {
     const bool two = mode == EPI_GATED_BWD || g.batch > 1;
-    p.tma_y = aligned(g.epi.y, g.epi.ldy, 2) && (!two || aligned(g.epi.y2, g.epi.ldy, 2));
+    const int es = f32 ? 4 : 2;
+    const CUtensorMapDataType ytype = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type;
+    p.tma_y = aligned(g.epi.y, g.epi.ldy, es) && (!two || aligned(g.epi.y2, g.epi.ldy, es));
     if (p.tma_y) {
-      ok = ok && encode(&maps.y[0], type, g.epi.y, g.N, g.M, g.epi.ldy, 0, 32, 64);
-      if (two) ok = ok && encode(&maps.y[1], type, g.epi.y2, g.N, g.M, g.epi.ldy, 0, 32, 64);
+      ok = ok && encode(&maps.y[0], ytype, g.epi.y, g.N, g.M, g.epi.ldy, 0, 32, 32 * es);
+      if (two) ok = ok && encode(&maps.y[1], ytype, g.epi.y2, g.N, g.M, g.epi.ldy, 0, 32, 32 * es);
     }
     if (mode == EPI_GATED_BWD && !(p.tma_y && aligned(g.epi.pre, g.epi.ldp, 4) && aligned(g.epi.pre2, g.epi.ldp, 4)))
       return cudaErrorInvalidValue;  // the library's own layout
@@ -223,6 +246,7 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
     }
   }
   if (!ok) return cudaErrorInvalidValue;
+  if (f32) return launch_dense_tc32(mode, g.a_mn, g.b_mn, p, maps, t.blocks, s);
   return dtype == CONV_F16 ? launch_dense_tc_f16(t, mode, g.a_mn, g.b_mn, p, maps, s)
                            : launch_dense_tc_bf16(t, mode, g.a_mn, g.b_mn, p, maps, s);
 }

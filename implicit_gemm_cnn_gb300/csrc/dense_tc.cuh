@@ -156,6 +156,14 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, ui
   else CONV_MMA_STAGE("1", ".b64 [%7]");
 #undef CONV_MMA_STAGE
 }
+// The MMAs of 64 terms alone (one SM).
+template <int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_terms(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
+  mma_f16(d, a, b, idesc, acc);
+  mma_f16(d, a + A_STEP, b + B_STEP, idesc, 1);
+  mma_f16(d, a + 2 * A_STEP, b + 2 * B_STEP, idesc, 1);
+  mma_f16(d, a + 3 * A_STEP, b + 3 * B_STEP, idesc, 1);
+}
 template <int CG>
 __device__ __forceinline__ void commit(uint32_t bar) {
   if constexpr (CG == 2)
@@ -300,6 +308,8 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
   if constexpr (CG == 2) cluster_sync_all(); else __syncthreads();
   tc_fence_after();
   const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  griddep_wait();
+  griddep_launch();
   const int first = blockIdx.x / CG, step = gridDim.x / CG;
 
   // The two issuing loops are one thread's: every instruction of theirs counts (a stage's MMAs take 512 clocks at most).

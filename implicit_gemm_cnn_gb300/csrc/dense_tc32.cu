@@ -1,0 +1,341 @@
+// dense_tc32.cu -- the dense products of float32 operands on the tensor cores.
+//
+// A float32 value is the exact sum of three bfloat16 values, each the rounding
+// of what the ones before leave (8 significand bits each, 24 in all).  A pass
+// over the operands writes the three as planes; a product then is
+//   a b = a0 b0 + (a0 b1 + a1 b0) + (a1 b1 + a0 b2 + a2 b0)
+// without a1 b2, a2 b1 and a2 b2, which are below 2^-24 of |a b|: six bfloat16
+// products, still three times the CUDA cores' float32 rate and more.
+//
+// The tensor cores cut their float32 accumulator instead of rounding it (the
+// sum of 1024 positive terms came out 2.2e-6 low, 64 terms 8e-8), so no
+// accumulator lives long: each 64 terms start a new one, the five small
+// products go first, while the accumulator is some 2^-8 of its final size, and
+// the epilogue warps add the finished 64-term sums up in registers, rounding to
+// nearest.  That work overlaps the next stage's MMAs (two accumulators).
+//
+// Otherwise as dense_tc.cuh, with tiles of 128 x 64 or 128 x 128 on one SM: a
+// stage is three planes of both operands, 96 KB, for 24 MMAs.
+#include <string.h>
+
+#include <algorithm>
+
+#include "dense_tc.cuh"
+
+namespace conv {
+namespace {
+using namespace dtc;
+
+constexpr int kEpiWarps = 4;
+constexpr int kThreads32 = 64 + 32 * kEpiWarps;
+constexpr int kPlaneBytes = 128 * 128;          // one plane of a 128-row operand tile, 64 terms
+constexpr int kStage32 = 6 * kPlaneBytes;
+constexpr int kStages32 = 2;
+constexpr int kStaging32 = kEpiWarps * 2 * kBufBytes;
+constexpr int kSmem32 = kStages32 * kStage32 + kStaging32 + 2032;
+
+template <int MODE, bool A_MN, bool B_MN>
+__global__ void __launch_bounds__(kThreads32, 1)
+    dense_tc32(const __grid_constant__ DenseTcArgs p, const __grid_constant__ DenseTcMaps maps) {
+  const int nt = p.nt, out_cols = MODE == EPI_GATED ? nt / 2 : nt;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ volatile int abort_flag;
+  __shared__ uint32_t tmem_slot;
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t staging = base + kStages32 * kStage32;
+  const uint32_t bars = staging + kStaging32;
+  auto full = [&](int s) { return bars + 8u * s; };
+  auto empty = [&](int s) { return bars + 8u * (kStages32 + s); };
+  auto acc_full = [&](int b) { return bars + 8u * (2 * kStages32 + b); };
+  auto acc_empty = [&](int b) { return bars + 8u * (2 * kStages32 + 2 + b); };
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
+  if (warp == 0 && lane == 0) {
+    for (int s = 0; s < kStages32; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
+    }
+    for (int b = 0; b < 2; ++b) {
+      mbar_init(acc_full(b), 1);
+      mbar_init(acc_empty(b), kEpiWarps);
+    }
+    abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
+    fence_proxy_async();
+  }
+  if (warp == 1) alloc_tmem<1>(smem_u32(&tmem_slot), 256);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_slot, 0);
+  griddep_wait();
+  griddep_launch();
+  const int first = blockIdx.x, step = gridDim.x;
+
+  if (warp == 0) {
+    if (elect_one()) {
+      // k-major: a box of 128 (nt) rows x 64 terms x 3 planes; mn-major: of 64 columns x 64 terms x 3 planes, one after
+      // another
+      const int b_boxes = nt / 64;
+      const uint32_t stage_bytes = 3 * (kPlaneBytes + nt * 128);
+      int s = 0;
+      uint32_t parity = 1;
+      bool ok = true;
+      for (int u = first; u < p.units && ok; u += step) {
+        const Tile t = tile_of(p, u);
+        const int kb0 = t.range * p.kb_range, kb1 = min(kb0 + p.kb_range, p.kb_total);
+        const int m0 = t.m * 128, n0 = t.n * out_cols;
+        for (int kb = kb0; kb < kb1; ++kb) {
+          if (!wait_phase(p.err, empty(s), parity, &abort_flag, 1u)) {
+            ok = false;
+            break;
+          }
+          mbar_arrive_expect_tx(full(s), stage_bytes);
+          const int seg = kb >= p.kb_seg ? 1 : 0, k0 = (kb - seg * p.kb_seg) * kBK;
+          const int op = p.segs > 1 ? seg : t.batch;
+          const uint32_t a = base + s * kStage32, b = a + 3 * kPlaneBytes;
+          if constexpr (A_MN) {
+            load_3d<1>(a, &maps.a[op], m0, k0, 0, full(s));
+            load_3d<1>(a + 3 * 8192, &maps.a[op], m0 + 64, k0, 0, full(s));
+          } else {
+            load_3d<1>(a, &maps.a[op], k0, m0, 0, full(s));
+          }
+          if constexpr (MODE == EPI_GATED) {
+            load_3d<1>(b, &maps.b[0], k0, n0, 0, full(s));
+            load_3d<1>(b + 3 * out_cols * 128, &maps.b[1], k0, n0, 0, full(s));
+          } else if constexpr (B_MN) {
+            for (int i = 0; i < b_boxes; ++i) load_3d<1>(b + i * 3 * 8192, &maps.b[op], n0 + 64 * i, k0, 0, full(s));
+          } else {
+            load_3d<1>(b, &maps.b[op], k0, n0, 0, full(s));
+          }
+          if (++s == kStages32) { s = 0; parity ^= 1; }
+        }
+      }
+      for (int left = kStages32; left > 0 && ok; --left) {
+        ok = wait_phase(p.err, empty(s), parity, &abort_flag, 1u);
+        if (++s == kStages32) { s = 0; parity ^= 1; }
+      }
+      if (!ok)  // copies in flight end within microseconds; the block does not return before
+        for (int i = 0; i < 1000; ++i) __nanosleep(10000);
+    }
+  } else if (warp == 1) {
+    if (elect_one()) {
+      // The gated product's B is two boxes (gate, up), each of three planes: two MMAs of half the columns.
+      constexpr int kHalves = MODE == EPI_GATED ? 2 : 1;
+      const int cols = nt / kHalves;
+      const uint32_t idesc = (1u << 4) | (1u << 7) | (1u << 10) | (static_cast<uint32_t>(A_MN) << 15) |
+                             (static_cast<uint32_t>(B_MN) << 16) | (static_cast<uint32_t>(cols >> 3) << 17) | (8u << 24);
+      constexpr int kAStep = A_MN ? 2048 >> 4 : 32 >> 4, kBStep = B_MN ? 2048 >> 4 : 32 >> 4;
+      // planes lie one after another within a box: mn-major 64-column blocks are three planes apart
+      const uint64_t a0 = smem_desc(base, A_MN ? 3 * 8192 : 16, 1024, 2);
+      const uint64_t b0 = smem_desc(base + 3 * kPlaneBytes, B_MN ? 3 * 8192 : 16, 1024, 2);
+      const uint64_t a_plane = (A_MN ? 8192 : kPlaneBytes) >> 4;
+      const uint64_t b_plane = (B_MN ? 8192 : cols * 128) >> 4;
+      int s = 0, it = 0;
+      uint32_t parity = 0;
+      bool ok = true;
+      for (int u = first; u < p.units && ok; u += step) {
+        const int kb0 = u / p.tiles * p.kb_range, kbs = min(p.kb_range, p.kb_total - kb0);
+        for (int kb = 0; kb < kbs; ++kb, ++it) {
+          const int buf = it & 1;
+          if (!wait_phase(p.err, acc_empty(buf), ((it >> 1) & 1) ^ 1, &abort_flag, 2u) ||
+              !wait_phase(p.err, full(s), parity, &abort_flag, 4u)) {
+            ok = false;
+            break;
+          }
+          tc_fence_after();
+          const uint64_t off = static_cast<uint64_t>(s) * (kStage32 >> 4);
+#pragma unroll
+          for (int h = 0; h < kHalves; ++h) {
+            const uint32_t d = tmem + buf * 128 + h * cols;
+            const uint64_t a = a0 + off, b = b0 + off + h * 3 * b_plane;
+            // the small products first, the large one last
+            mma_terms<kAStep, kBStep>(d, a, b + 2 * b_plane, idesc, 0);
+            mma_terms<kAStep, kBStep>(d, a + 2 * a_plane, b, idesc, 1);
+            mma_terms<kAStep, kBStep>(d, a + a_plane, b + b_plane, idesc, 1);
+            mma_terms<kAStep, kBStep>(d, a, b + b_plane, idesc, 1);
+            mma_terms<kAStep, kBStep>(d, a + a_plane, b, idesc, 1);
+            mma_terms<kAStep, kBStep>(d, a, b, idesc, 1);
+          }
+          commit<1>(empty(s));
+          commit<1>(acc_full(buf));
+          if (++s == kStages32) { s = 0; parity ^= 1; }
+        }
+      }
+      if (abort_flag)
+        for (int i = 0; i < 1000; ++i) __nanosleep(10000);
+    }
+  } else {
+    const int quarter = warp & 3;
+    const uint32_t mine = staging + (warp - 2) * 2 * kBufBytes;
+    const DenseEpi& e = p.epi;
+    int turn = 0, it = 0;
+    // 32 float32 columns of this lane's row
+    auto put = [&](const float (&v)[32], const CUtensorMap* map, float* out, long long ld, bool tma, int n, int m_warp,
+                   int plane) {
+      if (tma) {
+        if (lane == 0) bulk_wait_read<1>();
+        __syncwarp();
+        const uint32_t b = mine + (turn & 1) * kBufBytes;
+        ++turn;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          sts_v4(b + lane * 128 + ((q ^ (lane & 7)) << 4),
+                 make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                            __float_as_uint(v[4 * q + 3])));
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          if (plane >= 0) store_3d(map, b, n, m_warp, plane);
+          else store_2d(map, b, n, m_warp);
+          bulk_commit();
+        }
+      } else {
+        // rows of any alignment: through shared memory, so that a store instruction covers one row's consecutive columns
+        if (lane == 0) bulk_wait_read<0>();
+        __syncwarp();
+        float* tile = static_cast<float*>(__cvta_shared_to_generic(mine));
+#pragma unroll
+        for (int i = 0; i < 32; ++i) tile[lane * 33 + i] = v[i];
+        __syncwarp();
+        out += (plane >= 0 ? static_cast<long long>(plane) * p.M * p.N : 0) + static_cast<long long>(m_warp) * ld + n;
+        const int rows = min(32, p.M - m_warp);
+        if (n + lane < p.N)
+          for (int r = 0; r < rows; ++r) out[r * ld + lane] = tile[r * 33 + lane];
+        __syncwarp();
+      }
+    };
+    // 32 float32 values of a row, `n` of which exist, at any alignment
+    auto add_row = [&](float (&v)[32], const float* row, int n) {
+#pragma unroll
+      for (int i = 0; i < 32; ++i)
+        if (i < n) v[i] = __fadd_rn(v[i], row[i]);
+    };
+    for (int u = first; u < p.units; u += step) {
+      const Tile t = tile_of(p, u);
+      const int kb0 = t.range * p.kb_range, kbs = min(p.kb_range, p.kb_total - kb0);
+      const int m_warp = t.m * 128 + quarter * 32, m = m_warp + lane, n_tile = t.n * out_cols;
+      float acc[4][32];
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+#pragma unroll
+        for (int i = 0; i < 32; ++i) acc[c][i] = 0.0f;
+      bool ok = true;
+      for (int kb = 0; kb < kbs; ++kb, ++it) {
+        const int buf = it & 1;
+        if (!warp_wait(p.err, acc_full(buf), (it >> 1) & 1, &abort_flag, 8u)) {
+          ok = false;
+          break;
+        }
+        __syncwarp();
+        tc_fence_after();
+        const uint32_t at = tmem + buf * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (32 * c < nt) {
+            float v[32];
+            tmem_ld32(at + 32 * c, v);
+            tmem_arrived(v);
+#pragma unroll
+            for (int i = 0; i < 32; ++i) acc[c][i] += v[i];
+          }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(acc_empty(buf));
+      }
+      if (!ok) break;
+      if (m_warp >= p.M) continue;
+      // one copy of the code for all pieces: the next piece's sums move into acc[0]
+#pragma unroll 1
+      for (int c = 0; 32 * c < out_cols; ++c) {
+        if (c > 0) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            acc[0][i] = acc[1][i];
+            if (MODE != EPI_GATED) acc[1][i] = acc[2][i];
+            acc[2][i] = acc[3][i];
+          }
+        }
+        const int n = n_tile + 32 * c, left = p.N - n;
+        if (left <= 0) break;
+        const bool row_ok = m < p.M;
+        if constexpr (MODE == EPI_PARTIAL) {
+          put(acc[0], &maps.pre[0], p.part, p.N, p.tma_pre, n, m_warp, t.range * p.batch + t.batch);
+        } else if constexpr (MODE == EPI_GATED) {
+          // gate columns are the tile's first half, up columns its second
+          float up[32];
+#pragma unroll
+          for (int i = 0; i < 32; ++i) up[i] = nt == 64 ? acc[1][i] : acc[2][i];
+          if (e.pre) {
+            put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp, -1);
+            put(up, &maps.pre[1], e.pre2, e.ldp, p.tma_pre, n, m_warp, -1);
+          }
+          dense_activate<false, 32>(acc[0], e.act, e.alpha, e.beta);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) up[i] *= acc[0][i];
+          put(up, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.tma_y, n, m_warp, -1);
+        } else if constexpr (MODE == EPI_GATED_BWD) {
+          float g[32], slope[32];
+          const float* gp = e.pre + static_cast<long long>(m) * e.ldp + n;
+          const float* up = e.pre2 + static_cast<long long>(m) * e.ldp + n;
+#pragma unroll
+          for (int i = 0; i < 32; ++i) g[i] = row_ok && i < left ? gp[i] : 0.0f;
+          dense_activate_grad<false, 32>(g, slope, e.act, e.alpha, e.beta);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) {
+            slope[i] *= acc[0][i] * (row_ok && i < left ? up[i] : 0.0f);
+            g[i] *= acc[0][i];
+          }
+          put(slope, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.tma_y, n, m_warp, -1);
+          put(g, &maps.y[1], static_cast<float*>(e.y2), e.ldy, p.tma_y, n, m_warp, -1);
+        } else {
+          const float* res = e.residual && row_ok ? static_cast<const float*>(e.residual) + static_cast<long long>(m) * e.ldr + n
+                                                  : nullptr;
+          if (e.bias) add_row(acc[0], static_cast<const float*>(e.bias) + n, left);
+          if (res && !e.residual_last) add_row(acc[0], res, left);
+          if (e.pre) put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp, -1);
+          dense_activate<false, 32>(acc[0], e.act, e.alpha, e.beta);
+          if (res && e.residual_last) add_row(acc[0], res, left);
+          put(acc[0], &maps.y[t.batch], static_cast<float*>(t.batch ? e.y2 : e.y), e.ldy, p.tma_y, n, m_warp, -1);
+        }
+      }
+    }
+    if (lane == 0) bulk_wait_all();
+    __syncwarp();
+  }
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    free_tmem<1>(tmem, 256);
+  }
+}
+
+template <int MODE, bool A_MN, bool B_MN>
+cudaError_t go32(const DenseTcArgs& args, const DenseTcMaps& maps, int blocks, cudaStream_t s) {
+  auto kern = dense_tc32<MODE, A_MN, B_MN>;
+  cudaError_t err = opt_in_smem(reinterpret_cast<const void*>(kern), kSmem32);
+  if (err != cudaSuccess) return err;
+  return launch_overlapped(kern, dim3(static_cast<unsigned>(blocks)), kThreads32, kSmem32, 1, s, args, maps);
+}
+template <int MODE>
+cudaError_t order32(int a_mn, int b_mn, const DenseTcArgs& args, const DenseTcMaps& maps, int blocks, cudaStream_t s) {
+  if (a_mn) return b_mn ? go32<MODE, true, true>(args, maps, blocks, s) : cudaErrorInvalidValue;
+  return b_mn ? go32<MODE, false, true>(args, maps, blocks, s) : go32<MODE, false, false>(args, maps, blocks, s);
+}
+
+}  // namespace
+
+cudaError_t launch_dense_tc32(int mode, int a_mn, int b_mn, const DenseTcArgs& args, const DenseTcMaps& maps, int blocks,
+                              cudaStream_t s) {
+  switch (mode) {
+    case EPI_GATED:
+      return a_mn || b_mn ? cudaErrorInvalidValue : go32<EPI_GATED, false, false>(args, maps, blocks, s);
+    case EPI_GATED_BWD:
+      return a_mn || !b_mn ? cudaErrorInvalidValue : go32<EPI_GATED_BWD, false, true>(args, maps, blocks, s);
+    case EPI_PARTIAL: return order32<EPI_PARTIAL>(a_mn, b_mn, args, maps, blocks, s);
+    default: return order32<EPI_LINEAR>(a_mn, b_mn, args, maps, blocks, s);
+  }
+}
+
+}  // namespace conv

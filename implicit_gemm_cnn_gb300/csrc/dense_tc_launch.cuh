@@ -13,19 +13,7 @@ cudaError_t go(const DenseTcArgs& args, const DenseTcMaps& maps, int blocks, cud
   auto kern = dense_tc<T, CG, NT, MODE, A_MN, B_MN>;
   cudaError_t err = opt_in_smem(reinterpret_cast<const void*>(kern), C::kSmem);
   if (err != cudaSuccess) return err;
-  cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(blocks));
-  cfg.blockDim = dim3(C::kThreads);
-  cfg.dynamicSmemBytes = C::kSmem;
-  cfg.stream = s;
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = CG;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  cfg.attrs = attr;
-  cfg.numAttrs = CG > 1 ? 1 : 0;
-  return cudaLaunchKernelEx(&cfg, kern, args, maps);
+  return launch_overlapped(kern, dim3(static_cast<unsigned>(blocks)), C::kThreads, C::kSmem, CG, s, args, maps);
 }
 
 // The operand orders that occur: the layer's, its input gradient's, its weight gradient's.
