@@ -184,7 +184,8 @@ __global__ void __launch_bounds__(256) dense_reduce(const DenseGemm g) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) { col[j] = n + j; ok[j] = n + j < g.N; }
   const bool vec = g.N % 4 == 0;  // planes are 16-byte aligned then
-  for (int s = 0; s < g.split; ++s) {
+#pragma unroll 4
+  for (int s = 0; s < g.split; ++s) {  // (loads of four ranges in flight; added in order)
     if (vec) {
       const float4 t = *reinterpret_cast<const float4*>(p);
       v[0] += t.x; v[1] += t.y; v[2] += t.z; v[3] += t.w;

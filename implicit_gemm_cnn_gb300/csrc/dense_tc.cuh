@@ -59,7 +59,7 @@ struct Cfg {
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kABytes = 128 * 128;
   static constexpr int kStageBytes = kABytes + NT / CG * 128;
-  static constexpr int kWarpBufs = MODE == EPI_GATED_BWD ? 3 : 1;  // g, u and the outputs; or the outputs alone
+  static constexpr int kWarpBufs = MODE == EPI_GATED_BWD ? 2 : 1;  // g and u, whose place the outputs take; or outputs alone
   static constexpr int kStaging = kEpiWarps * kWarpBufs * kBufBytes;
   static constexpr int kFit = (232448 - 2048 - kStaging) / kStageBytes;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
@@ -247,6 +247,10 @@ __device__ __forceinline__ void add_row32(float (&v)[32], const uint32_t (&w)[16
   }
 }
 
+__device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
+  asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
+}
+
 // Where unit u's tile lies: blocks of `group` tile rows are walked column by
 // column, so that the tiles in flight share operands in L2.
 struct Tile {
@@ -419,7 +423,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
     const DenseEpi& e = p.epi;
     // The outputs' staging tile: one float32 piece, or two 16-bit ones in turn.  A piece waits until the stores that
     // read its place have done so: the last but one's if both are 16-bit, else the last one's.
-    const uint32_t out_buf = mine + (C::kWarpBufs - 1) * kBufBytes;
+    const uint32_t out_buf = mine;
     int turn = 0;
     bool last_wide = true;
     auto acquire = [&](bool wide) {
@@ -442,13 +446,19 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       for (int q = 0; q < 4; ++q)
         sts_v4(b + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
     };
+    // rows of any alignment: through shared memory, a store instruction covers 32 consecutive columns of one row
     auto plain16 = [&](const uint32_t (&w)[16], T* y, int n, int m_warp) {
-      if (m_warp + lane < p.M) {
-        uint16_t* row = reinterpret_cast<uint16_t*>(y + static_cast<long long>(m_warp + lane) * e.ldy + n);
+      const uint32_t b = acquire(true);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (n + j < p.N) row[j] = static_cast<uint16_t>(w[j / 2] >> (16 * (j & 1)));
+      for (int i = 0; i < 16; ++i) sts_u32(b + lane * 68 + 4 * i, w[i]);
+      __syncwarp();
+      uint16_t* out = reinterpret_cast<uint16_t*>(y + static_cast<long long>(m_warp) * e.ldy + n) + lane;
+      const int rows = min(32, p.M - m_warp);
+      if (n + lane < p.N) {
+#pragma unroll 8
+        for (int r = 0; r < rows; ++r) out[r * e.ldy] = lds_u16(b + r * 68 + 2 * lane);
       }
+      __syncwarp();
     };
     auto put16 = [&](const uint32_t (&w)[16], const CUtensorMap* map, T* y, int n, int m_warp) {
       if (!p.tma_y) return plain16(w, y, n, m_warp);
@@ -475,12 +485,24 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
           else store_2d(map, b, n, m_warp);
           bulk_commit();
         }
-      } else if (m_warp + lane < p.M) {
-        float* row = out + (plane >= 0 ? static_cast<long long>(plane) * p.M * p.N : 0) +
-                     static_cast<long long>(m_warp + lane) * ld + n;
+      } else {
+        // in two halves of 16 rows (33 words apart), which fit the staging tile
+        out += (plane >= 0 ? static_cast<long long>(plane) * p.M * p.N : 0) + static_cast<long long>(m_warp) * ld + n + lane;
+        const uint32_t b = acquire(true);
 #pragma unroll
-        for (int j = 0; j < 32; ++j)
-          if (n + j < p.N) row[j] = v[j];
+        for (int h = 0; h < 2; ++h) {
+          if (lane / 16 == h) {
+#pragma unroll
+            for (int i = 0; i < 32; ++i) sts_u32(b + (lane % 16) * 132 + 4 * i, __float_as_uint(v[i]));
+          }
+          __syncwarp();
+          const int rows = min(16, p.M - m_warp - 16 * h);
+          if (n + lane < p.N) {
+#pragma unroll 8
+            for (int r = 0; r < rows; ++r) out[(16 * h + r) * ld] = lds_f32(b + r * 132 + 4 * lane);
+          }
+          __syncwarp();
+        }
       }
     };
     const bool vec_r = e.ldr % 8 == 0 && reinterpret_cast<uintptr_t>(e.residual) % 16 == 0;
@@ -495,7 +517,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       const int m = m_warp + lane, n_tile = t.n * out_cols;
       // pieces that exist: this warp's rows, and columns below N
       const int c_end = m_warp < p.M ? min(c1, (p.N - n_tile + 31) / 32) : c0;
-      // g and u of a piece, loaded while the one before is worked on
+      // g and u of a piece (a tile's first one is on its way before its sums are)
       auto fetch = [&](int c) {
         if (lane == 0) {
           mbar_arrive_expect_tx(in_full(warp - 2), 2 * kBufBytes);
@@ -563,17 +585,17 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
             w2[2 * q] = pack_pair<T>(v[4 * q] * g[4 * q], v[4 * q + 1] * g[4 * q + 1]);
             w2[2 * q + 1] = pack_pair<T>(v[4 * q + 2] * g[4 * q + 2], v[4 * q + 3] * g[4 * q + 3]);
           }
-          __syncwarp();  // g and u have been read
-          if (c + 1 < c_end) fetch(c + 1);
-          const uint32_t b = acquire(true);
-          stage16(b, w);
-          stage16(b + kBufBytes / 2, w2);
+          __syncwarp();  // g and u have been read: the outputs take g's place, then the next piece's come
+          stage16(mine, w);
+          stage16(mine + kBufBytes / 2, w2);
           publish();
           if (lane == 0) {
-            store_2d(&maps.y[0], b, n, m_warp);
-            store_2d(&maps.y[1], b + kBufBytes / 2, n, m_warp);
+            store_2d(&maps.y[0], mine, n, m_warp);
+            store_2d(&maps.y[1], mine + kBufBytes / 2, n, m_warp);
             bulk_commit();
+            bulk_wait_read<0>();
           }
+          if (c + 1 < c_end) fetch(c + 1);
         } else {
           uint32_t bias[16];
           if (e.bias) load_row32(static_cast<const T*>(e.bias) + n, vec_b, left, bias);

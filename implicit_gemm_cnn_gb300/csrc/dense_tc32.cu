@@ -204,6 +204,15 @@ __global__ void __launch_bounds__(kThreads32, 1)
         __syncwarp();
       }
     };
+    auto activate = [&](float (&v)[32]) {
+      if (e.act == ACT_IDENTITY) return;
+      float t[32];
+#pragma unroll
+      for (int i = 0; i < 32; ++i) t[i] = v[i];
+      dense_activate_array(t, e.act, e.alpha, e.beta);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) v[i] = t[i];
+    };
     // 32 float32 values of a row, `n` of which exist, at any alignment
     auto add_row = [&](float (&v)[32], const float* row, int n) {
 #pragma unroll
@@ -269,7 +278,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
             put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp, -1);
             put(up, &maps.pre[1], e.pre2, e.ldp, p.tma_pre, n, m_warp, -1);
           }
-          dense_activate<false, 32>(acc[0], e.act, e.alpha, e.beta);
+          activate(acc[0]);
 #pragma unroll
           for (int i = 0; i < 32; ++i) up[i] *= acc[0][i];
           put(up, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.tma_y, n, m_warp, -1);
@@ -279,7 +288,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
           const float* up = e.pre2 + static_cast<long long>(m) * e.ldp + n;
 #pragma unroll
           for (int i = 0; i < 32; ++i) g[i] = row_ok && i < left ? gp[i] : 0.0f;
-          dense_activate_grad<false, 32>(g, slope, e.act, e.alpha, e.beta);
+          dense_activate_grad_array(g, slope, e.act, e.alpha, e.beta);
 #pragma unroll
           for (int i = 0; i < 32; ++i) {
             slope[i] *= acc[0][i] * (row_ok && i < left ? up[i] : 0.0f);
@@ -293,7 +302,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
           if (e.bias) add_row(acc[0], static_cast<const float*>(e.bias) + n, left);
           if (res && !e.residual_last) add_row(acc[0], res, left);
           if (e.pre) put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp, -1);
-          dense_activate<false, 32>(acc[0], e.act, e.alpha, e.beta);
+          activate(acc[0]);
           if (res && e.residual_last) add_row(acc[0], res, left);
           put(acc[0], &maps.y[t.batch], static_cast<float*>(t.batch ? e.y2 : e.y), e.ldy, p.tma_y, n, m_warp, -1);
         }
