@@ -126,6 +126,25 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const void* map, int c0, i
         "[%5];\n" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
+// What an epilogue reads or writes passes through L2 once: it is the first to go, so that the operands' tiles, which are
+// read by many blocks, stay.
+__device__ __forceinline__ uint64_t once_policy() {
+  uint64_t p;
+  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(p));
+  return p;
+}
+__device__ __forceinline__ void load_2d_once(uint32_t dst, const void* map, int c0, int c1, uint32_t bar, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
+      "%3}], [%4], %5;\n" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
+      : "memory");
+}
+__device__ __forceinline__ void store_2d_once(const void* map, uint32_t src, int c0, int c1, uint64_t policy) {
+  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2}], [%3], %4;\n" ::"l"(
+                   map),
+               "r"(c0), "r"(c1), "r"(src), "l"(policy)
+               : "memory");
+}
 __device__ __forceinline__ void store_2d(const void* map, uint32_t src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(c0),
                "r"(c1), "r"(src)
@@ -421,6 +440,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
     constexpr int kParts = C::kEpiWarps / 4;       // warps that share a quarter's columns
     const uint32_t mine = staging + (warp - 2) * C::kWarpBufs * kBufBytes;
     const DenseEpi& e = p.epi;
+    const uint64_t once = once_policy();
     // The outputs' staging tile: one float32 piece, or two 16-bit ones in turn.  A piece waits until the stores that
     // read its place have done so: the last but one's if both are 16-bit, else the last one's.
     const uint32_t out_buf = mine;
@@ -466,7 +486,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       stage16(b, w);
       publish();
       if (lane == 0) {
-        store_2d(map, b, n, m_warp);
+        store_2d_once(map, b, n, m_warp, once);
         bulk_commit();
       }
     };
@@ -482,7 +502,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
         publish();
         if (lane == 0) {
           if (plane >= 0) store_3d(map, b, n, m_warp, plane);
-          else store_2d(map, b, n, m_warp);
+          else store_2d_once(map, b, n, m_warp, once);
           bulk_commit();
         }
       } else {
@@ -521,8 +541,8 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       auto fetch = [&](int c) {
         if (lane == 0) {
           mbar_arrive_expect_tx(in_full(warp - 2), 2 * kBufBytes);
-          load_2d<1>(mine, &maps.pre[0], n_tile + 32 * c, m_warp, in_full(warp - 2));
-          load_2d<1>(mine + kBufBytes, &maps.pre[1], n_tile + 32 * c, m_warp, in_full(warp - 2));
+          load_2d_once(mine, &maps.pre[0], n_tile + 32 * c, m_warp, in_full(warp - 2), once);
+          load_2d_once(mine + kBufBytes, &maps.pre[1], n_tile + 32 * c, m_warp, in_full(warp - 2), once);
         }
       };
       if (MODE == EPI_GATED_BWD && c0 < c_end) fetch(c0);
@@ -590,8 +610,8 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
           stage16(mine + kBufBytes / 2, w2);
           publish();
           if (lane == 0) {
-            store_2d(&maps.y[0], mine, n, m_warp);
-            store_2d(&maps.y[1], mine + kBufBytes / 2, n, m_warp);
+            store_2d_once(&maps.y[0], mine, n, m_warp, once);
+            store_2d_once(&maps.y[1], mine + kBufBytes / 2, n, m_warp, once);
             bulk_commit();
             bulk_wait_read<0>();
           }
