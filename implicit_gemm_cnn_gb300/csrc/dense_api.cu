@@ -103,12 +103,14 @@ Product plan_product(const DenseGemm& g, int dtype, bool tc, bool few, int sm) {
     r.variant = V_TC;
     r.tc = dense_tc_plan(g, dtype, sm);
     r.split = r.tc.split;
+    r.part_bytes = r.tc.part_bytes;
   } else {
     r.variant = V_FFMA;
     r.ffma = dense_ffma_plan(g, sm);
     r.split = r.ffma.split;
   }
-  if (r.split > 1) r.part_bytes = static_cast<size_t>(r.split) * dense_products(g) * g.M * g.N * sizeof(float);
+  if (r.variant == V_FFMA && r.split > 1)
+    r.part_bytes = static_cast<size_t>(r.split) * dense_products(g) * g.M * g.N * sizeof(float);
   r.launches = r.split > 1 ? 2 : 1;
   return r;
 }
@@ -116,17 +118,12 @@ Product plan_product(const DenseGemm& g, int dtype, bool tc, bool few, int sm) {
 // `follows`: the kernel before in the stream is this call's own.
 cudaError_t launch_product(const Product& r, DenseGemm g, int dtype, void* part, bool follows, cudaStream_t s) {
   if (r.variant == V_FEW) return launch_dense_few(g, dtype, follows, s);
+  if (r.variant == V_TC) return launch_dense_tc(r.tc, g, dtype, part, s);
   g.split = r.split;
   g.part = static_cast<float*>(part);
-  cudaError_t err;
-  if (r.variant == V_TC) {
-    err = launch_dense_tc(r.tc, g, dtype, s);
-  } else {
-    g.k_per_split = r.ffma.k_per_split;
-    err = launch_dense_ffma(r.ffma, g, dtype, s);
-  }
-  if (err == cudaSuccess && g.split > 1) err = launch_dense_reduce(g, dtype, s);
-  return err;
+  g.k_per_split = r.ffma.k_per_split;
+  const cudaError_t err = launch_dense_ffma(r.ffma, g, dtype, s);
+  return err == cudaSuccess && g.split > 1 ? launch_dense_reduce(g, dtype, s) : err;
 }
 
 void describe_product(const Product& r, const DenseGemm& g, bool f32, int sm, char* buf, size_t len) {
@@ -134,8 +131,8 @@ void describe_product(const Product& r, const DenseGemm& g, bool f32, int sm, ch
   if (r.variant == V_FEW)
     snprintf(buf, len, "few_rows tile=%dx16 split=1 products=%d sums over %lld sms=%d launches=1", g.M, dense_products(g), k, sm);
   else if (r.variant == V_TC)
-    snprintf(buf, len, "%s tile=%dx%d sms_per_tile=%d tiles=%lld split=%d products=%d sums over %lld sms=%d launches=%d",
-             f32 ? "tcgen05_bf16x3" : "tcgen05", 128 * r.tc.cg, r.tc.nt, r.tc.cg, r.tc.tiles, r.split, dense_products(g), k, sm, r.launches);
+    snprintf(buf, len, "%s tile=%dx%d sms_per_tile=%d tiles=%d whole=%d split=%d products=%d sums over %lld sms=%d launches=%d",
+             f32 ? "tcgen05_bf16x3" : "tcgen05", 128 * r.tc.cg, r.tc.nt, r.tc.cg, r.tc.tiles, r.tc.whole, r.split, dense_products(g), k, sm, r.launches);
   else
     snprintf(buf, len, "ffma tile=%dx%d split=%d products=%d sums over %lld sms=%d launches=%d", r.ffma.bm, r.ffma.bn,
              r.split, dense_products(g), k, sm, r.launches);
@@ -318,7 +315,7 @@ struct GatedPlan {
   Copy x, wg, wu, wd, dy, h, dg, du;
   DenseGemm up, down;                 // forward
   DenseGemm dh, dx, dwgu, dwd;        // backward
-  Product pup, pdown, pdh, pdx, pdwgu, pdwd;
+  Product pup, pdown, pdh, pdx, pdwgu, pdw1, pdwd;  // pdw1: one of dWg, dWu alone
   size_t h_off, dg_off, du_off, part_off, total;
 };
 struct GatedSaved {
@@ -391,11 +388,14 @@ GatedPlan plan_gated_backward(const conv_gated_problem* p, const GatedShape& sh,
     r.dwgu.batch = 2;
     r.dwgu.epi.ldy = p->c_in;
     r.pdwgu = plan_product(r.dwgu, p->dtype, mode.tc, false, sm);
+    DenseGemm one = r.dwgu;
+    one.batch = 1;
+    r.pdw1 = plan_product(one, p->dtype, mode.tc, false, sm);
     r.dwd = make_gemm(p->c_out, p->hidden, p->rows, 1, 1, r.dy.ld, r.h.ld);
     r.dwd.epi.ldy = p->hidden;
     r.pdwd = plan_product(r.dwd, p->dtype, mode.tc, false, sm);
   }
-  r.part_off = l.take(std::max({r.pdh.part_bytes, r.pdx.part_bytes, r.pdwgu.part_bytes, r.pdwd.part_bytes}));
+  r.part_off = l.take(std::max({r.pdh.part_bytes, r.pdx.part_bytes, r.pdwgu.part_bytes, r.pdw1.part_bytes, r.pdwd.part_bytes}));
   r.total = l.total;
   return r;
 }
@@ -773,8 +773,9 @@ conv_status conv_gated_backward(const conv_gated_problem* p, const void* x, cons
     g.a[1] = du;
     g.epi.y = dw_gate;
     g.epi.y2 = dw_up;
-    if (!dw_gate || !dw_up) {  // one of the two: its planes fit where both would
+    if (!dw_gate || !dw_up) {
       g.batch = 1;
+      q = r.pdw1;
       if (!dw_gate) g.a[0] = g.a[1], g.epi.y = dw_up;
     }
     CONV_TRY(launch_product(q, g, p->dtype, part, false, s));

@@ -21,8 +21,7 @@ constexpr int ACT_GELU_TANH = 10;
 enum DenseEpiMode {
   EPI_LINEAR = 0,     // bias, residual, activation; y, and the activation's argument if wanted
   EPI_GATED = 1,      // two products g, u: y = act(g) * u; g and u if wanted
-  EPI_GATED_BWD = 2,  // the product dh, and g, u as saved: y = dh * u * act'(g), y2 = dh * act(g)
-  EPI_PARTIAL = 3     // the raw float32 sums of a k range, into a plane of scratch
+  EPI_GATED_BWD = 2   // the product dh, and g, u as saved: y = dh * u * act'(g), y2 = dh * act(g)
 };
 
 struct DenseEpi {
@@ -49,7 +48,7 @@ struct DenseGemm {
   const void* b[2];
   long long lda, ldb;
   DenseEpi epi;
-  // k ranges: `split` of `k_per_split` terms of the whole sum (segs * K), each
+  // k ranges of the CUDA-core kernel: `split` of `k_per_split` terms of the whole sum (segs * K), each
   // into plane s of `part` (float32 [split][products][M][N]); 1: the whole sum
   int split;
   long long k_per_split;

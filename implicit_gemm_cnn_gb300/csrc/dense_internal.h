@@ -47,13 +47,14 @@ cudaError_t launch_dense_ffma(const DenseFfmaPlan& p, const DenseGemm& g, int dt
 // the three bfloat16 planes of float32 ones (dense_tc32.cu).
 struct DenseTcPlan {
   int cg, nt;       // SMs per tile, MMA columns: tiles of 128 * cg x nt (nt / 2 gated)
-  int split;        // k ranges
+  int tiles, whole; // tiles; the first ones, done whole
+  int split;        // k ranges of the others
   int kb_range;     // 64-term blocks of a range
-  long long tiles;
   int blocks;       // persistent blocks
+  size_t part_bytes;  // the ranges' sums
 };
 DenseTcPlan dense_tc_plan(const DenseGemm& g, int dtype, int sm);
-cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype, cudaStream_t s);
+cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype, void* part, cudaStream_t s);
 cudaError_t dense_error_word(uint32_t* word, int reset);
 
 // Few rows (dense_few.cu): at most 16, any alignment.  `follows`:

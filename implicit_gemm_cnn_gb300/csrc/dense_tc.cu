@@ -103,42 +103,82 @@ bool aligned(const void* p, long long ld, size_t es) {
 
 // The tile and the k ranges of least time by this model, in clocks, fitted to full waves of 4096-term sums (bfloat16,
 // 1.85 GHz): 64 terms of a pair's tile take 165 + 1.73 nt (608 at nt = 256, 386 at 128: 512 and 256 are the MMAs
-// alone), of one SM's 128 columns 415 (its stage is as many bytes as the pair's of 256); a tile adds 600, a launch
-// 6000, the ranges' planes pass through L2 twice at some 3000 bytes a clock, with a launch of their own.
-// float32 (dense_tc32.cu): one SM's tiles of 64 or 128 columns, six products; a stage of 64 terms takes the MMAs' 12 nt
-// clocks or its 16-byte rows' and hand-overs' 1000, whichever is more.
+// alone), of one SM's 190 + 1.76 nt (415 at 128: its stage is as many bytes as the pair's of 256); a tile adds 600, a
+// launch 6000.  Tiles run in rounds of one per block.  The last round, if it is not full, may be cut into k ranges, so
+// that it takes a part of a round's time; their sums pass through L2 twice, at some 4000 bytes a clock, and cost a launch.
+// float32 (dense_tc32.cu): one SM's tiles of 64 or 128 columns, six products; a stage of 64 terms takes 13 nt clocks, or
+// the 1000 of its copies and hand-overs.
 DenseTcPlan search(const DenseGemm& g, int f32, int sm) {
   DenseTcPlan best = {};
   const int kb = static_cast<int>((static_cast<long long>(g.K) + dtc::kBK - 1) / dtc::kBK) * g.segs;
-  const int products = dense_products(g);
   double best_t = 0.0;
   for (int cg = f32 ? 1 : 2; cg >= 1; --cg) {
     const long long slots = sm / cg;
     for (int nt = cg == 2 ? 256 : 128; nt >= 64; nt -= 32) {
       if ((g.dual || f32) && nt % 64) continue;
+      const int cols = g.dual ? nt / 2 : nt;
+      const long long tiles = ((g.M + 128LL * cg - 1) / (128 * cg)) * ((static_cast<long long>(g.N) + cols - 1) / cols) * g.batch;
+      const double per = f32 ? std::max(13.0 * nt, 1000.0) : cg == 2 ? 165.0 + 1.73 * nt : 190.0 + 1.76 * nt;
+      const long long rest = tiles % slots;
       for (int split = 1; split <= 16; ++split) {
-        if (split > 1 && kb / split < 4) break;
-        // a gated product whose k is split runs as two products (its planes meet in the second launch)
-        const int cols = g.dual && split == 1 ? nt / 2 : nt;
-        const long long tiles = ((g.M + 128LL * cg - 1) / (128 * cg)) * ((static_cast<long long>(g.N) + cols - 1) / cols) *
-                                (g.dual && split > 1 ? 2 : g.batch);
+        if (split > 1 && (kb / split < 4 || rest == 0)) break;
         const int range = (kb + split - 1) / split;
         if ((kb + range - 1) / range != split) continue;  // every range holds terms
-        const long long units = tiles * split;
-        if (split > 1 && units > 2 * slots) break;
-        const double per = f32 ? std::max(13.0 * nt, 1000.0) : cg == 2 ? 165.0 + 1.73 * nt : 190.0 + 1.76 * nt;
-        double t = static_cast<double>((units + slots - 1) / slots) * (range * per + 600.0) + 6000.0;
-        if (split > 1) t += 4000.0 + 2.0 * split * products * 4.0 * g.M * g.N / 3000.0;
+        const long long whole = split > 1 ? tiles - rest : tiles, ranges = (tiles - whole) * split;
+        if (split > 1 && ranges > 2 * slots) break;
+        const double bytes = split > 1 ? static_cast<double>(ranges) * 128 * cg * nt * 4 : 0.0;
+        double t = static_cast<double>((whole + slots - 1) / slots) * (kb * per + 600.0) + 6000.0;
+        if (split > 1)
+          t += static_cast<double>((ranges + slots - 1) / slots) * (range * per + 600.0) + 4000.0 + 2.0 * bytes / 4000.0;
         if (!best.cg || t < best_t) {
           best_t = t;
           best.cg = cg; best.nt = nt; best.split = split; best.kb_range = range;
-          best.tiles = tiles;
-          best.blocks = static_cast<int>(std::min(units, slots)) * cg;
+          best.tiles = static_cast<int>(tiles);
+          best.whole = static_cast<int>(whole);
+          best.blocks = static_cast<int>(std::min(whole + ranges, slots)) * cg;
+          best.part_bytes = static_cast<size_t>(bytes);
         }
       }
     }
   }
   return best;
+}
+
+// Adds the k ranges' sums of the tiles that were cut, in order, and runs their epilogue: four columns per thread.
+template <typename T>
+__global__ void __launch_bounds__(256) dense_join(const __grid_constant__ DenseTcArgs p, const float* part, int tile_rows,
+                                                  int dual) {
+  griddep_wait();
+  griddep_launch();
+  const int out_cols = dual ? p.nt / 2 : p.nt, quads = out_cols / 4;
+  const long long per = static_cast<long long>(tile_rows) * quads;
+  const long long i = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
+  const int q = static_cast<int>(i / per);
+  if (p.whole + static_cast<long long>(q) * p.split >= p.units) return;
+  const int at = static_cast<int>(i - q * per), row = at / quads, c = at % quads * 4;
+  const dtc::Tile t = dtc::tile_of(p, p.whole + q * p.split);
+  const int m = t.m * tile_rows + row, n = t.n * out_cols + c;
+  if (m >= p.M || n >= p.N) return;
+  const long long tile = static_cast<long long>(tile_rows) * p.nt;
+  const float* src = part + (static_cast<long long>(q) * p.split * tile_rows + row) * p.nt + c;
+  float v[4] = {0.0f, 0.0f, 0.0f, 0.0f}, u[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 4
+  for (int s = 0; s < p.split; ++s) {
+    const float4 f = *reinterpret_cast<const float4*>(src + s * tile);
+    v[0] += f.x; v[1] += f.y; v[2] += f.z; v[3] += f.w;
+    if (dual) {
+      const float4 h = *reinterpret_cast<const float4*>(src + s * tile + p.nt / 2);
+      u[0] += h.x; u[1] += h.y; u[2] += h.z; u[3] += h.w;
+    }
+  }
+  int col[4];
+  bool ok[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    col[j] = n + j;
+    ok[j] = n + j < p.N;
+  }
+  dense_epilogue<T, 4>(p.epi, t.batch, m, col, ok, v, u);
 }
 
 // The plans of the shapes used last (a search takes microseconds, a small product too).
@@ -174,14 +214,8 @@ DenseTcPlan dense_tc_plan(const DenseGemm& g, int dtype, int sm) {
   return plan;
 }
 
-cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dtype, cudaStream_t s) {
+cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype, void* part, cudaStream_t s) {
   if (!encoder()) return cudaErrorNotSupported;
-  DenseGemm g = given;
-  if (g.dual && t.split > 1) {
-    g.dual = 0;
-    g.batch = 2;
-    g.a[1] = g.a[0];
-  }
   DenseTcArgs p;
   DenseTcMaps maps;
   memset(&p, 0, sizeof(p));
@@ -196,11 +230,10 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
   const int cols = g.dual ? t.nt / 2 : t.nt;
   p.mtiles = static_cast<int>((g.M + 128LL * t.cg - 1) / (128 * t.cg));
   p.ntiles = static_cast<int>((static_cast<long long>(g.N) + cols - 1) / cols);
-  p.tiles = p.mtiles * p.ntiles * g.batch;
-  p.units = p.tiles * t.split;
+  p.whole = t.whole;
+  p.units = t.whole + (t.tiles - t.whole) * t.split;
   p.group = 16;  // 8 to 19 rows of tiles measured alike, 1 and 32 some 5% slower
   p.epi = g.epi;
-  p.part = g.part;
   p.err = error_word();
   if (!p.err) return cudaErrorNotSupported;
   const bool f32 = dtype == CONV_F32;
@@ -220,12 +253,12 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
   };
   for (int i = 0; i < as; ++i) ok = ok && operand(&maps.a[i], g.a[i], g.a_mn, p.a_3d, g.M, g.lda, 128, 2);
   for (int i = 0; i < bs; ++i) ok = ok && operand(&maps.b[i], g.b[i], g.b_mn, p.b_3d, g.N, g.ldb, b_rows, b_rows / 64);
-  const int mode = t.split > 1 ? EPI_PARTIAL : g.epi.mode;
-  if (mode == EPI_PARTIAL) {
-    const int planes = t.split * dense_products(g);
-    p.tma_pre = aligned(g.part, g.N, 4);
-    if (p.tma_pre) ok = ok && encode(&maps.pre[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.part, g.N, g.M, g.N, planes, 32);
-  } else {
+  const int mode = g.epi.mode;
+  const int tile_rows = 128 * t.cg, cut = t.tiles - t.whole;
+  if (cut > 0)
+    ok = ok && encode(&maps.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, t.nt, static_cast<long long>(cut) * t.split * tile_rows,
+                      t.nt, 0, 32);
+  {
     const bool two = mode == EPI_GATED_BWD || g.batch > 1;
     const int es = f32 ? 4 : 2;
     const CUtensorMapDataType ytype = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type;
@@ -246,9 +279,14 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& given, int dt
     }
   }
   if (!ok) return cudaErrorInvalidValue;
-  if (f32) return launch_dense_tc32(mode, g.a_mn, g.b_mn, p, maps, t.blocks, s);
-  return dtype == CONV_F16 ? launch_dense_tc_f16(t, mode, g.a_mn, g.b_mn, p, maps, s)
-                           : launch_dense_tc_bf16(t, mode, g.a_mn, g.b_mn, p, maps, s);
+  const cudaError_t err = f32 ? launch_dense_tc32(mode, g.a_mn, g.b_mn, p, maps, t.blocks, s)
+                          : dtype == CONV_F16 ? launch_dense_tc_f16(t, mode, g.a_mn, g.b_mn, p, maps, s)
+                                              : launch_dense_tc_bf16(t, mode, g.a_mn, g.b_mn, p, maps, s);
+  if (err != cudaSuccess || cut == 0) return err;
+  const long long threads = static_cast<long long>(cut) * tile_rows * (cols / 4);
+  const dim3 grid(static_cast<unsigned>((threads + 255) / 256));
+  auto join = f32 ? dense_join<float> : dtype == CONV_F16 ? dense_join<__half> : dense_join<__nv_bfloat16>;
+  return launch_overlapped(join, grid, 256, 0, 1, s, p, static_cast<const float*>(part), tile_rows, g.dual);
 }
 
 cudaError_t dense_error_word(uint32_t* word, int reset) {

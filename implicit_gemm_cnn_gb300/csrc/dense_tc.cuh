@@ -29,7 +29,8 @@ namespace conv {
 struct DenseTcMaps {
   CUtensorMap a[2], b[2];
   CUtensorMap y[2];    // outputs, boxes of 32 columns x 32 rows
-  CUtensorMap pre[2];  // float32 g and u, the activation's argument, or the ranges' planes: 32 x 32
+  CUtensorMap pre[2];  // float32 g and u, or the activation's argument: 32 x 32
+  CUtensorMap part;    // the k ranges' raw sums: 32 x 32
 };
 
 struct DenseTcArgs {
@@ -39,11 +40,12 @@ struct DenseTcArgs {
   int a_3d, b_3d;           // mn-major: all of a stage's 64-wide boxes in one copy
   int kb_seg;               // 64-term blocks of a segment
   int kb_total, kb_range;   // of the sum; of a k range
-  int split;
-  int mtiles, ntiles, tiles, units, group;
+  // Units of work: `whole` tiles with their epilogue, then the others (the last, partly filled round of blocks) as
+  // `split` k ranges each, whose raw sums go to `part`, one tile after another (a second kernel adds them)
+  int whole, split, units;
+  int mtiles, ntiles, group;
   int tma_y, tma_pre;       // those outputs lie on 16-byte boundaries: written by TMA
   DenseEpi epi;
-  float* part;
   uint32_t* err;
 };
 
@@ -148,11 +150,6 @@ __device__ __forceinline__ void store_2d_once(const void* map, uint32_t src, int
 __device__ __forceinline__ void store_2d(const void* map, uint32_t src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(c0),
                "r"(c1), "r"(src)
-               : "memory");
-}
-__device__ __forceinline__ void store_3d(const void* map, uint32_t src, int c0, int c1, int c2) {
-  asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];\n" ::"l"(map),
-               "r"(c0), "r"(c1), "r"(c2), "r"(src)
                : "memory");
 }
 // The MMAs of one 64-term stage, then the arrival on `bar` (of every block of the pair) when they are done.
@@ -270,15 +267,26 @@ __device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
 }
 
-// Where unit u's tile lies: blocks of `group` tile rows are walked column by
-// column, so that the tiles in flight share operands in L2.
+// Unit u: its tile (blocks of `group` tile rows are walked column by column, so that the tiles in flight share operands
+// in L2) and its 64-term blocks.
 struct Tile {
-  int m, n, batch, range;
+  int m, n, batch;
+  int slot;      // raw sums: the place in `part`; -1: the whole tile
+  int kb0, kbs;
 };
 __device__ __forceinline__ Tile tile_of(const DenseTcArgs& p, int u) {
   Tile t;
-  t.range = u / p.tiles;
-  int i = u - t.range * p.tiles;
+  int i = u;
+  t.slot = -1;
+  t.kb0 = 0;
+  t.kbs = p.kb_total;
+  if (u >= p.whole) {
+    t.slot = u - p.whole;
+    const int q = t.slot / p.split;
+    i = p.whole + q;
+    t.kb0 = (t.slot - q * p.split) * p.kb_range;
+    t.kbs = min(p.kb_range, p.kb_total - t.kb0);
+  }
   const int per = p.mtiles * p.ntiles;
   t.batch = i / per;
   i -= t.batch * per;
@@ -349,7 +357,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       bool ok = true;
       for (int u = first; u < p.units && ok; u += step) {
         const Tile t = tile_of(p, u);
-        const int kb0 = t.range * p.kb_range, kb1 = min(kb0 + p.kb_range, p.kb_total);
+        const int kb0 = t.kb0, kb1 = kb0 + t.kbs;
         const int m0 = t.m * (128 * CG) + static_cast<int>(rank) * 128;
         const int n0 = MODE == EPI_GATED ? t.n * out_cols : t.n * nt + static_cast<int>(rank) * b_rows;
         for (int kb = kb0; kb < kb1 && ok;) {
@@ -415,7 +423,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       uint32_t parity = 0;
       bool ok = true;
       for (int u = first; u < p.units && ok; u += step, ++tile_it) {
-        const int kb0 = u / p.tiles * p.kb_range, kbs = min(p.kb_range, p.kb_total - kb0);
+        const int kbs = tile_of(p, u).kbs;
         const int buf = tile_it & 1;
         if (!wait_phase(p.err, acc_empty(buf), ((tile_it >> 1) & 1) ^ 1, &abort_flag, 2u)) break;
         tc_fence_after();
@@ -490,24 +498,26 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
         bulk_commit();
       }
     };
-    // 32 float32 columns of this lane's row (plane >= 0: of the ranges' planes)
-    auto put32 = [&](const float (&v)[32], const CUtensorMap* map, float* out, long long ld, int n, int m_warp, int plane) {
+    // 32 float32 columns of this lane's row into a staging tile of 128-byte rows (128-byte swizzle)
+    auto stage32 = [&](uint32_t b, const float (&v)[32]) {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        sts_v4(b + lane * 128 + ((q ^ (lane & 7)) << 4),
+               make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
+                          __float_as_uint(v[4 * q + 3])));
+    };
+    auto put32 = [&](const float (&v)[32], const CUtensorMap* map, float* out, long long ld, int n, int m_warp) {
       if (p.tma_pre) {
         const uint32_t b = acquire(true);
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          sts_v4(b + lane * 128 + ((q ^ (lane & 7)) << 4),
-                 make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
-                            __float_as_uint(v[4 * q + 3])));
+        stage32(b, v);
         publish();
         if (lane == 0) {
-          if (plane >= 0) store_3d(map, b, n, m_warp, plane);
-          else store_2d_once(map, b, n, m_warp, once);
+          store_2d_once(map, b, n, m_warp, once);
           bulk_commit();
         }
       } else {
         // in two halves of 16 rows (33 words apart), which fit the staging tile
-        out += (plane >= 0 ? static_cast<long long>(plane) * p.M * p.N : 0) + static_cast<long long>(m_warp) * ld + n + lane;
+        out += static_cast<long long>(m_warp) * ld + n + lane;
         const uint32_t b = acquire(true);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
@@ -529,6 +539,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
     const bool vec_b = reinterpret_cast<uintptr_t>(e.bias) % 16 == 0;
     const int chunks = out_cols / 32, per_warp = (chunks + kParts - 1) / kParts;
     const int c0 = half * per_warp, c1 = min(c0 + per_warp, chunks);
+    const int raw0 = half * (nt / 32 / kParts), raw1 = kParts == 1 || half ? nt / 32 : raw0 + nt / 32 / kParts;
     int tile_it = 0, fetched = 0;
     for (int u = first; u < p.units; u += step, ++tile_it) {
       const Tile t = tile_of(p, u);
@@ -536,10 +547,11 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       const int m_warp = t.m * (128 * CG) + static_cast<int>(rank) * 128 + quarter * 32;
       const int m = m_warp + lane, n_tile = t.n * out_cols;
       // pieces that exist: this warp's rows, and columns below N
-      const int c_end = m_warp < p.M ? min(c1, (p.N - n_tile + 31) / 32) : c0;
+      const int c_end = t.slot < 0 && m_warp < p.M ? min(c1, (p.N - n_tile + 31) / 32) : c0;
       // g and u of a piece (a tile's first one is on its way before its sums are)
       auto fetch = [&](int c) {
         if (lane == 0) {
+          bulk_wait_read<0>();
           mbar_arrive_expect_tx(in_full(warp - 2), 2 * kBufBytes);
           load_2d_once(mine, &maps.pre[0], n_tile + 32 * c, m_warp, in_full(warp - 2), once);
           load_2d_once(mine + kBufBytes, &maps.pre[1], n_tile + 32 * c, m_warp, in_full(warp - 2), once);
@@ -553,7 +565,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       };
       if (MODE == EPI_LINEAR && e.residual) fetch_residual(c0);
       if (!warp_wait(p.err, acc_full(buf), (tile_it >> 1) & 1, &abort_flag, 8u, false, 128,
-                      kWaitNs + 1000ull * p.kb_range)) {  // a stage takes below a microsecond
+                      kWaitNs + 1000ull * p.kb_total)) {  // a stage takes below a microsecond
         if (MODE == EPI_GATED_BWD && c0 < c_end)  // the copies under way land before the block ends
           warp_wait(p.err, in_full(warp - 2), fetched & 1, &abort_flag, 16u, true);
         break;
@@ -561,23 +573,36 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       __syncwarp();
       tc_fence_after();
       const uint32_t acc = tmem + buf * NT + (static_cast<uint32_t>(quarter * 32) << 16);
+      if (t.slot >= 0 && m_warp < p.M) {  // a k range: its sums as they are
+        const int row = t.slot * (128 * CG) + static_cast<int>(rank) * 128 + quarter * 32;
+#pragma unroll 1
+        for (int c = raw0; c < raw1; ++c) {
+          float v[32];
+          tmem_ld32(acc + 32 * c, v);
+          tmem_arrived(v);
+          const uint32_t b = acquire(true);
+          stage32(b, v);
+          publish();
+          if (lane == 0) {
+            store_2d(&maps.part, b, 32 * c, row);
+            bulk_commit();
+          }
+        }
+      }
 #pragma unroll 1
       for (int c = c0; c < c_end; ++c) {
         const int n = n_tile + 32 * c, left = p.N - n;
         float v[32];
         uint32_t w[16];
         tmem_ld32(acc + 32 * c, v);
-        if constexpr (MODE == EPI_PARTIAL) {
-          tmem_arrived(v);
-          put32(v, &maps.pre[0], p.part, p.N, n, m_warp, t.range * p.batch + t.batch);
-        } else if constexpr (MODE == EPI_GATED) {
+        if constexpr (MODE == EPI_GATED) {
           float g[32];
           tmem_ld32(acc + nt / 2 + 32 * c, g);
           tmem_arrived(v);
           tmem_arrived(g);
           if (e.pre) {
-            put32(v, &maps.pre[0], e.pre, e.ldp, n, m_warp, -1);
-            put32(g, &maps.pre[1], e.pre2, e.ldp, n, m_warp, -1);
+            put32(v, &maps.pre[0], e.pre, e.ldp, n, m_warp);
+            put32(g, &maps.pre[1], e.pre2, e.ldp, n, m_warp);
           }
           dense_activate<true, 32>(v, e.act, e.alpha, e.beta);
 #pragma unroll
@@ -613,7 +638,6 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
             store_2d_once(&maps.y[0], mine, n, m_warp, once);
             store_2d_once(&maps.y[1], mine + kBufBytes / 2, n, m_warp, once);
             bulk_commit();
-            bulk_wait_read<0>();
           }
           if (c + 1 < c_end) fetch(c + 1);
         } else {
@@ -625,7 +649,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
             add_row32<T>(v, res);
             fetch_residual(c + 1);
           }
-          if (e.pre) put32(v, &maps.pre[0], e.pre, e.ldp, n, m_warp, -1);
+          if (e.pre) put32(v, &maps.pre[0], e.pre, e.ldp, n, m_warp);
           dense_activate<true, 32>(v, e.act, e.alpha, e.beta);
           if (e.residual && e.residual_last) {
             add_row32<T>(v, res);

@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
       bool ok = true;
       for (int u = first; u < p.units && ok; u += step) {
         const Tile t = tile_of(p, u);
-        const int kb0 = t.range * p.kb_range, kb1 = min(kb0 + p.kb_range, p.kb_total);
+        const int kb0 = t.kb0, kb1 = kb0 + t.kbs;
         const int m0 = t.m * 128, n0 = t.n * out_cols;
         for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_phase(p.err, empty(s), parity, &abort_flag, 1u)) {
@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
       uint32_t parity = 0;
       bool ok = true;
       for (int u = first; u < p.units && ok; u += step) {
-        const int kb0 = u / p.tiles * p.kb_range, kbs = min(p.kb_range, p.kb_total - kb0);
+        const int kbs = tile_of(p, u).kbs;
         for (int kb = 0; kb < kbs; ++kb, ++it) {
           const int buf = it & 1;
           if (!wait_phase(p.err, acc_empty(buf), ((it >> 1) & 1) ^ 1, &abort_flag, 2u) ||
@@ -170,8 +170,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
     const DenseEpi& e = p.epi;
     int turn = 0, it = 0;
     // 32 float32 columns of this lane's row
-    auto put = [&](const float (&v)[32], const CUtensorMap* map, float* out, long long ld, bool tma, int n, int m_warp,
-                   int plane) {
+    auto put = [&](const float (&v)[32], const CUtensorMap* map, float* out, long long ld, bool tma, int n, int m_warp) {
       if (tma) {
         if (lane == 0) bulk_wait_read<1>();
         __syncwarp();
@@ -185,8 +184,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
-          if (plane >= 0) store_3d(map, b, n, m_warp, plane);
-          else store_2d(map, b, n, m_warp);
+          store_2d(map, b, n, m_warp);
           bulk_commit();
         }
       } else {
@@ -197,7 +195,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
 #pragma unroll
         for (int i = 0; i < 32; ++i) tile[lane * 33 + i] = v[i];
         __syncwarp();
-        out += (plane >= 0 ? static_cast<long long>(plane) * p.M * p.N : 0) + static_cast<long long>(m_warp) * ld + n;
+        out += static_cast<long long>(m_warp) * ld + n;
         const int rows = min(32, p.M - m_warp);
         if (n + lane < p.N)
           for (int r = 0; r < rows; ++r) out[r * ld + lane] = tile[r * 33 + lane];
@@ -221,7 +219,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
     };
     for (int u = first; u < p.units; u += step) {
       const Tile t = tile_of(p, u);
-      const int kb0 = t.range * p.kb_range, kbs = min(p.kb_range, p.kb_total - kb0);
+      const int kbs = t.kbs;
       const int m_warp = t.m * 128 + quarter * 32, m = m_warp + lane, n_tile = t.n * out_cols;
       float acc[4][32];
 #pragma unroll
@@ -253,6 +251,12 @@ __global__ void __launch_bounds__(kThreads32, 1)
       }
       if (!ok) break;
       if (m_warp >= p.M) continue;
+      if (t.slot >= 0) {  // a k range: its sums as they are
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (32 * c < nt) put(acc[c], &maps.part, nullptr, 0, true, 32 * c, t.slot * 128 + quarter * 32);
+        continue;
+      }
       // one copy of the code for all pieces: the next piece's sums move into acc[0]
 #pragma unroll 1
       for (int c = 0; 32 * c < out_cols; ++c) {
@@ -267,21 +271,19 @@ __global__ void __launch_bounds__(kThreads32, 1)
         const int n = n_tile + 32 * c, left = p.N - n;
         if (left <= 0) break;
         const bool row_ok = m < p.M;
-        if constexpr (MODE == EPI_PARTIAL) {
-          put(acc[0], &maps.pre[0], p.part, p.N, p.tma_pre, n, m_warp, t.range * p.batch + t.batch);
-        } else if constexpr (MODE == EPI_GATED) {
+        if constexpr (MODE == EPI_GATED) {
           // gate columns are the tile's first half, up columns its second
           float up[32];
 #pragma unroll
           for (int i = 0; i < 32; ++i) up[i] = nt == 64 ? acc[1][i] : acc[2][i];
           if (e.pre) {
-            put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp, -1);
-            put(up, &maps.pre[1], e.pre2, e.ldp, p.tma_pre, n, m_warp, -1);
+            put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp);
+            put(up, &maps.pre[1], e.pre2, e.ldp, p.tma_pre, n, m_warp);
           }
           activate(acc[0]);
 #pragma unroll
           for (int i = 0; i < 32; ++i) up[i] *= acc[0][i];
-          put(up, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.tma_y, n, m_warp, -1);
+          put(up, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.tma_y, n, m_warp);
         } else if constexpr (MODE == EPI_GATED_BWD) {
           float g[32], slope[32];
           const float* gp = e.pre + static_cast<long long>(m) * e.ldp + n;
@@ -294,17 +296,17 @@ __global__ void __launch_bounds__(kThreads32, 1)
             slope[i] *= acc[0][i] * (row_ok && i < left ? up[i] : 0.0f);
             g[i] *= acc[0][i];
           }
-          put(slope, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.tma_y, n, m_warp, -1);
-          put(g, &maps.y[1], static_cast<float*>(e.y2), e.ldy, p.tma_y, n, m_warp, -1);
+          put(slope, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.tma_y, n, m_warp);
+          put(g, &maps.y[1], static_cast<float*>(e.y2), e.ldy, p.tma_y, n, m_warp);
         } else {
           const float* res = e.residual && row_ok ? static_cast<const float*>(e.residual) + static_cast<long long>(m) * e.ldr + n
                                                   : nullptr;
           if (e.bias) add_row(acc[0], static_cast<const float*>(e.bias) + n, left);
           if (res && !e.residual_last) add_row(acc[0], res, left);
-          if (e.pre) put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp, -1);
+          if (e.pre) put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp);
           activate(acc[0]);
           if (res && e.residual_last) add_row(acc[0], res, left);
-          put(acc[0], &maps.y[t.batch], static_cast<float*>(t.batch ? e.y2 : e.y), e.ldy, p.tma_y, n, m_warp, -1);
+          put(acc[0], &maps.y[t.batch], static_cast<float*>(t.batch ? e.y2 : e.y), e.ldy, p.tma_y, n, m_warp);
         }
       }
     }
@@ -342,7 +344,6 @@ cudaError_t launch_dense_tc32(int mode, int a_mn, int b_mn, const DenseTcArgs& a
       return a_mn || b_mn ? cudaErrorInvalidValue : go32<EPI_GATED, false, false>(args, maps, blocks, s);
     case EPI_GATED_BWD:
       return a_mn || !b_mn ? cudaErrorInvalidValue : go32<EPI_GATED_BWD, false, true>(args, maps, blocks, s);
-    case EPI_PARTIAL: return order32<EPI_PARTIAL>(a_mn, b_mn, args, maps, blocks, s);
     default: return order32<EPI_LINEAR>(a_mn, b_mn, args, maps, blocks, s);
   }
 }

@@ -31,7 +31,6 @@ cudaError_t by_mode(int mode, int a_mn, int b_mn, const DenseTcArgs& args, const
       return a_mn || b_mn ? cudaErrorInvalidValue : go<T, CG, NT, EPI_GATED, false, false>(args, maps, blocks, s);
     case EPI_GATED_BWD:
       return a_mn || !b_mn ? cudaErrorInvalidValue : go<T, CG, NT, EPI_GATED_BWD, false, true>(args, maps, blocks, s);
-    case EPI_PARTIAL: return by_order<T, CG, NT, EPI_PARTIAL>(a_mn, b_mn, args, maps, blocks, s);
     default: return by_order<T, CG, NT, EPI_LINEAR>(a_mn, b_mn, args, maps, blocks, s);
   }
 }
