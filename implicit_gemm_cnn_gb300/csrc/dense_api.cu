@@ -73,7 +73,7 @@ conv_status validate(const conv_gated_problem* p, GatedShape* s) {
   if (!stride_of(p->x_stride, p->c_in, &s->ldx) || !stride_of(p->residual_stride, p->c_out, &s->ldr) ||
       !stride_of(p->y_stride, p->c_out, &s->ldy))
     return CONV_ERR_SHAPE;
-  s->ldh = round8(p->hidden);
+  s->ldh = (p->hidden + 15) / 16 * 16;  // 32-byte rows
   if (!elems_ok(p->rows, s->ldx) || !elems_ok(p->rows, s->ldy) || (p->has_residual && !elems_ok(p->rows, s->ldr)) ||
       !elems_ok(p->rows, s->ldh) || !elems_ok(round8(p->c_in), s->ldh) || !elems_ok(round8(p->c_out), s->ldh))
     return CONV_ERR_OVERFLOW;

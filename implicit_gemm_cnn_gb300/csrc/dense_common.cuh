@@ -66,10 +66,21 @@ __device__ __forceinline__ float dense_sigmoid(float t) {
   if constexpr (FAST) return __fdividef(1.0f, 1.0f + __expf(-t));
   else return sigmoid_f32(t);
 }
+// Phi(t) and exp(-t^2 / 2) for results of 16 bits: the rational approximation of erf of Abramowitz and Stegun, Handbook of
+// Mathematical Functions, 7.1.26 (error below 1.5e-7), with x = |t| / sqrt(2); one exponential, one reciprocal.
+__device__ __forceinline__ float dense_cdf_fast(float t, float* e) {
+  const float x = fabsf(t) * 0.70710678f;
+  const float k = __fdividef(1.0f, fmaf(0.3275911f, x, 1.0f));
+  *e = __expf(-x * x);
+  const float poly = k * fmaf(k, fmaf(k, fmaf(k, fmaf(k, 1.061405429f, -1.453152027f), 1.421413741f), -0.284496736f), 0.254829592f);
+  const float tail = 0.5f * poly * *e;  // Phi(-|t|)
+  return t >= 0.0f ? 1.0f - tail : tail;
+}
 template <int ACT, bool FAST>
 __device__ __forceinline__ float dense_act_fn(float t, float alpha, float beta) {
   if constexpr (ACT == ACT_GELU) {
-    if constexpr (FAST) return 0.5f * t * (1.0f + erff(t * 0.70710678f));
+    float e;
+    if constexpr (FAST) return t * dense_cdf_fast(t, &e);
     else return t * normcdff(t);
   } else if constexpr (ACT == ACT_GELU_TANH) {
     // t/2 (1 + tanh v) = t * sigmoid(2v)
@@ -100,9 +111,14 @@ __device__ __forceinline__ float dense_act_grad(float t, float alpha, float beta
   else if constexpr (ACT == ACT_LEAKY_RELU) return t >= 0.0f ? 1.0f : (t == t ? alpha : t);
   else if constexpr (ACT == ACT_GELU) {
     const float c = fminf(fmaxf(t, -40.0f), 40.0f);
-    const float cdf = FAST ? 0.5f * (1.0f + erff(t * 0.70710678f)) : normcdff(t);
-    const float pdf = 0.3989422804f * (FAST ? __expf(-0.5f * c * c) : expf(-0.5f * c * c));
-    return fmaf(c, pdf, cdf);
+    float e, cdf;
+    if constexpr (FAST) {
+      cdf = dense_cdf_fast(t, &e);
+    } else {
+      cdf = normcdff(t);
+      e = expf(-0.5f * c * c);
+    }
+    return fmaf(c, 0.3989422804f * e, cdf);
   } else if constexpr (ACT == ACT_GELU_TANH) {
     const float c = fminf(fmaxf(t, -40.0f), 40.0f);
     const float s = dense_sigmoid<FAST>(1.5957691216f * t * fmaf(0.044715f * t, t, 1.0f));

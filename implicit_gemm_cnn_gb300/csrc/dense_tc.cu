@@ -97,9 +97,6 @@ bool encode_planes(CUtensorMap* map, const void* base, long long inner, long lon
                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-bool aligned(const void* p, long long ld, size_t es) {
-  return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld * static_cast<long long>(es) % 16 == 0;
-}
 
 // The tile and the k ranges of least time by this model, in clocks, fitted to full waves of 4096-term sums (bfloat16,
 // 1.85 GHz): 64 terms of a pair's tile take 165 + 1.73 nt (608 at nt = 256, 386 at 128: 512 and 256 are the MMAs
@@ -255,27 +252,28 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype,
   for (int i = 0; i < bs; ++i) ok = ok && operand(&maps.b[i], g.b[i], g.b_mn, p.b_3d, g.N, g.ldb, b_rows, b_rows / 64);
   const int mode = g.epi.mode;
   const int tile_rows = 128 * t.cg, cut = t.tiles - t.whole;
-  if (cut > 0)
-    ok = ok && encode(&maps.part, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, part, t.nt, static_cast<long long>(cut) * t.split * tile_rows,
-                      t.nt, 0, 32);
-  {
-    const bool two = mode == EPI_GATED_BWD || g.batch > 1;
-    const int es = f32 ? 4 : 2;
-    const CUtensorMapDataType ytype = f32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type;
-    p.tma_y = aligned(g.epi.y, g.epi.ldy, es) && (!two || aligned(g.epi.y2, g.epi.ldy, es));
-    if (p.tma_y) {
-      ok = ok && encode(&maps.y[0], ytype, g.epi.y, g.N, g.M, g.epi.ldy, 0, 32, 32 * es);
-      if (two) ok = ok && encode(&maps.y[1], ytype, g.epi.y2, g.N, g.M, g.epi.ldy, 0, 32, 32 * es);
+  const bool two = mode == EPI_GATED_BWD || g.batch > 1, saves = mode != EPI_GATED_BWD && g.epi.pre;
+  const int es = f32 ? 4 : 2;
+  auto align = [](const void* a, const void* b, long long row_bytes) {
+    const uintptr_t all = reinterpret_cast<uintptr_t>(a) | reinterpret_cast<uintptr_t>(b) | static_cast<uintptr_t>(row_bytes);
+    return all % 32 == 0 ? 32 : all % 16 == 0 ? 16 : 0;
+  };
+  p.align_y = align(g.epi.y, two ? g.epi.y2 : nullptr, g.epi.ldy * es);
+  p.align_pre = align(g.epi.pre, mode == EPI_LINEAR ? nullptr : g.epi.pre2, g.epi.ldp * 4);
+  if (mode == EPI_GATED_BWD && (p.align_pre != 32 || !p.align_y)) return cudaErrorInvalidValue;  // the library's own layout
+  p.part = static_cast<float*>(part);
+  if (f32) {
+    auto out = [&](CUtensorMap* map, const void* base, long long cols, long long rows, long long ld) {
+      return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, cols, rows, ld, 0, 32);
+    };
+    if (cut > 0) ok = ok && out(&maps.part, part, t.nt, static_cast<long long>(cut) * t.split * tile_rows, t.nt);
+    if (p.align_y) {
+      ok = ok && out(&maps.y[0], g.epi.y, g.N, g.M, g.epi.ldy);
+      if (two) ok = ok && out(&maps.y[1], g.epi.y2, g.N, g.M, g.epi.ldy);
     }
-    if (mode == EPI_GATED_BWD && !(p.tma_y && aligned(g.epi.pre, g.epi.ldp, 4) && aligned(g.epi.pre2, g.epi.ldp, 4)))
-      return cudaErrorInvalidValue;  // the library's own layout
-    if (g.epi.pre) {
-      p.tma_pre = aligned(g.epi.pre, g.epi.ldp, 4);
-      if (p.tma_pre) {
-        ok = ok && encode(&maps.pre[0], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.epi.pre, g.N, g.M, g.epi.ldp, 0, 32);
-        if (mode != EPI_LINEAR)
-          ok = ok && encode(&maps.pre[1], CU_TENSOR_MAP_DATA_TYPE_FLOAT32, g.epi.pre2, g.N, g.M, g.epi.ldp, 0, 32);
-      }
+    if (saves && p.align_pre) {
+      ok = ok && out(&maps.pre[0], g.epi.pre, g.N, g.M, g.epi.ldp);
+      if (mode == EPI_GATED) ok = ok && out(&maps.pre[1], g.epi.pre2, g.N, g.M, g.epi.ldp);
     }
   }
   if (!ok) return cudaErrorInvalidValue;

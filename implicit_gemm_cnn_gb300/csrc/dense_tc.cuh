@@ -15,8 +15,8 @@
 // fly), so neither the layer nor its two gradients need a transposed copy.  The
 // gated product loads half a tile of gate columns and half a tile of up
 // columns as one B: g and u of an element arrive in one lane of one
-// accumulator.  Edges need no code: TMA fills zeros past a matrix's end and
-// does not write past the output's.
+// accumulator.  TMA fills zeros past a matrix's end, so edges need no code in the
+// loops.
 #pragma once
 
 #include <cuda.h>
@@ -28,9 +28,7 @@ namespace conv {
 
 struct DenseTcMaps {
   CUtensorMap a[2], b[2];
-  CUtensorMap y[2];    // outputs, boxes of 32 columns x 32 rows
-  CUtensorMap pre[2];  // float32 g and u, or the activation's argument: 32 x 32
-  CUtensorMap part;    // the k ranges' raw sums: 32 x 32
+  CUtensorMap y[2], pre[2], part;  // float32 products: the outputs, boxes of 32 columns x 32 rows
 };
 
 struct DenseTcArgs {
@@ -44,8 +42,9 @@ struct DenseTcArgs {
   // `split` k ranges each, whose raw sums go to `part`, one tile after another (a second kernel adds them)
   int whole, split, units;
   int mtiles, ntiles, group;
-  int tma_y, tma_pre;       // those outputs lie on 16-byte boundaries: written by TMA
+  int align_y, align_pre;   // the rows' boundaries: 32 or 16 bytes, 0: neither
   DenseEpi epi;
+  float* part;
   uint32_t* err;
 };
 
@@ -53,16 +52,15 @@ namespace dtc {
 using namespace tcx;
 
 constexpr int kBK = 64;
-constexpr int kBufBytes = 4096;  // a staging tile: 32 rows of 32 float32, or two of 32 16-bit values
+constexpr int kBufBytes = 2304;  // a warp's staging: 32 rows of 32 16-bit values, or 16 of 32 float32, a word apart
 
-template <int CG, int NT, int MODE>
+template <int CG, int NT>
 struct Cfg {
   static constexpr int kEpiWarps = NT >= 256 ? 8 : 4;
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kABytes = 128 * 128;
   static constexpr int kStageBytes = kABytes + NT / CG * 128;
-  static constexpr int kWarpBufs = MODE == EPI_GATED_BWD ? 2 : 1;  // g and u, whose place the outputs take; or outputs alone
-  static constexpr int kStaging = kEpiWarps * kWarpBufs * kBufBytes;
+  static constexpr int kStaging = kEpiWarps * kBufBytes;
   static constexpr int kFit = (232448 - 2048 - kStaging) / kStageBytes;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kSmem = kStages * kStageBytes + kStaging + 2032;  // 1024 to align, the rest for barriers
@@ -128,24 +126,47 @@ __device__ __forceinline__ void load_3d(uint32_t dst, const void* map, int c0, i
         "[%5];\n" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
         : "memory");
 }
-// What an epilogue reads or writes passes through L2 once: it is the first to go, so that the operands' tiles, which are
-// read by many blocks, stay.
-__device__ __forceinline__ uint64_t once_policy() {
-  uint64_t p;
-  asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;\n" : "=l"(p));
-  return p;
-}
-__device__ __forceinline__ void load_2d_once(uint32_t dst, const void* map, int c0, int c1, uint32_t bar, uint64_t policy) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint [%0], [%1, {%2, "
-      "%3}], [%4], %5;\n" ::"r"(dst), "l"(map), "r"(c0), "r"(c1), "r"(bar), "l"(policy)
-      : "memory");
-}
-__device__ __forceinline__ void store_2d_once(const void* map, uint32_t src, int c0, int c1, uint64_t policy) {
-  asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group.L2::cache_hint [%0, {%1, %2}], [%3], %4;\n" ::"l"(
-                   map),
-               "r"(c0), "r"(c1), "r"(src), "l"(policy)
+// 32 bytes from or to global memory (on a 32-byte boundary).  What an epilogue reads or writes passes through L2 once: it
+// is the first to go, so that the operands' tiles, which are read by many blocks, stay.
+__device__ __forceinline__ void load_32b(const void* p, uint32_t* r) {
+  asm volatile("ld.global.L2::evict_first.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];\n"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "l"(p)
                : "memory");
+}
+__device__ __forceinline__ void store_32b(void* p, const uint32_t* r) {
+  asm volatile("st.global.L2::evict_first.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};\n" ::"l"(p), "r"(r[0]), "r"(r[1]),
+               "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+__device__ __forceinline__ void store_16b(void* p, const uint32_t* r) {
+  asm volatile("st.global.v4.b32 [%0], {%1, %2, %3, %4};\n" ::"l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]) : "memory");
+}
+__device__ __forceinline__ void prefetch_l2(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];\n" ::"l"(p) : "memory");
+}
+// 32 values of B bytes each (packed into words) of a row, `left` of which exist, on boundaries of `align` (16 or 32)
+// bytes.
+template <int B>
+__device__ __forceinline__ void store_row32(uint8_t* row, const uint32_t (&w)[8 * B], int left, int align) {
+  constexpr int kPer = 32 / B;  // values of 32 bytes
+#pragma unroll
+  for (int j = 0; j < B; ++j) {
+    if (left >= kPer * (j + 1)) {
+      if (align == 32) store_32b(row + 32 * j, w + 8 * j);
+      else {
+        store_16b(row + 32 * j, w + 8 * j);
+        store_16b(row + 32 * j + 16, w + 8 * j + 4);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (kPer * j + i < left) {
+          if constexpr (B == 4) reinterpret_cast<uint32_t*>(row)[kPer * j + i] = w[8 * j + i];
+          else reinterpret_cast<uint16_t*>(row)[kPer * j + i] = static_cast<uint16_t>(w[8 * j + i / 2] >> (16 * (i & 1)));
+        }
+    }
+  }
 }
 __device__ __forceinline__ void store_2d(const void* map, uint32_t src, int c0, int c1) {
   asm volatile("cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n" ::"l"(map), "r"(c0),
@@ -299,9 +320,9 @@ __device__ __forceinline__ Tile tile_of(const DenseTcArgs& p, int u) {
 }
 
 template <typename T, int CG, int NT, int MODE, bool A_MN, bool B_MN>
-__global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
+__global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
     dense_tc(const __grid_constant__ DenseTcArgs p, const __grid_constant__ DenseTcMaps maps) {
-  using C = Cfg<CG, NT, MODE>;
+  using C = Cfg<CG, NT>;
   const int nt = p.nt, out_cols = MODE == EPI_GATED ? nt / 2 : nt;  // a tile's columns of the output
   const int b_rows = nt / CG;                                      // rows of B in this block
   extern __shared__ uint8_t smem_raw[];
@@ -315,7 +336,6 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
   auto empty = [&](int s) { return bars + 8u * (C::kStages + s); };
   auto acc_full = [&](int b) { return bars + 8u * (2 * C::kStages + b); };
   auto acc_empty = [&](int b) { return bars + 8u * (2 * C::kStages + 2 + b); };
-  auto in_full = [&](int w) { return bars + 8u * (2 * C::kStages + 4 + w); };  // a warp's g and u
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x / 32, 0), lane = threadIdx.x % 32;
   const uint32_t rank = CG == 2 ? cluster_rank() : 0;
 
@@ -328,8 +348,6 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       mbar_init(acc_full(b), 1);
       mbar_init(acc_empty(b), C::kEpiWarps * CG);
     }
-    if (MODE == EPI_GATED_BWD)
-      for (int w = 0; w < C::kEpiWarps; ++w) mbar_init(in_full(w), 1);
     abort_flag = 0;
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     fence_proxy_async();
@@ -446,93 +464,49 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     constexpr int kParts = C::kEpiWarps / 4;       // warps that share a quarter's columns
-    const uint32_t mine = staging + (warp - 2) * C::kWarpBufs * kBufBytes;
+    const uint32_t mine = staging + (warp - 2) * kBufBytes;
     const DenseEpi& e = p.epi;
-    const uint64_t once = once_policy();
-    // The outputs' staging tile: one float32 piece, or two 16-bit ones in turn.  A piece waits until the stores that
-    // read its place have done so: the last but one's if both are 16-bit, else the last one's.
-    const uint32_t out_buf = mine;
-    int turn = 0;
-    bool last_wide = true;
-    auto acquire = [&](bool wide) {
-      if (lane == 0) {
-        if (wide || last_wide) bulk_wait_read<0>();
-        else bulk_wait_read<1>();
+    // A lane holds 32 columns of one row.  On 16-byte boundaries it writes them itself, in whole sectors: nothing to wait
+    // for.  (Staged tiles that TMA stores took 400 to 1300 clocks each until their place was free again.)  Rows of other
+    // alignments go through shared memory: a store instruction covers 32 consecutive columns of one row.
+    auto put16 = [&](const uint32_t (&w)[16], T* y, int n, int left, int m_warp) {
+      if (p.align_y) {
+        if (m_warp + lane < p.M)
+          store_row32<2>(reinterpret_cast<uint8_t*>(y + static_cast<long long>(m_warp + lane) * e.ldy + n), w, left, p.align_y);
+        return;
       }
-      last_wide = wide;
-      __syncwarp();
-      turn ^= wide ? 0 : 1;
-      return wide ? out_buf : out_buf + turn * (kBufBytes / 2);
-    };
-    auto publish = [&]() {
-      fence_proxy_async();
-      __syncwarp();
-    };
-    // 32 16-bit columns of this lane's row into a staging tile of 64-byte rows (64-byte swizzle)
-    auto stage16 = [&](uint32_t b, const uint32_t (&w)[16]) {
 #pragma unroll
-      for (int q = 0; q < 4; ++q)
-        sts_v4(b + lane * 64 + ((q ^ ((lane >> 1) & 3)) << 4), make_uint4(w[4 * q], w[4 * q + 1], w[4 * q + 2], w[4 * q + 3]));
-    };
-    // rows of any alignment: through shared memory, a store instruction covers 32 consecutive columns of one row
-    auto plain16 = [&](const uint32_t (&w)[16], T* y, int n, int m_warp) {
-      const uint32_t b = acquire(true);
-#pragma unroll
-      for (int i = 0; i < 16; ++i) sts_u32(b + lane * 68 + 4 * i, w[i]);
+      for (int i = 0; i < 16; ++i) sts_u32(mine + lane * 68 + 4 * i, w[i]);
       __syncwarp();
       uint16_t* out = reinterpret_cast<uint16_t*>(y + static_cast<long long>(m_warp) * e.ldy + n) + lane;
       const int rows = min(32, p.M - m_warp);
-      if (n + lane < p.N) {
+      if (lane < left) {
 #pragma unroll 8
-        for (int r = 0; r < rows; ++r) out[r * e.ldy] = lds_u16(b + r * 68 + 2 * lane);
+        for (int r = 0; r < rows; ++r) out[r * e.ldy] = lds_u16(mine + r * 68 + 2 * lane);
       }
       __syncwarp();
     };
-    auto put16 = [&](const uint32_t (&w)[16], const CUtensorMap* map, T* y, int n, int m_warp) {
-      if (!p.tma_y) return plain16(w, y, n, m_warp);
-      const uint32_t b = acquire(false);
-      stage16(b, w);
-      publish();
-      if (lane == 0) {
-        store_2d_once(map, b, n, m_warp, once);
-        bulk_commit();
+    auto put32 = [&](const float (&v)[32], float* out, int n, int left, int m_warp) {
+      if (p.align_pre) {
+        if (m_warp + lane < p.M)
+          store_row32<4>(reinterpret_cast<uint8_t*>(out + static_cast<long long>(m_warp + lane) * e.ldp + n),
+                         reinterpret_cast<const uint32_t(&)[32]>(v), left, p.align_pre);
+        return;
       }
-    };
-    // 32 float32 columns of this lane's row into a staging tile of 128-byte rows (128-byte swizzle)
-    auto stage32 = [&](uint32_t b, const float (&v)[32]) {
+      out += static_cast<long long>(m_warp) * e.ldp + n + lane;
 #pragma unroll
-      for (int q = 0; q < 8; ++q)
-        sts_v4(b + lane * 128 + ((q ^ (lane & 7)) << 4),
-               make_uint4(__float_as_uint(v[4 * q]), __float_as_uint(v[4 * q + 1]), __float_as_uint(v[4 * q + 2]),
-                          __float_as_uint(v[4 * q + 3])));
-    };
-    auto put32 = [&](const float (&v)[32], const CUtensorMap* map, float* out, long long ld, int n, int m_warp) {
-      if (p.tma_pre) {
-        const uint32_t b = acquire(true);
-        stage32(b, v);
-        publish();
-        if (lane == 0) {
-          store_2d_once(map, b, n, m_warp, once);
-          bulk_commit();
+      for (int h = 0; h < 2; ++h) {  // 16 rows at a time
+        if (lane / 16 == h) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) sts_u32(mine + (lane % 16) * 132 + 4 * i, __float_as_uint(v[i]));
         }
-      } else {
-        // in two halves of 16 rows (33 words apart), which fit the staging tile
-        out += static_cast<long long>(m_warp) * ld + n + lane;
-        const uint32_t b = acquire(true);
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-          if (lane / 16 == h) {
-#pragma unroll
-            for (int i = 0; i < 32; ++i) sts_u32(b + (lane % 16) * 132 + 4 * i, __float_as_uint(v[i]));
-          }
-          __syncwarp();
-          const int rows = min(16, p.M - m_warp - 16 * h);
-          if (n + lane < p.N) {
+        __syncwarp();
+        const int rows = min(16, p.M - m_warp - 16 * h);
+        if (lane < left) {
 #pragma unroll 8
-            for (int r = 0; r < rows; ++r) out[(16 * h + r) * ld] = lds_f32(b + r * 132 + 4 * lane);
-          }
-          __syncwarp();
+          for (int r = 0; r < rows; ++r) out[(16 * h + r) * e.ldp] = lds_f32(mine + r * 132 + 4 * lane);
         }
+        __syncwarp();
       }
     };
     const bool vec_r = e.ldr % 8 == 0 && reinterpret_cast<uintptr_t>(e.residual) % 16 == 0;
@@ -540,7 +514,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
     const int chunks = out_cols / 32, per_warp = (chunks + kParts - 1) / kParts;
     const int c0 = half * per_warp, c1 = min(c0 + per_warp, chunks);
     const int raw0 = half * (nt / 32 / kParts), raw1 = kParts == 1 || half ? nt / 32 : raw0 + nt / 32 / kParts;
-    int tile_it = 0, fetched = 0;
+    int tile_it = 0;
     for (int u = first; u < p.units; u += step, ++tile_it) {
       const Tile t = tile_of(p, u);
       const int buf = tile_it & 1;
@@ -548,16 +522,15 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       const int m = m_warp + lane, n_tile = t.n * out_cols;
       // pieces that exist: this warp's rows, and columns below N
       const int c_end = t.slot < 0 && m_warp < p.M ? min(c1, (p.N - n_tile + 31) / 32) : c0;
-      // g and u of a piece (a tile's first one is on its way before its sums are)
-      auto fetch = [&](int c) {
-        if (lane == 0) {
-          bulk_wait_read<0>();
-          mbar_arrive_expect_tx(in_full(warp - 2), 2 * kBufBytes);
-          load_2d_once(mine, &maps.pre[0], n_tile + 32 * c, m_warp, in_full(warp - 2), once);
-          load_2d_once(mine + kBufBytes, &maps.pre[1], n_tile + 32 * c, m_warp, in_full(warp - 2), once);
+      // Short sums: g and u come into L2 under the tile's MMAs (679 terms: 141 -> 112 us at 2603 x 8966; sums of 4096
+      // terms hide the loads anyway, and took 536 instead of 511 us at 8192 x 12288).
+      if (MODE == EPI_GATED_BWD && p.kb_total <= 32) {
+        const long long at = static_cast<long long>(min(m, p.M - 1)) * e.ldp + n_tile;
+        for (int c = c0; c < c_end; ++c) {
+          prefetch_l2(e.pre + at + 32 * c);
+          prefetch_l2(e.pre2 + at + 32 * c);
         }
-      };
-      if (MODE == EPI_GATED_BWD && c0 < c_end) fetch(c0);
+      }
       uint32_t res[16];
       const T* res_row = static_cast<const T*>(e.residual) + static_cast<long long>(m) * e.ldr + n_tile;
       auto fetch_residual = [&](int c) {
@@ -566,8 +539,6 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
       if (MODE == EPI_LINEAR && e.residual) fetch_residual(c0);
       if (!warp_wait(p.err, acc_full(buf), (tile_it >> 1) & 1, &abort_flag, 8u, false, 128,
                       kWaitNs + 1000ull * p.kb_total)) {  // a stage takes below a microsecond
-        if (MODE == EPI_GATED_BWD && c0 < c_end)  // the copies under way land before the block ends
-          warp_wait(p.err, in_full(warp - 2), fetched & 1, &abort_flag, 16u, true);
         break;
       }
       __syncwarp();
@@ -580,13 +551,8 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
           float v[32];
           tmem_ld32(acc + 32 * c, v);
           tmem_arrived(v);
-          const uint32_t b = acquire(true);
-          stage32(b, v);
-          publish();
-          if (lane == 0) {
-            store_2d(&maps.part, b, 32 * c, row);
-            bulk_commit();
-          }
+          store_row32<4>(reinterpret_cast<uint8_t*>(p.part + static_cast<long long>(row + lane) * nt + 32 * c),
+                         reinterpret_cast<const uint32_t(&)[32]>(v), 32, 32);
         }
       }
 #pragma unroll 1
@@ -601,45 +567,35 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
           tmem_arrived(v);
           tmem_arrived(g);
           if (e.pre) {
-            put32(v, &maps.pre[0], e.pre, e.ldp, n, m_warp);
-            put32(g, &maps.pre[1], e.pre2, e.ldp, n, m_warp);
+            put32(v, e.pre, n, left, m_warp);
+            put32(g, e.pre2, n, left, m_warp);
           }
           dense_activate<true, 32>(v, e.act, e.alpha, e.beta);
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] = pack_pair<T>(v[2 * i] * g[2 * i], v[2 * i + 1] * g[2 * i + 1]);
-          put16(w, &maps.y[0], static_cast<T*>(e.y), n, m_warp);
+          put16(w, static_cast<T*>(e.y), n, left, m_warp);
         } else if constexpr (MODE == EPI_GATED_BWD) {
-          float g[32], slope[32];
-          if (!warp_wait(p.err, in_full(warp - 2), fetched & 1, &abort_flag, 16u, true)) break;
-          ++fetched;
-          __syncwarp();
+          // the library's own rows: a multiple of 16 long, so 8 values that begin below N exist
+          float g[32], u[32], slope[32];
+          const long long at = static_cast<long long>(min(m, p.M - 1)) * e.ldp + n;
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 f = *reinterpret_cast<const float4*>(__cvta_shared_to_generic(mine + lane * 128 + ((q ^ (lane & 7)) << 4)));
-            g[4 * q] = f.x; g[4 * q + 1] = f.y; g[4 * q + 2] = f.z; g[4 * q + 3] = f.w;
-          }
+          for (int j = 0; j < 4; ++j)
+            if (8 * j < left) {
+              load_32b(e.pre + at + 8 * j, reinterpret_cast<uint32_t*>(g) + 8 * j);
+              load_32b(e.pre2 + at + 8 * j, reinterpret_cast<uint32_t*>(u) + 8 * j);
+            } else {
+#pragma unroll
+              for (int i = 0; i < 8; ++i) g[8 * j + i] = u[8 * j + i] = 0.0f;
+            }
           dense_activate_grad<true, 32>(g, slope, e.act, e.alpha, e.beta);
           tmem_arrived(v);
-          uint32_t w2[16];
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float4 f = *reinterpret_cast<const float4*>(
-                __cvta_shared_to_generic(mine + kBufBytes + lane * 128 + ((q ^ (lane & 7)) << 4)));
-            w[2 * q] = pack_pair<T>(v[4 * q] * f.x * slope[4 * q], v[4 * q + 1] * f.y * slope[4 * q + 1]);
-            w[2 * q + 1] = pack_pair<T>(v[4 * q + 2] * f.z * slope[4 * q + 2], v[4 * q + 3] * f.w * slope[4 * q + 3]);
-            w2[2 * q] = pack_pair<T>(v[4 * q] * g[4 * q], v[4 * q + 1] * g[4 * q + 1]);
-            w2[2 * q + 1] = pack_pair<T>(v[4 * q + 2] * g[4 * q + 2], v[4 * q + 3] * g[4 * q + 3]);
-          }
-          __syncwarp();  // g and u have been read: the outputs take g's place, then the next piece's come
-          stage16(mine, w);
-          stage16(mine + kBufBytes / 2, w2);
-          publish();
-          if (lane == 0) {
-            store_2d_once(&maps.y[0], mine, n, m_warp, once);
-            store_2d_once(&maps.y[1], mine + kBufBytes / 2, n, m_warp, once);
-            bulk_commit();
-          }
-          if (c + 1 < c_end) fetch(c + 1);
+          for (int i = 0; i < 16; ++i)
+            w[i] = pack_pair<T>(v[2 * i] * u[2 * i] * slope[2 * i], v[2 * i + 1] * u[2 * i + 1] * slope[2 * i + 1]);
+          put16(w, static_cast<T*>(e.y), n, left, m_warp);
+#pragma unroll
+          for (int i = 0; i < 16; ++i) w[i] = pack_pair<T>(v[2 * i] * g[2 * i], v[2 * i + 1] * g[2 * i + 1]);
+          put16(w, static_cast<T*>(e.y2), n, left, m_warp);
         } else {
           uint32_t bias[16];
           if (e.bias) load_row32(static_cast<const T*>(e.bias) + n, vec_b, left, bias);
@@ -649,7 +605,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
             add_row32<T>(v, res);
             fetch_residual(c + 1);
           }
-          if (e.pre) put32(v, &maps.pre[0], e.pre, e.ldp, n, m_warp);
+          if (e.pre) put32(v, e.pre, n, left, m_warp);
           dense_activate<true, 32>(v, e.act, e.alpha, e.beta);
           if (e.residual && e.residual_last) {
             add_row32<T>(v, res);
@@ -657,7 +613,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
           }
 #pragma unroll
           for (int i = 0; i < 16; ++i) w[i] = pack_pair<T>(v[2 * i], v[2 * i + 1]);
-          put16(w, &maps.y[t.batch], static_cast<T*>(t.batch ? e.y2 : e.y), n, m_warp);
+          put16(w, static_cast<T*>(t.batch ? e.y2 : e.y), n, left, m_warp);
         }
       }
       // the accumulator has been read: the next but one tile may have it
@@ -668,8 +624,6 @@ __global__ void __launch_bounds__(Cfg<CG, NT, MODE>::kThreads, 1)
         else mbar_arrive(acc_empty(buf));
       }
     }
-    if (lane == 0) bulk_wait_all();
-    __syncwarp();
   }
 
   __syncwarp();

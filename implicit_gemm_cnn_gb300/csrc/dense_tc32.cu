@@ -31,7 +31,8 @@ constexpr int kThreads32 = 64 + 32 * kEpiWarps;
 constexpr int kPlaneBytes = 128 * 128;          // one plane of a 128-row operand tile, 64 terms
 constexpr int kStage32 = 6 * kPlaneBytes;
 constexpr int kStages32 = 2;
-constexpr int kStaging32 = kEpiWarps * 2 * kBufBytes;
+constexpr int kBuf32 = 4096;                    // a staging tile of 32 rows of 32 float32
+constexpr int kStaging32 = kEpiWarps * 2 * kBuf32;
 constexpr int kSmem32 = kStages32 * kStage32 + kStaging32 + 2032;
 
 template <int MODE, bool A_MN, bool B_MN>
@@ -166,7 +167,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
     }
   } else {
     const int quarter = warp & 3;
-    const uint32_t mine = staging + (warp - 2) * 2 * kBufBytes;
+    const uint32_t mine = staging + (warp - 2) * 2 * kBuf32;
     const DenseEpi& e = p.epi;
     int turn = 0, it = 0;
     // 32 float32 columns of this lane's row
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
       if (tma) {
         if (lane == 0) bulk_wait_read<1>();
         __syncwarp();
-        const uint32_t b = mine + (turn & 1) * kBufBytes;
+        const uint32_t b = mine + (turn & 1) * kBuf32;
         ++turn;
 #pragma unroll
         for (int q = 0; q < 8; ++q)
@@ -277,13 +278,13 @@ __global__ void __launch_bounds__(kThreads32, 1)
 #pragma unroll
           for (int i = 0; i < 32; ++i) up[i] = nt == 64 ? acc[1][i] : acc[2][i];
           if (e.pre) {
-            put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp);
-            put(up, &maps.pre[1], e.pre2, e.ldp, p.tma_pre, n, m_warp);
+            put(acc[0], &maps.pre[0], e.pre, e.ldp, p.align_pre != 0, n, m_warp);
+            put(up, &maps.pre[1], e.pre2, e.ldp, p.align_pre != 0, n, m_warp);
           }
           activate(acc[0]);
 #pragma unroll
           for (int i = 0; i < 32; ++i) up[i] *= acc[0][i];
-          put(up, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.tma_y, n, m_warp);
+          put(up, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.align_y != 0, n, m_warp);
         } else if constexpr (MODE == EPI_GATED_BWD) {
           float g[32], slope[32];
           const float* gp = e.pre + static_cast<long long>(m) * e.ldp + n;
@@ -296,17 +297,17 @@ __global__ void __launch_bounds__(kThreads32, 1)
             slope[i] *= acc[0][i] * (row_ok && i < left ? up[i] : 0.0f);
             g[i] *= acc[0][i];
           }
-          put(slope, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.tma_y, n, m_warp);
-          put(g, &maps.y[1], static_cast<float*>(e.y2), e.ldy, p.tma_y, n, m_warp);
+          put(slope, &maps.y[0], static_cast<float*>(e.y), e.ldy, p.align_y != 0, n, m_warp);
+          put(g, &maps.y[1], static_cast<float*>(e.y2), e.ldy, p.align_y != 0, n, m_warp);
         } else {
           const float* res = e.residual && row_ok ? static_cast<const float*>(e.residual) + static_cast<long long>(m) * e.ldr + n
                                                   : nullptr;
           if (e.bias) add_row(acc[0], static_cast<const float*>(e.bias) + n, left);
           if (res && !e.residual_last) add_row(acc[0], res, left);
-          if (e.pre) put(acc[0], &maps.pre[0], e.pre, e.ldp, p.tma_pre, n, m_warp);
+          if (e.pre) put(acc[0], &maps.pre[0], e.pre, e.ldp, p.align_pre != 0, n, m_warp);
           activate(acc[0]);
           if (res && e.residual_last) add_row(acc[0], res, left);
-          put(acc[0], &maps.y[t.batch], static_cast<float*>(t.batch ? e.y2 : e.y), e.ldy, p.tma_y, n, m_warp);
+          put(acc[0], &maps.y[t.batch], static_cast<float*>(t.batch ? e.y2 : e.y), e.ldy, p.align_y != 0, n, m_warp);
         }
       }
     }

@@ -9,7 +9,7 @@ namespace dtc {
 
 template <typename T, int CG, int NT, int MODE, bool A_MN, bool B_MN>
 cudaError_t go(const DenseTcArgs& args, const DenseTcMaps& maps, int blocks, cudaStream_t s) {
-  using C = Cfg<CG, NT, MODE>;
+  using C = Cfg<CG, NT>;
   auto kern = dense_tc<T, CG, NT, MODE, A_MN, B_MN>;
   cudaError_t err = opt_in_smem(reinterpret_cast<const void*>(kern), C::kSmem);
   if (err != cudaSuccess) return err;
