@@ -265,19 +265,40 @@ __global__ void __launch_bounds__(256) dense_copies(const __grid_constant__ Copy
         put_planes(v, dst + col, job.rows * job.ld);
       }
     } else {
-      const uint16_t* src = static_cast<const uint16_t*>(job.in) + r * job.ld_in;
-      uint16_t* dst = static_cast<uint16_t*>(job.out) + r * job.ld;
-      uint16_t v[8];
+      // A lane writes eight values (16 bytes): out of the two aligned 16-byte pieces that they lie in, where both are
+      // inside the matrix, shifted together; else one by one.
+      const char* first = static_cast<const char*>(job.in);
+      const char* end = first + ((job.rows - 1) * job.ld_in + job.cols) * 2;
+      const long long col = c0 + 8 * lane;
+      if (col >= job.cols) continue;
+      const char* src = first + (r * job.ld_in + col) * 2;
+      uint16_t* dst = static_cast<uint16_t*>(job.out) + r * job.ld + col;
+      const uint32_t off = reinterpret_cast<uintptr_t>(src) % 16;
+      const char* at = src - off;
+      uint32_t w[4];
+      if (at >= first && at + 32 <= end) {
+        const uint4 lo = __ldg(reinterpret_cast<const uint4*>(at)), hi = __ldg(reinterpret_cast<const uint4*>(at) + 1);
+        const uint32_t q[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+        const int word = off / 4;
+        const uint32_t bits = 8 * (off % 4);
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const long long col = c0 + k * 32 + lane;
-        v[k] = col < job.cols ? src[col] : 0;
-      }
+        for (int i = 0; i < 4; ++i) {
+          uint32_t a = 0, b = 0;
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const long long col = c0 + k * 32 + lane;
-        if (col < job.cols) dst[col] = v[k];
+          for (int k = 0; k < 4; ++k)
+            if (k == word) { a = q[i + k]; b = q[i + k + 1]; }
+          w[i] = __funnelshift_r(a, b, bits);
+        }
+      } else {
+        const uint16_t* h = reinterpret_cast<const uint16_t*>(src);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t a = col + 2 * i < job.cols ? h[2 * i] : 0, b = col + 2 * i + 1 < job.cols ? h[2 * i + 1] : 0;
+          w[i] = a | (b << 16);
+        }
       }
+      // (the copy's rows are a multiple of 8 long; what lies past the columns there is never read as a term)
+      *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
 }

@@ -52,7 +52,8 @@ namespace dtc {
 using namespace tcx;
 
 constexpr int kBK = 64;
-constexpr int kBufBytes = 2304;  // a warp's staging: 32 rows of 32 16-bit values, or 16 of 32 float32, a word apart
+constexpr int kBufBytes = 2304;   // a warp's staging: 32 rows of 32 16-bit values, or 16 of 32 float32, a word apart
+constexpr int kBiasBytes = 256;   // and the bias of its (up to 128) columns
 
 template <int CG, int NT>
 struct Cfg {
@@ -60,7 +61,7 @@ struct Cfg {
   static constexpr int kThreads = 64 + 32 * kEpiWarps;
   static constexpr int kABytes = 128 * 128;
   static constexpr int kStageBytes = kABytes + NT / CG * 128;
-  static constexpr int kStaging = kEpiWarps * kBufBytes;
+  static constexpr int kStaging = kEpiWarps * (kBufBytes + kBiasBytes);
   static constexpr int kFit = (232448 - 2048 - kStaging) / kStageBytes;
   static constexpr int kStages = kFit > 8 ? 8 : kFit;
   static constexpr int kSmem = kStages * kStageBytes + kStaging + 2032;  // 1024 to align, the rest for barriers
@@ -284,6 +285,9 @@ __device__ __forceinline__ void add_row32(float (&v)[32], const uint32_t (&w)[16
   }
 }
 
+__device__ __forceinline__ void lds_v4(uint32_t addr, uint32_t* r) {
+  asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];\n" : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
+}
 __device__ __forceinline__ void sts_u32(uint32_t addr, uint32_t v) {
   asm volatile("st.shared.u32 [%0], %1;\n" ::"r"(addr), "r"(v) : "memory");
 }
@@ -464,7 +468,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
   } else {
     const int quarter = warp & 3, half = (warp - 2) >> 2;
     constexpr int kParts = C::kEpiWarps / 4;       // warps that share a quarter's columns
-    const uint32_t mine = staging + (warp - 2) * kBufBytes;
+    const uint32_t mine = staging + (warp - 2) * (kBufBytes + kBiasBytes);
     const DenseEpi& e = p.epi;
     // A lane holds 32 columns of one row.  On 16-byte boundaries it writes them itself, in whole sectors: nothing to wait
     // for.  (Staged tiles that TMA stores took 400 to 1300 clocks each until their place was free again.)  Rows of other
@@ -510,7 +514,6 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
       }
     };
     const bool vec_r = e.ldr % 8 == 0 && reinterpret_cast<uintptr_t>(e.residual) % 16 == 0;
-    const bool vec_b = reinterpret_cast<uintptr_t>(e.bias) % 16 == 0;
     const int chunks = out_cols / 32, per_warp = (chunks + kParts - 1) / kParts;
     const int c0 = half * per_warp, c1 = min(c0 + per_warp, chunks);
     const int raw0 = half * (nt / 32 / kParts), raw1 = kParts == 1 || half ? nt / 32 : raw0 + nt / 32 / kParts;
@@ -530,6 +533,16 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
           prefetch_l2(e.pre + at + 32 * c);
           prefetch_l2(e.pre2 + at + 32 * c);
         }
+      }
+      if (MODE == EPI_LINEAR && e.bias) {  // 16-bit, four columns a lane
+        const uint16_t* h = static_cast<const uint16_t*>(e.bias);
+        const int at = n_tile + 32 * c0 + 4 * lane;
+        uint16_t b[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) b[i] = at + i < p.N ? h[at + i] : static_cast<uint16_t>(0);
+        sts_u32(mine + kBufBytes + 8 * lane, pack2(b[0], b[1]));
+        sts_u32(mine + kBufBytes + 8 * lane + 4, pack2(b[2], b[3]));
+        __syncwarp();
       }
       uint32_t res[16];
       const T* res_row = static_cast<const T*>(e.residual) + static_cast<long long>(m) * e.ldr + n_tile;
@@ -598,7 +611,10 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
           put16(w, static_cast<T*>(e.y2), n, left, m_warp);
         } else {
           uint32_t bias[16];
-          if (e.bias) load_row32(static_cast<const T*>(e.bias) + n, vec_b, left, bias);
+          if (e.bias) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) lds_v4(mine + kBufBytes + 64 * (c - c0) + 16 * i, bias + 4 * i);
+          }
           tmem_arrived(v);
           if (e.bias) add_row32<T>(v, bias);
           if (e.residual && !e.residual_last) {
