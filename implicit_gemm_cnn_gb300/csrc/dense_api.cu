@@ -36,10 +36,6 @@ bool elems_ok(long long rows, long long stride) {
   long long n;
   return !__builtin_mul_overflow(rows, stride, &n) && n <= kMaxElems;
 }
-size_t range_bytes(long long rows, long long width, long long stride, size_t es) {
-  return rows < 1 ? 0 : (static_cast<size_t>(rows - 1) * stride + width) * es;
-}
-
 struct LinearShape {
   long long ldx, ldw, ldr, ldy;
 };
@@ -266,16 +262,27 @@ LinearPlan plan_linear_backward(const conv_linear_problem* p, const LinearShape&
 
 // Outputs overlap neither inputs, nor scratch, nor one another.
 struct Ranges {
-  struct R { const void* p; size_t n; };
+  // rows of `width` bytes, `stride` bytes apart (one row: stride 0)
+  struct R { uintptr_t p; size_t width, stride, span; };
   R in[8], out[8];  // the most that a call has
   int ins = 0, outs = 0;
-  void add_in(const void* p, size_t n) { if (p && n) in[ins++] = {p, n}; }
-  void add_out(const void* p, size_t n) { if (p && n) out[outs++] = {p, n}; }
+  static R rows_of(const void* p, size_t rows, size_t width, size_t stride) {
+    return {reinterpret_cast<uintptr_t>(p), width, rows > 1 ? stride : 0, rows < 1 ? 0 : (rows - 1) * stride + width};
+  }
+  void add(R* list, int* n, const R& r) { if (r.p && r.span) list[(*n)++] = r; }
+  void add_in(const void* p, size_t n) { add(in, &ins, rows_of(p, n ? 1 : 0, n, n)); }
+  void add_out(const void* p, size_t n) { add(out, &outs, rows_of(p, n ? 1 : 0, n, n)); }
+  void add_in(const void* p, size_t rows, size_t width, size_t stride) { add(in, &ins, rows_of(p, rows, width, stride)); }
+  void add_out(const void* p, size_t rows, size_t width, size_t stride) { add(out, &outs, rows_of(p, rows, width, stride)); }
+  static bool hit(const R& a, const R& b) {
+    if (a.p >= b.p + b.span || b.p >= a.p + a.span) return false;
+    if (a.stride && a.stride == b.stride) {  // columns side by side in one wider matrix
+      const size_t d = (b.p >= a.p ? b.p - a.p : a.stride - (a.p - b.p) % a.stride) % a.stride;
+      if (d >= a.width && d + b.width <= a.stride) return false;
+    }
+    return true;
+  }
   bool clash() const {
-    auto hit = [](const R& a, const R& b) {
-      const uintptr_t x = reinterpret_cast<uintptr_t>(a.p), y = reinterpret_cast<uintptr_t>(b.p);
-      return x < y + b.n && y < x + a.n;
-    };
     for (int i = 0; i < outs; ++i) {
       for (int j = 0; j < ins; ++j) if (hit(out[i], in[j])) return true;
       for (int j = 0; j < i; ++j) if (hit(out[i], out[j])) return true;
@@ -495,11 +502,11 @@ conv_status conv_linear_forward(const conv_linear_problem* p, const void* x, con
   if (!x || !w || !y || (p->has_bias && !bias) || (p->has_residual && !residual)) return CONV_ERR_NULL;
   const size_t es = elem_size(p->dtype);
   Ranges ranges;
-  ranges.add_in(x, range_bytes(p->rows, p->c_in, sh.ldx, es));
-  ranges.add_in(w, range_bytes(p->c_out, p->c_in, sh.ldw, es));
+  ranges.add_in(x, p->rows, p->c_in * es, sh.ldx * es);
+  ranges.add_in(w, p->c_out, p->c_in * es, sh.ldw * es);
   if (p->has_bias) ranges.add_in(bias, p->c_out * es);
-  if (p->has_residual) ranges.add_in(residual, range_bytes(p->rows, p->c_out, sh.ldr, es));
-  ranges.add_out(y, range_bytes(p->rows, p->c_out, sh.ldy, es));
+  if (p->has_residual) ranges.add_in(residual, p->rows, p->c_out * es, sh.ldr * es);
+  ranges.add_out(y, p->rows, p->c_out * es, sh.ldy * es);
   ranges.add_out(pre, static_cast<size_t>(p->rows) * p->c_out * 4);
   if (ranges.clash()) return CONV_ERR_ALIAS;
   int dev, sm;
@@ -537,10 +544,10 @@ conv_status conv_linear_backward(const conv_linear_problem* p, const void* x, co
   if (p->rows > 0 && (!dy || (dw && !x) || (dx && !w) || (act && !pre))) return CONV_ERR_NULL;
   Ranges ranges;
   if (p->rows > 0) {
-    if (dw) ranges.add_in(x, range_bytes(p->rows, p->c_in, sh.ldx, es));
-    if (dx) ranges.add_in(w, range_bytes(p->c_out, p->c_in, sh.ldw, es));
+    if (dw) ranges.add_in(x, p->rows, p->c_in * es, sh.ldx * es);
+    if (dx) ranges.add_in(w, p->c_out, p->c_in * es, sh.ldw * es);
     if (act) ranges.add_in(pre, static_cast<size_t>(p->rows) * p->c_out * 4);
-    ranges.add_in(dy, range_bytes(p->rows, p->c_out, sh.ldy, es));
+    ranges.add_in(dy, p->rows, p->c_out * es, sh.ldy * es);
   }
   ranges.add_out(dx, static_cast<size_t>(p->rows) * p->c_in * es);
   ranges.add_out(dw, static_cast<size_t>(p->c_out) * p->c_in * es);
@@ -641,12 +648,12 @@ conv_status conv_gated_forward(const conv_gated_problem* p, const void* x, const
   const size_t wbytes = static_cast<size_t>(p->hidden) * p->c_in * es;
   const GatedSaved keep = gated_saved(p, sh);
   Ranges ranges;
-  ranges.add_in(x, range_bytes(p->rows, p->c_in, sh.ldx, es));
+  ranges.add_in(x, p->rows, p->c_in * es, sh.ldx * es);
   ranges.add_in(w_gate, wbytes);
   ranges.add_in(w_up, wbytes);
   ranges.add_in(w_down, static_cast<size_t>(p->c_out) * p->hidden * es);
-  if (p->has_residual) ranges.add_in(residual, range_bytes(p->rows, p->c_out, sh.ldr, es));
-  ranges.add_out(y, range_bytes(p->rows, p->c_out, sh.ldy, es));
+  if (p->has_residual) ranges.add_in(residual, p->rows, p->c_out * es, sh.ldr * es);
+  ranges.add_out(y, p->rows, p->c_out * es, sh.ldy * es);
   ranges.add_out(saved, keep.total);
   if (ranges.clash()) return CONV_ERR_ALIAS;
   int dev, sm;
@@ -700,14 +707,14 @@ conv_status conv_gated_backward(const conv_gated_problem* p, const void* x, cons
   const GatedSaved keep = gated_saved(p, sh);
   Ranges ranges;
   if (p->rows > 0) {
-    if (dw_gate || dw_up) ranges.add_in(x, range_bytes(p->rows, p->c_in, sh.ldx, es));
+    if (dw_gate || dw_up) ranges.add_in(x, p->rows, p->c_in * es, sh.ldx * es);
     if (dx) {
       ranges.add_in(w_gate, wbytes);
       ranges.add_in(w_up, wbytes);
     }
     if (dgu) ranges.add_in(w_down, wdbytes);
     ranges.add_in(saved, keep.total);
-    ranges.add_in(dy, range_bytes(p->rows, p->c_out, sh.ldy, es));
+    ranges.add_in(dy, p->rows, p->c_out * es, sh.ldy * es);
   }
   ranges.add_out(dx, static_cast<size_t>(p->rows) * p->c_in * es);
   ranges.add_out(dw_gate, wbytes);

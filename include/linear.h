@@ -79,7 +79,8 @@ CONV_API conv_status conv_linear_describe_plan(const conv_linear_problem* p, int
  * would add a rounding error of the size of the result's own to every gradient.
  * Errors: those of conv_linear_scratch_bytes; CONV_ERR_NULL, CONV_ERR_SCRATCH
  * (too small, or not 256-byte aligned), CONV_ERR_ALIAS (y, pre or scratch
- * overlaps an operand), CONV_ERR_CUDA. */
+ * overlaps an operand; columns side by side in one wider matrix do not),
+ * CONV_ERR_CUDA. */
 CONV_API conv_status conv_linear_forward(const conv_linear_problem* p, const void* x, const void* w,
                                          const void* bias, const void* residual, void* y, float* pre,
                                          void* scratch, size_t scratch_bytes, void* stream);

@@ -86,6 +86,14 @@ def test_linear_pointer_refusals(lib):
     for bad in (x + 127, w, b + 4, r + 100):
         assert call(x, w, b, r, bad, None) == ALIAS
     assert call(x, w, b, r, y, y + 64) == ALIAS and call(x, w, b, r, y, x) == ALIAS
+    # columns side by side in one wider matrix do not overlap; shifted by a row they still do not, by a value they do
+    side = conv.make_linear_problem(4, 8, 8, x_stride=24, y_stride=24)
+    for at, want in ((x + 32, None), (x + 64, None), (x + 96 + 32, None), (x - 96 + 64, None), (x + 28, ALIAS),
+                     (x + 68, ALIAS), (x + 96 + 28, ALIAS)):
+        if torch.cuda.is_available() and want is None:
+            continue  # (with a device it would run)
+        got = f(ctypes.byref(side), x, w, None, None, at, None, None, 0, None)
+        assert (got == ALIAS) == (want == ALIAS), at - x
     p.rows = 0
     assert call(None, None, None, None, None, None) == OK  # nothing to do
     p.rows = 4
@@ -172,3 +180,26 @@ def test_python_argument_checks():
                 torch.zeros(3, 16)[:, ::2], torch.zeros(())):
         with pytest.raises(ValueError):
             dense._rows(bad, 8, "x")
+
+
+def test_plans(lib):
+    """Which kernel runs is a function of the shape and the SM count."""
+    def plan(rows, c_in, c_out, which=0, **kw):
+        return conv.conv_linear_describe_plan(conv.make_linear_problem(rows, c_in, c_out, **kw), which, 152)
+    assert plan(0, 8, 8) == "nothing launches=0"
+    for dtype in ("f32", "f16", "bf16"):
+        assert plan(1, 1024, 1024, dtype=dtype).startswith("few_rows")
+        assert plan(16, 1024, 1024, dtype=dtype).startswith("few_rows")
+        assert "launches=1" in plan(16, 1024, 1024, dtype=dtype)
+        for flags in (conv.FLAG_LINEAR_NO_FEW_ROWS, 0):
+            assert plan(17 if not flags else 1, 1024, 1024, dtype=dtype, flags=flags).startswith("tcgen05")
+        assert plan(500, 1024, 1024, dtype=dtype, flags=conv.FLAG_LINEAR_FORCE_FFMA).startswith("ffma")
+    assert plan(500, 1024, 1024, dtype="f32").startswith("tcgen05_bf16x3")
+    assert "tile=256x256 sms_per_tile=2" in plan(8192, 4096, 8192, dtype="bf16")
+    # 256 tiles on 76 pairs: three rounds whole, the last 28 tiles as two ranges each
+    d = plan(8192, 2048, 8192, 1, dtype="bf16")
+    assert "tiles=256 whole=228 split=2" in d and "launches=2" in d
+    # few tiles: all of them in ranges
+    assert "whole=0 split=" in plan(64, 8192, 256, dtype="bf16")
+    for a in ((3, 5, 7), (100, 1000, 3), (5000, 70, 900), (64, 30000, 64)):
+        assert plan(*a, dtype="f16") == plan(*a, dtype="f16")

@@ -365,3 +365,149 @@ def test_clip_the_norm_alone():
     assert torch.equal(t, before) and abs(norm.item() - want) <= 2.0 ** -19 * want
     conv.conv_clip_grads([], None, [], [], 1.0, 1e-6, norm, scratch, n)
     assert norm.item() == 0
+
+
+# ---- as programs use them ---------------------------------------------------
+def test_the_last_round_of_tiles_in_ranges():
+    """Plans whose last tiles are cut into k ranges, for each operand order and for the gated products."""
+    found = set()
+    for rows, c_in, c_out, dtype in ((40, 3000, 300, "bf16"), (3328, 2048, 1536, "bf16"), (60, 2000, 200, "f32"),
+                                     (1300, 1000, 1600, "f32"), (700, 2300, 2500, "f16")):
+        p = conv.make_linear_problem(rows, c_in, c_out, dtype=dtype)
+        for i in range(3):
+            d = conv.conv_linear_describe_plan(p, i, 152)
+            if "split=1 " not in d:
+                found.add((dtype == "f32", " whole=0 " in d))
+        linear_case(rows, c_in, c_out, dtype, act="silu", seed=rows)
+    assert found == {(False, False), (False, True), (True, False), (True, True)}
+    gated_case(90, 1500, 700, 300, "f16", seed=3)
+    gated_case(3328, 1024, 768, 64, "bf16", seed=4)
+
+
+def test_other_tile_widths():
+    for c_out in (70, 130, 200, 260, 330, 450):
+        linear_case(600, 192, c_out, "bf16", act="gelu", seed=c_out)
+
+
+def test_in_a_graph():
+    x, w, b = (t.cuda() for t in (rand(300, 200, dtype="bf16", seed=1), rand(250, 200, dtype="bf16", seed=2, scale=0.1),
+                                  rand(250, dtype="bf16", seed=3)))
+    wg, wu, wd = (t.cuda() for t in (rand(264, 200, dtype="bf16", seed=4, scale=0.1),
+                                     rand(264, 200, dtype="bf16", seed=5, scale=0.1),
+                                     rand(200, 264, dtype="bf16", seed=6, scale=0.1)))
+
+    def step():
+        y, pre = conv.linear(x, w, b, act="silu", save=True)
+        grads = conv.linear_backward(y, x, w, pre, act="silu", need_dbias=True)[:3]
+        z, saved = conv.gated_ffn(x, wg, wu, wd, x, save=True)
+        more = conv.gated_ffn_backward(z, x, wg, wu, wd, saved)
+        one = conv.gated_ffn(x[:1], wg, wu, wd, x[:1])
+        outs = [torch.empty_like(t) for t in grads + more]
+        norm = conv.clip_grad_norm(grads + more, 1.0, out=outs)
+        return [y, z, one, norm, *outs]
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = step()
+    for seed in (7, 8):
+        x.copy_(rand(300, 200, dtype="bf16", seed=seed))
+        graph.replay()
+        torch.cuda.synchronize()
+        for a, c in zip(step(), captured):
+            assert torch.equal(a, c)
+
+
+def test_two_streams_at_once():
+    """Calls on two streams, each with its own scratch, overlap and give what they give alone."""
+    cases = []
+    for i in range(2):
+        x, w = rand(50, 6000, dtype="bf16", seed=i).cuda(), rand(64, 6000, dtype="bf16", seed=9 + i, scale=0.02).cuda()
+        cases.append((x, w, conv.linear(x, w)))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    outs = [[] for _ in cases]
+    for _ in range(20):
+        for (x, w, _), s, o in zip(cases, streams, outs):
+            o.append(conv.linear(x, w, stream=s))
+    torch.cuda.synchronize()
+    for (_, _, want), o in zip(cases, outs):
+        assert all(torch.equal(want, y) for y in o)
+
+
+def test_offsets_past_32_bits():
+    big = torch.empty(600 << 22, dtype=torch.bfloat16, device="cuda")  # 2.5e9 elements
+    x = big.view(600, 1 << 22)[:, 5000:5080]
+    x.copy_(rand(600, 80, dtype="bf16", seed=1))
+    w = rand(40, 80, dtype="bf16", seed=2, scale=0.1).cuda()
+    y = conv.linear(x, w, out=big.view(600, 1 << 22)[:, 9000:9040])
+    dx, dw, _, _ = conv.linear_backward(y, x, w)
+    few = conv.linear(x[592:], w)
+    want = ref.linear64(*wide(x.cpu(), w.cpu(), None, None), "identity", 0, 0, False, "bf16")
+    ref.check(y, want["y"])
+    ref.check(few, tuple(t[592:] for t in want["y"]))
+    back = ref.linear_backward64(*wide(y.cpu(), x.cpu(), w.cpu()), *want["z"], "identity", 0, 0, False, "bf16")
+    ref.check(dx, back["dx"])
+    ref.check(dw, back["dw"])
+    flat = big[:(1 << 31) + 77]
+    flat.zero_()
+    flat[[3, 1 << 30, (1 << 31) - 1, 1 << 31, (1 << 31) + 76]] = 2.0
+    norm = conv.clip_grad_norm([flat], 1.0, eps=0.0)
+    assert abs(norm.item() - 20 ** 0.5) < 1e-5
+    assert (flat[[3, 1 << 30, (1 << 31) - 1, 1 << 31, (1 << 31) + 76]].float() - 2 / 20 ** 0.5).abs().max() < 2e-3
+    del big, x, flat
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_the_example(dtype):
+    import importlib.util
+    import os
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "examples", "train_block.py")
+    spec = importlib.util.spec_from_file_location("train_block", path)
+    example = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(example)
+    losses, norms, apart = example.train(12, dtype)
+    assert all(b < a for a, b in zip(losses, losses[1:])), losses  # a plain gradient step of a clipped size
+    assert norms[0] > 0.5 and all(n == n for n in norms)
+    # two float32 sums of 320 terms of h (their absolute values sum to below 64 here), and one rounding each
+    assert apart <= 2 * 320 * 2.0 ** -23 * 64 + 2 * ref.HALF_UNIT[dtype] * 16
+
+
+def test_refusals_of_tensors():
+    x, w = torch.zeros(4, 8, device="cuda"), torch.zeros(6, 8, device="cuda")
+    for bad in (dict(bias=torch.zeros(5, device="cuda")), dict(residual=torch.zeros(4, 5, device="cuda")),
+                dict(out=torch.zeros(5, 6, device="cuda")), dict(bias=torch.zeros(6, device="cuda").half()),
+                dict(residual=torch.zeros(4, 6))):
+        with pytest.raises(ValueError):
+            conv.linear(x, w, **bad)
+    with pytest.raises(ValueError):
+        conv.linear(x, torch.zeros(6, 9, device="cuda"))
+    with pytest.raises(ValueError):
+        conv.linear_backward(torch.zeros(4, 6, device="cuda"), x, w, act="silu")      # no pre
+    with pytest.raises(KeyError):
+        conv.linear(x, w, act="softmax")
+    with pytest.raises(conv.ConvError, match="ALIAS"):
+        conv.linear(x, w, out=torch.as_strided(w, (4, 6), (8, 1)))
+    with pytest.raises(conv.ConvError, match="SCRATCH"):
+        conv.linear(torch.zeros(64, 4096, device="cuda"), torch.zeros(64, 4096, device="cuda"),
+                    scratch=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    g = torch.zeros(12, 8, device="cuda")
+    with pytest.raises(ValueError):
+        conv.gated_ffn(x, g, torch.zeros(11, 8, device="cuda"), torch.zeros(8, 12, device="cuda"))
+    with pytest.raises(ValueError):
+        conv.gated_ffn(x, g, g.clone(), torch.zeros(12, 8, device="cuda").t())
+    y, saved = conv.gated_ffn(x, g, g.clone(), torch.zeros(8, 12, device="cuda"), save=True)
+    with pytest.raises(ValueError):
+        conv.gated_ffn_backward(y, x, g, g.clone(), torch.zeros(8, 12, device="cuda"), saved[:-256])
+    with pytest.raises(ValueError):
+        conv.clip_grad_norm([], 1.0)
+    with pytest.raises(ValueError):
+        conv.clip_grad_norm([x, w.t()], 1.0)
+    with pytest.raises(TypeError):
+        conv.clip_grad_norm([x.double()], 1.0)
+    with pytest.raises(ValueError):
+        conv.clip_grad_norm([x], 1.0, out=[w])
+    with pytest.raises(conv.ConvError, match="ALIAS"):
+        conv.clip_grad_norm([x, x], 1.0)
+    with pytest.raises(conv.ConvError, match="ARG"):
+        conv.clip_grad_norm([x], -1.0)
