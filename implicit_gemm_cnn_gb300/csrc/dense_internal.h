@@ -80,7 +80,7 @@ cudaError_t launch_dense_copies(const CopyJob* jobs, int count, bool planes, cud
 // dz = dy * act'(pre) in the element type (`dz`, may be nullptr: not wanted;
 // planes: as the three planes of CopyJob) and float32 column sums of the unrounded dz over row blocks
 // (part [blocks][cols]), summed in order into dbias by the second kernel.
-constexpr int kColRowsMin = 64;
+constexpr int kColRowsMin = 32;
 int dense_col_blocks(long long rows, long long cols, int sm);
 cudaError_t launch_dense_dz(const void* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz, bool planes, void* dbias,
                             float* part, int blocks, long long rows, long long cols, int act, float alpha, float beta,
