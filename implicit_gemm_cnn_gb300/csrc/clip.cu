@@ -7,6 +7,10 @@
 // between calls); work is cut into chunks of kChunk elements of one tensor, so
 // that short and long tensors fill the same grid.
 //
+// Measured, 300 tensors, 800 million bfloat16: the norm 253 us (6.3 TB/s, 93% of
+// measured), the scaling 495 us (6.5 TB/s).  40 tensors of 150 thousand float32
+// in all: 6 and 8 us, less than the call's host side (some 1.2 us a tensor).
+//
 // The sum: a thread squares and adds kVecs 16-byte vectors in float32 and adds
 // that to a float64; no conversion per element (the FP64 units do two
 // operations a clock per SM).  With float32's range the squares could overflow

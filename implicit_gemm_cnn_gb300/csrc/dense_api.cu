@@ -45,7 +45,7 @@ conv_status validate(const conv_linear_problem* p, LinearShape* s) {
   if (p->act < CONV_ACT_IDENTITY || p->act > CONV_ACT_GELU_TANH) return CONV_ERR_ACT;
   if (p->flags & ~kFlags) return CONV_ERR_ARG;
   if (p->rows < 0 || p->c_in < 1 || p->c_out < 1) return CONV_ERR_SHAPE;
-  if (p->rows > kI32 - 1024 || p->c_in > kI32 - 1024 || p->c_out > kI32 - 1024) return CONV_ERR_SHAPE;
+  if (p->rows > kI32 - 65536 || p->c_in > kI32 - 65536 || p->c_out > kI32 - 65536) return CONV_ERR_SHAPE;
   if (!stride_of(p->x_stride, p->c_in, &s->ldx) || !stride_of(p->w_stride, p->c_in, &s->ldw) ||
       !stride_of(p->residual_stride, p->c_out, &s->ldr) || !stride_of(p->y_stride, p->c_out, &s->ldy))
     return CONV_ERR_SHAPE;
@@ -64,7 +64,7 @@ conv_status validate(const conv_gated_problem* p, GatedShape* s) {
   if (p->act < CONV_ACT_IDENTITY || p->act > CONV_ACT_GELU_TANH) return CONV_ERR_ACT;
   if (p->flags & ~(kFlags & ~CONV_LINEAR_FLAG_RESIDUAL_LAST)) return CONV_ERR_ARG;
   if (p->rows < 0 || p->c_in < 1 || p->hidden < 1 || p->c_out < 1) return CONV_ERR_SHAPE;
-  if (p->rows > kI32 - 1024 || p->c_in > kI32 - 1024 || p->hidden > kI32 - 1024 || p->c_out > kI32 - 1024)
+  if (p->rows > kI32 - 65536 || p->c_in > kI32 - 65536 || p->hidden > kI32 - 65536 || p->c_out > kI32 - 65536)
     return CONV_ERR_SHAPE;
   if (!stride_of(p->x_stride, p->c_in, &s->ldx) || !stride_of(p->residual_stride, p->c_out, &s->ldr) ||
       !stride_of(p->y_stride, p->c_out, &s->ldy))
@@ -86,12 +86,13 @@ struct Product {
   DenseTcPlan tc;
   int split;
   size_t part_bytes;   // planes of the k ranges
-  int launches;
+  int launches, sm;
 };
 
 // `g` without addresses.  `tc`: 16-bit operands with rows a tensor-core copy can take.
 Product plan_product(const DenseGemm& g, int dtype, bool tc, bool few, int sm) {
   Product r = {};
+  r.sm = sm;
   if (few) {
     r.variant = V_FEW;
     r.split = 1;
@@ -113,7 +114,7 @@ Product plan_product(const DenseGemm& g, int dtype, bool tc, bool few, int sm) {
 
 // `follows`: the kernel before in the stream is this call's own.
 cudaError_t launch_product(const Product& r, DenseGemm g, int dtype, void* part, bool follows, cudaStream_t s) {
-  if (r.variant == V_FEW) return launch_dense_few(g, dtype, follows, s);
+  if (r.variant == V_FEW) return launch_dense_few(g, dtype, follows, r.sm, s);
   if (r.variant == V_TC) return launch_dense_tc(r.tc, g, dtype, part, s);
   g.split = r.split;
   g.part = static_cast<float*>(part);

@@ -8,11 +8,17 @@
 // operand and the rows of x as the 8 columns; a lane loads 16 consecutive bytes
 // of a weight row and of an x row, and the eight values become the k's of two
 // MMAs (both operands in the same order, so which k is which does not matter).
-// The tensor cores' rate is beside the point (one MMA per kilobyte); the
-// tcgen05 kernel's 128-row tiles, with their barriers and k ranges through
-// memory, took 11 us where this one takes 4 (1 x 1024 x 1024).  float32
+// The tensor cores' rate is beside the point: one MMA per kilobyte.  float32
 // multiplies on the CUDA cores.  The warps' sums meet in shared memory and are
 // added in order.
+//
+// Measured, back to back in a graph (the tcgen05 kernel, whose 128-row tiles
+// need barriers and k ranges through memory, in brackets): one row of 2048 ->
+// 8192 8.2 us (18), 16 rows 10.7 (17.3); one row of 1000 -> 512 1.9 (5.3).
+// From 17 rows on x, which every block reads whole, costs as much as the
+// weights, and the other kernel is as fast (32 rows of 4096 -> 4096: 14.6 us
+// against 12.3).  One row of a 4096 x 12288 gated block, two launches, the
+// second's first loads under the first's end: 51 us, 5.9 TB/s.
 #include <algorithm>
 
 #include "dense_internal.h"
@@ -66,7 +72,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
 // (output, row).
 template <typename T, int ROWS, bool DUAL>
 __device__ __forceinline__ void finish(const DenseGemm& g, const float* red, int n0) {
-  __syncthreads();
   for (int i = threadIdx.x; i < kOuts * ROWS; i += kThreads) {
     const int o = i % kOuts, r = i / kOuts;
     if (r >= g.M || n0 + o >= g.N) continue;
@@ -82,22 +87,24 @@ __device__ __forceinline__ void finish(const DenseGemm& g, const float* red, int
   }
 }
 
-// NB: 8-row groups of x (1 or 2).  A piece is 32 * CH terms.
+// NB: 8-row groups of x (1 or 2).  A piece is 32 * CH terms.  Blocks walk over the groups of outputs, the next group's
+// first weights on their way while one group's sums are joined.
 template <typename T, int NB, bool DUAL, bool VEC>
 __global__ void __launch_bounds__(kThreads, 2) few_mma(const DenseGemm g, const int early) {
   constexpr int P = DUAL ? 2 : 1;
   constexpr int CH = DUAL ? 2 : 4;
-  __shared__ float red[P * kWarps * kOuts * NB * 8];
+  __shared__ float red[2][P * kWarps * kOuts * NB * 8];
   const int warp = threadIdx.x / 32, lane = threadIdx.x % 32, gq = lane / 4, t = lane % 4;
-  const int n0 = blockIdx.x * kOuts;
   const long long K = g.K;
   // this lane's two weight rows (of each product) and its x rows; rows past the end read the last one and are not stored
   const uint16_t* w[P][2];
+  auto rows_of = [&](int n0) {
 #pragma unroll
-  for (int p = 0; p < P; ++p)
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
-      w[p][h] = static_cast<const uint16_t*>(g.b[p]) + static_cast<long long>(min(n0 + gq + 8 * h, g.N - 1)) * g.ldb + t * 8;
+      for (int h = 0; h < 2; ++h)
+        w[p][h] = static_cast<const uint16_t*>(g.b[p]) + static_cast<long long>(min(n0 + gq + 8 * h, g.N - 1)) * g.ldb + t * 8;
+  };
   const uint16_t* x[NB];
   bool has[NB];
 #pragma unroll
@@ -105,14 +112,6 @@ __global__ void __launch_bounds__(kThreads, 2) few_mma(const DenseGemm g, const 
     has[b] = gq + 8 * b < g.M;
     x[b] = static_cast<const uint16_t*>(g.a[0]) + static_cast<long long>(has[b] ? gq + 8 * b : 0) * g.lda + t * 8;
   }
-  float acc[P][NB][4];
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) acc[p][b][i] = 0.0f;
-
   uint4 cur[P][2][CH], next[P][2][CH];
   auto load_w = [&](uint4 (&q)[P][2][CH], long long k) {
 #pragma unroll
@@ -122,43 +121,61 @@ __global__ void __launch_bounds__(kThreads, 2) few_mma(const DenseGemm g, const 
 #pragma unroll
         for (int h = 0; h < 2; ++h) q[p][h][c] = load8<VEC, true>(w[p][h] + k + 32 * c, K - (k + 32 * c + t * 8));
   };
-  const long long piece = 32 * CH, step = piece * kWarps;
-  long long k = warp * piece;
+  const long long piece = 32 * CH, step = piece * kWarps, k0 = warp * piece;
+  int n0 = blockIdx.x * kOuts, turn = 0;
+  rows_of(n0);
   // `early`: the kernel before is the same call's, whose output x is and the weights are not
   if (!early) griddep_wait();
-  if (k < K) load_w(cur, k);
+  if (k0 < K) load_w(cur, k0);
   griddep_wait();
   griddep_launch();
-  for (; k < K; k += step) {
-    if (k + step < K) load_w(next, k + step);
+  while (n0 < g.N) {
+    float acc[P][NB][4];
 #pragma unroll
-    for (int c = 0; c < CH; ++c) {
-      const long long left = K - (k + 32 * c + t * 8);
+    for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        const uint4 xv = load8<VEC, false>(x[b] + k + 32 * c, has[b] ? left : 0);
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int p = 0; p < P; ++p) {
-          mma16816<T>(acc[p][b], cur[p][0][c].x, cur[p][1][c].x, cur[p][0][c].y, cur[p][1][c].y, xv.x, xv.y);
-          mma16816<T>(acc[p][b], cur[p][0][c].z, cur[p][1][c].z, cur[p][0][c].w, cur[p][1][c].w, xv.z, xv.w);
+        for (int i = 0; i < 4; ++i) acc[p][b][i] = 0.0f;
+    const int n1 = n0 + static_cast<int>(gridDim.x) * kOuts;
+    for (long long k = k0; k < K; k += step) {
+      if (k + step < K) load_w(next, k + step);
+      else if (n1 < g.N) {
+        rows_of(n1);
+        load_w(next, k0);
+      }
+#pragma unroll
+      for (int c = 0; c < CH; ++c) {
+        const long long left = K - (k + 32 * c + t * 8);
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          const uint4 xv = load8<VEC, false>(x[b] + k + 32 * c, has[b] ? left : 0);
+#pragma unroll
+          for (int p = 0; p < P; ++p) {
+            mma16816<T>(acc[p][b], cur[p][0][c].x, cur[p][1][c].x, cur[p][0][c].y, cur[p][1][c].y, xv.x, xv.y);
+            mma16816<T>(acc[p][b], cur[p][0][c].z, cur[p][1][c].z, cur[p][0][c].w, cur[p][1][c].w, xv.z, xv.w);
+          }
         }
       }
+#pragma unroll
+      for (int p = 0; p < P; ++p)
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+          for (int c = 0; c < CH; ++c) cur[p][h][c] = next[p][h][c];
     }
 #pragma unroll
     for (int p = 0; p < P; ++p)
 #pragma unroll
-      for (int h = 0; h < 2; ++h)
+      for (int b = 0; b < NB; ++b)
 #pragma unroll
-        for (int c = 0; c < CH; ++c) cur[p][h][c] = next[p][h][c];
+        for (int i = 0; i < 4; ++i)
+          red[turn][((p * kWarps + warp) * kOuts + gq + 8 * (i / 2)) * (NB * 8) + b * 8 + 2 * t + i % 2] = acc[p][b][i];
+    __syncthreads();  // (the other buffer's sums were read before this)
+    finish<T, NB * 8, DUAL>(g, red[turn], n0);
+    turn ^= 1;
+    n0 = n1;
   }
-#pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int b = 0; b < NB; ++b)
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        red[((p * kWarps + warp) * kOuts + gq + 8 * (i / 2)) * (NB * 8) + b * 8 + 2 * t + i % 2] = acc[p][b][i];
-  finish<T, NB * 8, DUAL>(g, red, n0);
 }
 
 // float32: a warp multiplies pieces of 128 terms (four per lane) of the block's outputs with every row.  ROWS: rows
@@ -221,35 +238,39 @@ __global__ void __launch_bounds__(kThreads) few_f32(const DenseGemm g, const int
           if (lane == 0) red[((p * kWarps + warp) * kOuts + o0 + o) * ROWS + r] = v;
         }
   }
+  __syncthreads();
   finish<float, ROWS, DUAL>(g, red, n0);
 }
 
 template <typename K>
-cudaError_t start(K kern, const DenseGemm& g, bool follows, cudaStream_t s) {
-  return launch_overlapped(kern, dim3(static_cast<unsigned>((g.N + kOuts - 1) / kOuts)), kThreads, 0, 1, s, g,
-                           follows ? 1 : 0);
+cudaError_t start(K kern, const DenseGemm& g, bool follows, int blocks, cudaStream_t s) {
+  return launch_overlapped(kern, dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, s, g, follows ? 1 : 0);
 }
+int groups_of(const DenseGemm& g) { return static_cast<int>((static_cast<long long>(g.N) + kOuts - 1) / kOuts); }
 template <typename T, bool DUAL>
-cudaError_t go16(const DenseGemm& g, bool vec, bool follows, cudaStream_t s) {
-  if (g.M <= 8) return vec ? start(few_mma<T, 1, DUAL, true>, g, follows, s) : start(few_mma<T, 1, DUAL, false>, g, follows, s);
-  return vec ? start(few_mma<T, 2, DUAL, true>, g, follows, s) : start(few_mma<T, 2, DUAL, false>, g, follows, s);
+cudaError_t go16(const DenseGemm& g, bool vec, bool follows, int sm, cudaStream_t s) {
+  // two blocks per SM at most, each with as many groups of outputs as any other
+  const int groups = groups_of(g), rounds = (groups + 2 * sm - 1) / (2 * sm), blocks = (groups + rounds - 1) / rounds;
+  if (g.M <= 8) return vec ? start(few_mma<T, 1, DUAL, true>, g, follows, blocks, s) : start(few_mma<T, 1, DUAL, false>, g, follows, blocks, s);
+  return vec ? start(few_mma<T, 2, DUAL, true>, g, follows, blocks, s) : start(few_mma<T, 2, DUAL, false>, g, follows, blocks, s);
 }
 template <int ROWS, bool DUAL>
 cudaError_t go32(const DenseGemm& g, bool vec, bool follows, cudaStream_t s) {
-  return vec ? start(few_f32<ROWS, DUAL, true>, g, follows, s) : start(few_f32<ROWS, DUAL, false>, g, follows, s);
+  return vec ? start(few_f32<ROWS, DUAL, true>, g, follows, groups_of(g), s)
+             : start(few_f32<ROWS, DUAL, false>, g, follows, groups_of(g), s);
 }
 
 }  // namespace
 
-cudaError_t launch_dense_few(const DenseGemm& g, int dtype, bool follows, cudaStream_t s) {
+cudaError_t launch_dense_few(const DenseGemm& g, int dtype, bool follows, int sm, cudaStream_t s) {
   const int es = dtype == CONV_F32 ? 4 : 2, per = 16 / es;
   auto on16 = [&](const void* p, long long ld) { return reinterpret_cast<uintptr_t>(p) % 16 == 0 && ld % per == 0; };
   // whole 16-byte pieces: rows on 16-byte boundaries, k a multiple of a piece
   const bool vec = g.K % per == 0 && on16(g.a[0], g.M > 1 ? g.lda : 0) && on16(g.b[0], g.ldb) &&
                    (!g.dual || on16(g.b[1], g.ldb));
-  if (dtype == CONV_F16) return g.dual ? go16<__half, true>(g, vec, follows, s) : go16<__half, false>(g, vec, follows, s);
+  if (dtype == CONV_F16) return g.dual ? go16<__half, true>(g, vec, follows, sm, s) : go16<__half, false>(g, vec, follows, sm, s);
   if (dtype == CONV_BF16)
-    return g.dual ? go16<__nv_bfloat16, true>(g, vec, follows, s) : go16<__nv_bfloat16, false>(g, vec, follows, s);
+    return g.dual ? go16<__nv_bfloat16, true>(g, vec, follows, sm, s) : go16<__nv_bfloat16, false>(g, vec, follows, sm, s);
   if (g.M <= 1) return g.dual ? go32<1, true>(g, vec, follows, s) : go32<1, false>(g, vec, follows, s);
   if (g.M <= 4) return g.dual ? go32<4, true>(g, vec, follows, s) : go32<4, false>(g, vec, follows, s);
   if (g.M <= 8) return g.dual ? go32<8, true>(g, vec, follows, s) : go32<8, false>(g, vec, follows, s);

@@ -61,7 +61,7 @@ cudaError_t dense_error_word(uint32_t* word, int reset);
 // the kernel before in the stream is this call's own, and writes no weights: the
 // launch overlaps its end, the first weights' loads included.
 constexpr int kFewRows = 16;
-cudaError_t launch_dense_few(const DenseGemm& g, int dtype, bool follows, cudaStream_t s);
+cudaError_t launch_dense_few(const DenseGemm& g, int dtype, bool follows, int sm, cudaStream_t s);
 
 // Adds the k ranges' planes in order and applies the epilogue.
 cudaError_t launch_dense_reduce(const DenseGemm& g, int dtype, cudaStream_t s);

@@ -141,7 +141,8 @@ DenseTcPlan search(const DenseGemm& g, int f32, int sm) {
   return best;
 }
 
-// Adds the k ranges' sums of the tiles that were cut, in order, and runs their epilogue: four columns per thread.
+// Adds the k ranges' sums of the tiles that were cut, in order, and runs their epilogue: four columns per thread (28 tiles
+// of 256 x 256 in two ranges: 10 us, where a fourth round of whole tiles would be 20).
 template <typename T>
 __global__ void __launch_bounds__(256) dense_join(const __grid_constant__ DenseTcArgs p, const float* part, int tile_rows,
                                                   int dual) {

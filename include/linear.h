@@ -13,6 +13,11 @@
  * 16-bit results are rounded once, to nearest even.  No kernel uses atomics:
  * results are bit-identical from run to run on one device.
  *
+ * float32 operands (of more than 16 rows) are multiplied as three bfloat16
+ * parts each (all 24 bits of their significands), with sums at least as exact as
+ * float32 ones; an infinite operand may then give NaN where a plain product
+ * gives an infinity.
+ *
  * Matrices are row-major.  A row stride counts elements from one row to the
  * next; 0 stands for dense rows (stride = width).  Pointers and strides of any
  * alignment are legal.  16-bit operands whose address or row stride in bytes is
