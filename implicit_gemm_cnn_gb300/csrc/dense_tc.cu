@@ -238,6 +238,7 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype,
   const CUtensorMapDataType type = dtype == CONV_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16;
   const int b_rows = g.dual && t.cg == 1 ? t.nt / 2 : t.nt / t.cg;
   const int as = std::max(g.segs, g.batch), bs = g.segs > 1 || g.batch > 1 || g.dual ? 2 : 1;
+  p.a_rows = f32 ? 128 : std::min(128, (g.M + 7) / 8 * 8);
   // one copy per operand and stage where the blocks of 64 divide the matrix and the block's share of the tile
   p.a_3d = g.a_mn && g.M % 64 == 0 && !f32;
   p.b_3d = g.b_mn && g.N % 64 == 0 && b_rows % 64 == 0 && !f32;
@@ -249,7 +250,7 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype,
     if (blocks) return encode_blocks(map, type, base, rows, g.K, ld, box_blocks);
     return mn ? encode(map, type, base, rows, g.K, ld, 0, 64) : encode(map, type, base, g.K, rows, ld, 0, box_rows);
   };
-  for (int i = 0; i < as; ++i) ok = ok && operand(&maps.a[i], g.a[i], g.a_mn, p.a_3d, g.M, g.lda, 128, 2);
+  for (int i = 0; i < as; ++i) ok = ok && operand(&maps.a[i], g.a[i], g.a_mn, p.a_3d, g.M, g.lda, p.a_rows, 2);
   for (int i = 0; i < bs; ++i) ok = ok && operand(&maps.b[i], g.b[i], g.b_mn, p.b_3d, g.N, g.ldb, b_rows, b_rows / 64);
   const int mode = g.epi.mode;
   const int tile_rows = 128 * t.cg, cut = t.tiles - t.whole;

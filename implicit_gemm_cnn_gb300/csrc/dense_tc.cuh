@@ -47,6 +47,7 @@ struct DenseTcArgs {
   int M, N;
   int nt;                   // MMA columns of a tile: a multiple of 32 (64 gated), at most the kernel's NT
   int segs, batch;
+  int a_rows;               // k-major A: rows of a copy (128; fewer where M has no more: the rest of the tile is not stored)
   int a_3d, b_3d;           // mn-major: all of a stage's 64-wide boxes in one copy
   int kb_seg;               // 64-term blocks of a segment
   int kb_total, kb_range;   // of the sum; of a k range
@@ -383,7 +384,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
     if (elect_one()) {
       // bytes of a stage, both blocks' together: whole boxes, past the matrices' ends too
       const int b_boxes = (b_rows + 63) / 64;
-      const uint32_t stage_bytes = CG * (C::kABytes + (B_MN ? b_boxes * 8192 : b_rows * 128));
+      const uint32_t stage_bytes = CG * ((A_MN ? C::kABytes : p.a_rows * 128) + (B_MN ? b_boxes * 8192 : b_rows * 128));
       const uint32_t bar0 = CG == 2 ? map_rank(full(0), 0) : full(0);  // the first block's
       const bool a_3d = A_MN && p.a_3d, b_3d = B_MN && p.b_3d;
       int s = 0, left = 0;
