@@ -44,6 +44,16 @@ class GatedProblem(ctypes.Structure):
         ("dtype", ctypes.c_int32), ("has_residual", ctypes.c_int32), ("flags", ctypes.c_uint32)]
 
 
+torch = None  # imported by the first call that takes tensors
+
+
+def _torch():
+    global torch
+    import torch as module
+    torch = module
+    return module
+
+
 _lib = None
 
 
@@ -214,6 +224,13 @@ def _rows(t, width, what):
     return rows, stride if rows > 1 else 0
 
 
+def _rows_dense(t, width, what):
+    """_rows, quicker for the dense tensors that most calls have."""
+    if t.is_contiguous() and t.dim() and t.shape[-1] == width:
+        return t.numel() // width, 0
+    return _rows(t, width, what)
+
+
 def _same(x, others):
     """The operands' device number; ValueError unless they share x's type and device."""
     dtype, index = x.dtype, x.get_device()
@@ -233,7 +250,6 @@ class _On:
     __slots__ = ("handle", "ctx")
 
     def __init__(self, index, stream):
-        import torch
         if stream is None:
             self.ctx = torch.cuda.device(index)
             self.handle = torch.cuda.current_stream(index).cuda_stream
@@ -250,32 +266,21 @@ class _On:
         self.ctx.__exit__(*exc)
 
 
-class _Here:
-    """A call on the current stream of the current device."""
-
-    __slots__ = ("handle",)
-
-    def __enter__(self):
-        return self.handle
-
-    def __exit__(self, *exc):
-        pass
+_raw_stream = _device = None
 
 
-_raw_stream = None
-
-
-def _on(index, stream):
-    global _raw_stream
-    import torch
-    if stream is not None or index != torch.cuda.current_device():
-        return _On(index, stream)
+def _run(call, index, stream, *args):
+    """call(handle, *args) on the call's stream, with that stream and the operands' device current."""
+    global _raw_stream, _device
     if _raw_stream is None:
+        _torch()
+        _device = torch.cuda.current_device
         _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
             lambda i: torch.cuda.current_stream(i).cuda_stream)
-    here = _Here()
-    here.handle = _raw_stream(index)
-    return here
+    if stream is None and index == _device():
+        return call(_raw_stream(index), *args)
+    with _On(index, stream) as handle:
+        return call(handle, *args)
 
 
 # Problems and their scratch sizes by shape, so that a call of a shape seen before marshals nothing anew.
@@ -318,7 +323,6 @@ def _scratch(need, given, index, handle):
         return given, given.data_ptr(), given.numel() * given.element_size()
     if need == 0:
         return None, None, 0
-    import torch
     if need > _KEPT or torch.cuda.is_current_stream_capturing():
         t = torch.empty(need, dtype=torch.uint8, device=index)
         return t, t.data_ptr(), need
@@ -334,7 +338,6 @@ def _scratch(need, given, index, handle):
 
 
 def _dense_out(out, shape, like, what):
-    import torch
     if out is None:
         return torch.empty(shape, dtype=like.dtype, device=like.device)
     if tuple(out.shape) != tuple(shape) or out.dtype != like.dtype or out.device != like.device or \
@@ -355,8 +358,8 @@ def linear(x, w, bias=None, residual=None, *, act="identity", alpha=0.0, beta=0.
         raise ValueError("w must be [c_out, c_in]")
     c_out, c_in = w.shape
     index = _same(x, (w, bias, residual, out))
-    rows, ldx = _rows(x, c_in, "x")
-    ldw = _rows(w, c_in, "w")[1]
+    rows, ldx = _rows_dense(x, c_in, "x")
+    ldw = _rows_dense(w, c_in, "w")[1]
     xs = x.shape
     y_shape = (xs[0], c_out) if len(xs) == 2 else (*xs[:-1], c_out)
     ldr = ldy = 0
@@ -368,33 +371,32 @@ def linear(x, w, bias=None, residual=None, *, act="identity", alpha=0.0, beta=0.
     if residual is not None:
         if residual.shape != y_shape:
             raise ValueError("residual must have y's shape")
-        ldr = _rows(residual, c_out, "residual")[1]
+        ldr = _rows_dense(residual, c_out, "residual")[1]
         rp = residual.data_ptr()
     if out is not None:
         if out.shape != y_shape:
             raise ValueError("out must have y's shape")
-        ldy = _rows(out, c_out, "out")[1]
+        ldy = _rows_dense(out, c_out, "out")[1]
     if residual_last:
         flags |= FLAG_LINEAR_RESIDUAL_LAST
     if (xp | wp) & 15 and dt:
         flags |= FLAG_LINEAR_UNALIGNED
-    with _on(index, stream) as handle:
-        import torch
+
+    def call(handle, out):
         if out is None:
             # (empty_like is the quicker of the two)
-            out = torch.empty_like(residual) if rp is not None and ldr in (0, c_out) and residual.is_contiguous() else \
+            out = torch.empty_like(residual) if rp is not None and ldr == 0 and residual.is_contiguous() else \
                 torch.empty(y_shape, dtype=x.dtype, device=x.device)
-        pre = None
-        if save and act != "identity":
-            pre = torch.empty(y_shape, dtype=torch.float32, device=x.device)
+        pre = torch.empty(y_shape, dtype=torch.float32, device=x.device) if save and act != "identity" else None
         _, ref, need = _linear_problem(False, rows, c_in, c_out, ldx, ldw, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, dt,
                                        0 if bp is None else 1, 0 if rp is None else 1, flags)
-        buf, at, n = _scratch(need, scratch, index, handle)
+        _, at, n = _scratch(need, scratch, index, handle) if need else (None, None, 0)
         status = _load().conv_linear_forward(ref, xp, wp, bp, rp, out.data_ptr(), None if pre is None else pre.data_ptr(),
                                              at, n, handle or None)
         if status:
             _check(status, "conv_linear_forward")
-    return (out, pre) if save else out
+        return (out, pre) if save else out
+    return _run(call, index, stream, out)
 
 
 def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, residual_last=False, need_dx=True,
@@ -403,7 +405,7 @@ def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, 
     """The gradients of ``linear`` for dy [..., c_out]: (dx, dw, dbias,
     dresidual), None where not wanted.  ``pre`` is what linear(..., save=True)
     returned; act, alpha, beta and residual_last are that call's."""
-    import torch
+    torch = _torch()
     dt = DTYPES[_dtype_name(x)]
     if w.dim() != 2:
         raise ValueError("w must be [c_out, c_in]")
@@ -426,7 +428,8 @@ def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, 
     xp, wp, dyp = x.data_ptr(), w.data_ptr(), dy.data_ptr()
     if dt and ((xp if need_dw else 0) | (wp if need_dx else 0) | (dyp if pre is None else 0)) & 15:
         flags |= FLAG_LINEAR_UNALIGNED
-    with _on(index, stream) as handle:
+
+    def call(handle, dx, dw):
         dx = _dense_out(dx, x.shape, x, "dx") if need_dx else None
         dw = _dense_out(dw, w.shape, x, "dw") if need_dw else None
         dbias = torch.empty(c_out, dtype=x.dtype, device=x.device) if need_dbias else None
@@ -436,7 +439,8 @@ def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, 
         buf, at, n = _scratch(need, scratch, index, handle)
         _check(_load().conv_linear_backward(ref, xp, wp, _ptr(pre), dyp, _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dres), at, n,
                                             handle or None), "conv_linear_backward")
-    return dx, dw, dbias, dres
+        return dx, dw, dbias, dres
+    return _run(call, index, stream, dx, dw)
 
 
 def _gated(x, w_gate, w_up, w_down):
@@ -455,25 +459,25 @@ def gated_ffn(x, w_gate, w_up, w_down, residual=None, *, act="silu", alpha=0.0, 
     [..., c_in], w_gate and w_up [hidden, c_in], w_down [c_out, hidden],
     residual and y [..., c_out].  With ``save``, returns (y, saved) for
     ``gated_ffn_backward``."""
-    import torch
     dt = DTYPES[_dtype_name(x)]
     index = _same(x, (w_gate, w_up, w_down, residual, out))
     c_in, hidden, c_out = _gated(x, w_gate, w_up, w_down)
-    rows, ldx = _rows(x, c_in, "x")
-    y_shape = x.shape[:-1] + (c_out,)
+    rows, ldx = _rows_dense(x, c_in, "x")
+    y_shape = (*x.shape[:-1], c_out)
     ldr = ldy = 0
     if residual is not None:
         if residual.shape != y_shape:
             raise ValueError("residual must have y's shape")
-        ldr = _rows(residual, c_out, "residual")[1]
+        ldr = _rows_dense(residual, c_out, "residual")[1]
     if out is not None:
         if out.shape != y_shape:
             raise ValueError("out must have y's shape")
-        ldy = _rows(out, c_out, "out")[1]
+        ldy = _rows_dense(out, c_out, "out")[1]
     ptrs = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr()
     if dt and (ptrs[0] | ptrs[1] | ptrs[2] | ptrs[3]) & 15:
         flags |= FLAG_LINEAR_UNALIGNED
-    with _on(index, stream) as handle:
+
+    def call(handle, out):
         if out is None:
             out = torch.empty_like(residual) if residual is not None and residual.is_contiguous() else \
                 torch.empty(y_shape, dtype=x.dtype, device=x.device)
@@ -484,7 +488,8 @@ def gated_ffn(x, w_gate, w_up, w_down, residual=None, *, act="silu", alpha=0.0, 
         status = _load().conv_gated_forward(ref, *ptrs, _ptr(residual), out.data_ptr(), _ptr(saved), at, n, handle or None)
         if status:
             _check(status, "conv_gated_forward")
-    return (out, saved) if save else out
+        return (out, saved) if save else out
+    return _run(call, index, stream, out)
 
 
 def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=0.0, beta=0.0, need_dx=True,
@@ -493,7 +498,7 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=
     dw_down), None where not wanted.  ``saved`` is what gated_ffn(...,
     save=True) returned; act, alpha and beta are that call's.  The residual's
     gradient is dy."""
-    import torch
+    torch = _torch()
     dt = DTYPES[_dtype_name(x)]
     index = _same(x, (w_gate, w_up, w_down, dy))
     c_in, hidden, c_out = _gated(x, w_gate, w_up, w_down)
@@ -504,7 +509,8 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=
     ptrs = x.data_ptr(), w_gate.data_ptr(), w_up.data_ptr(), w_down.data_ptr()
     if dt and (ptrs[0] | ptrs[1] | ptrs[2] | ptrs[3] | dy.data_ptr()) & 15:
         flags |= FLAG_LINEAR_UNALIGNED
-    with _on(index, stream) as handle:
+
+    def call(handle):
         _, ref, need, kept = _gated_problem(True, rows, c_in, hidden, c_out, ldx, 0, ldy, LINEAR_ACTIVATIONS[act], alpha,
                                             beta, dt, 0, flags)
         if saved.dtype != torch.uint8 or saved.get_device() != index or saved.numel() != kept:
@@ -515,7 +521,8 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=
         buf, at, n = _scratch(need, scratch, index, handle)
         _check(_load().conv_gated_backward(ref, *ptrs, saved.data_ptr(), dy.data_ptr(), _ptr(dx), *[_ptr(t) for t in dws],
                                            at, n, handle or None), "conv_gated_backward")
-    return (dx, *dws)
+        return (dx, *dws)
+    return _run(call, index, stream)
 
 
 def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, scratch=None, stream=None):
@@ -523,7 +530,7 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, scratch=None, stream=
     device), and the tensors scaled by min(1, max_norm / (norm + eps)): in
     place, or into the tensors of ``out``.  Tensors are contiguous, of any mix
     of the element types."""
-    import torch
+    torch = _torch()
     grads = list(grads)
     n = len(grads)
     if n == 0:
@@ -552,7 +559,8 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, scratch=None, stream=
     ins = array("Q", map(tensor.data_ptr, grads))
     to = ins if out is None else array("Q", map(tensor.data_ptr, outs))
     lib = _load()
-    with _on(index, stream) as handle:
+
+    def call(handle):
         norm = torch.empty((), dtype=torch.float32, device=index)
         at_sizes = sizes.buffer_info()[0]
         need = ctypes.c_size_t()
@@ -560,4 +568,5 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, scratch=None, stream=
         buf, at, size = _scratch(need.value, scratch, index, handle)
         _check(lib.conv_clip_grads(n, ins.buffer_info()[0], to.buffer_info()[0], at_sizes, types.buffer_info()[0],
                                    max_norm, eps, norm.data_ptr(), at, size, handle or None), "conv_clip_grads")
-    return norm
+        return norm
+    return _run(call, index, stream)
