@@ -113,6 +113,7 @@ DenseTcPlan search(const DenseGemm& g, int f32, int sm) {
     const long long slots = sm / cg;
     for (int nt = cg == 2 ? 256 : 128; nt >= 64; nt -= 32) {
       if ((g.dual || f32) && nt % 64) continue;
+      if (g.b_mn && nt / cg % 64) continue;  // copied in blocks of 64 columns: other widths would load more than they use
       const int cols = g.dual ? nt / 2 : nt;
       const long long tiles = ((g.M + 128LL * cg - 1) / (128 * cg)) * ((static_cast<long long>(g.N) + cols - 1) / cols) * g.batch;
       const double per = f32 ? std::max(13.0 * nt, 1000.0) : cg == 2 ? 165.0 + 1.73 * nt : 190.0 + 1.76 * nt;
@@ -181,10 +182,10 @@ __global__ void __launch_bounds__(256) dense_join(const __grid_constant__ DenseT
 
 // The plans of the shapes used last (a search takes microseconds, a small product too).
 struct PlanKey {
-  int M, N, K, segs, batch, dual, f32, sm;
+  int M, N, K, segs, batch, dual, b_mn, f32, sm;
   bool operator==(const PlanKey& o) const {
-    return M == o.M && N == o.N && K == o.K && segs == o.segs && batch == o.batch && dual == o.dual && f32 == o.f32 &&
-           sm == o.sm;
+    return M == o.M && N == o.N && K == o.K && segs == o.segs && batch == o.batch && dual == o.dual &&
+           b_mn == o.b_mn && f32 == o.f32 && sm == o.sm;
   }
 };
 std::mutex g_plan_mu;
@@ -197,9 +198,9 @@ struct {
 
 DenseTcPlan dense_tc_plan(const DenseGemm& g, int dtype, int sm) {
   const int f32 = dtype == CONV_F32;
-  const PlanKey key{g.M, g.N, g.K, g.segs, g.batch, g.dual, f32, sm};
+  const PlanKey key{g.M, g.N, g.K, g.segs, g.batch, g.dual, g.b_mn, f32, sm};
   uint32_t h = 2166136261u;
-  for (int v : {key.M, key.N, key.K, key.segs, key.batch, key.dual, key.f32}) h = (h ^ static_cast<uint32_t>(v)) * 16777619u;
+  for (int v : {key.M, key.N, key.K, key.segs, key.batch, key.dual, key.b_mn, key.f32}) h = (h ^ static_cast<uint32_t>(v)) * 16777619u;
   auto& slot = g_plans[(h ^ (h >> 15)) % 256];
   {
     std::lock_guard<std::mutex> lock(g_plan_mu);
