@@ -23,7 +23,9 @@ constexpr uint32_t kFlags = CONV_LINEAR_FLAG_RESIDUAL_LAST | CONV_LINEAR_FLAG_UN
                             CONV_LINEAR_FLAG_NO_FEW_ROWS;
 
 size_t align256(size_t v) { return (v + 255) / 256 * 256; }
-long long round8(long long v) { return (v + 7) / 8 * 8; }
+// Row length of the library's own matrices: whole cache lines of 16-bit values, so that a copy of 64 values is one line,
+// and blocks of 64 columns exist.
+long long round64(long long v) { return (v + 63) / 64 * 64; }
 size_t elem_size(int dtype) { return dtype == CONV_F32 ? 4 : 2; }
 
 // Row stride as given (0: dense); false if it is below the width or too large.
@@ -50,7 +52,7 @@ conv_status validate(const conv_linear_problem* p, LinearShape* s) {
       !stride_of(p->residual_stride, p->c_out, &s->ldr) || !stride_of(p->y_stride, p->c_out, &s->ldy))
     return CONV_ERR_SHAPE;
   if (!elems_ok(p->rows, s->ldx) || !elems_ok(p->c_out, s->ldw) || !elems_ok(p->rows, s->ldy) ||
-      (p->has_residual && !elems_ok(p->rows, s->ldr)) || !elems_ok(p->rows, round8(p->c_out)))
+      (p->has_residual && !elems_ok(p->rows, s->ldr)) || !elems_ok(p->rows, round64(p->c_out)))
     return CONV_ERR_OVERFLOW;
   return CONV_OK;
 }
@@ -69,9 +71,9 @@ conv_status validate(const conv_gated_problem* p, GatedShape* s) {
   if (!stride_of(p->x_stride, p->c_in, &s->ldx) || !stride_of(p->residual_stride, p->c_out, &s->ldr) ||
       !stride_of(p->y_stride, p->c_out, &s->ldy))
     return CONV_ERR_SHAPE;
-  s->ldh = (p->hidden + 15) / 16 * 16;  // 32-byte rows
+  s->ldh = round64(p->hidden);
   if (!elems_ok(p->rows, s->ldx) || !elems_ok(p->rows, s->ldy) || (p->has_residual && !elems_ok(p->rows, s->ldr)) ||
-      !elems_ok(p->rows, s->ldh) || !elems_ok(round8(p->c_in), s->ldh) || !elems_ok(round8(p->c_out), s->ldh))
+      !elems_ok(p->rows, s->ldh) || !elems_ok(round64(p->c_in), s->ldh) || !elems_ok(round64(p->c_out), s->ldh))
     return CONV_ERR_OVERFLOW;
   return CONV_OK;
 }
@@ -154,7 +156,7 @@ struct Layout {
     c.planes = dtype == CONV_F32;
     c.on = tc && (c.planes || unaligned || ld % 8 != 0) && rows > 0;
     c.rows = rows; c.cols = cols; c.ld_in = ld;
-    c.ld = c.on ? round8(cols) : ld;
+    c.ld = c.on ? round64(cols) : ld;
     if (c.on) {
       c.bytes = static_cast<size_t>(rows) * c.ld * (c.planes ? 6 : 2);
       c.off = take(c.bytes);
@@ -242,7 +244,7 @@ LinearPlan plan_linear_backward(const conv_linear_problem* p, const LinearShape&
   r.dz = p->act != CONV_ACT_IDENTITY;
   // dz as it is written (or dy, which stands for it), then as the products read it
   r.dz_planes = tc && p->dtype == CONV_F32;
-  r.ldz = r.dz ? round8(p->c_out) : sh.ldy;
+  r.ldz = r.dz ? round64(p->c_out) : sh.ldy;
   if (r.dz) r.dz_off = l.take(static_cast<size_t>(p->rows) * r.ldz * (r.dz_planes ? 6 : elem_size(p->dtype)));
   else r.z = l.copy(tc, p->dtype, mode.copies, p->rows, p->c_out, r.ldz);
   const long long ldz = r.dz ? r.ldz : r.z.ld;
@@ -250,9 +252,12 @@ LinearPlan plan_linear_backward(const conv_linear_problem* p, const LinearShape&
     r.col_blocks = dense_col_blocks(p->rows, p->c_out, sm);
     r.col_off = l.take(static_cast<size_t>(r.col_blocks) * p->c_out * sizeof(float));
     r.dx = make_gemm(p->rows, p->c_in, p->c_out, 0, 1, ldz, r.w.ld);
+    r.dx.b_pad = r.w.on;
     r.dx.epi.ldy = p->c_in;
     r.pdx = plan_product(r.dx, p->dtype, mode.tc, false, sm);
     r.dw = make_gemm(p->c_out, p->c_in, p->rows, 1, 1, ldz, r.x.ld);
+    r.dw.a_pad = r.dz || r.z.on;
+    r.dw.b_pad = r.x.on;
     r.dw.epi.ldy = p->c_in;
     r.pdw = plan_product(r.dw, p->dtype, mode.tc, false, sm);
   }
@@ -384,15 +389,19 @@ GatedPlan plan_gated_backward(const conv_gated_problem* p, const GatedShape& sh,
   r.h = l.copy(tc, p->dtype, false, p->rows, p->hidden, sh.ldh);
   if (p->rows > 0) {
     r.dh = make_gemm(p->rows, p->hidden, p->c_out, 0, 1, r.dy.ld, r.wd.ld);
+    r.dh.b_pad = r.wd.on;
     r.dh.epi.mode = EPI_GATED_BWD;
     r.dh.epi.act = p->act; r.dh.epi.alpha = p->act_alpha; r.dh.epi.beta = p->act_beta;
     r.dh.epi.ldy = sh.ldh; r.dh.epi.ldp = sh.ldh;
     r.pdh = plan_product(r.dh, p->dtype, mode.tc, false, sm);
     r.dx = make_gemm(p->rows, p->c_in, p->hidden, 0, 1, r.dg.ld, r.wg.ld);
+    r.dx.b_pad = r.wg.on;
     r.dx.segs = 2;
     r.dx.epi.ldy = p->c_in;
     r.pdx = plan_product(r.dx, p->dtype, mode.tc, false, sm);
     r.dwgu = make_gemm(p->hidden, p->c_in, p->rows, 1, 1, r.dg.ld, r.x.ld);
+    r.dwgu.a_pad = 1;
+    r.dwgu.b_pad = r.x.on;
     r.dwgu.batch = 2;
     r.dwgu.epi.ldy = p->c_in;
     r.pdwgu = plan_product(r.dwgu, p->dtype, mode.tc, false, sm);
@@ -400,6 +409,8 @@ GatedPlan plan_gated_backward(const conv_gated_problem* p, const GatedShape& sh,
     one.batch = 1;
     r.pdw1 = plan_product(one, p->dtype, mode.tc, false, sm);
     r.dwd = make_gemm(p->c_out, p->hidden, p->rows, 1, 1, r.dy.ld, r.h.ld);
+    r.dwd.a_pad = r.dy.on;
+    r.dwd.b_pad = 1;
     r.dwd.epi.ldy = p->hidden;
     r.pdwd = plan_product(r.dwd, p->dtype, mode.tc, false, sm);
   }

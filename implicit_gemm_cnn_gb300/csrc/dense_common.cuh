@@ -47,6 +47,7 @@ struct DenseGemm {
   const void* a[2];
   const void* b[2];
   long long lda, ldb;
+  int a_pad, b_pad;      // mn-major: the library's own rows, which go on to a multiple of 64 (what is there is no result)
   DenseEpi epi;
   // k ranges of the CUDA-core kernel: `split` of `k_per_split` terms of the whole sum (segs * K), each
   // into plane s of `part` (float32 [split][products][M][N]); 1: the whole sum

@@ -233,7 +233,7 @@ __device__ __forceinline__ void put_planes(const float (&v)[4], __nv_bfloat16* o
 }
 
 // Operands' copies, bound by their bytes (30 MB of weights with odd rows 13 us).  A warp takes 256 columns of a row at a time: 16-bit rows as they are, or float32 rows as three planes (rows of the
-// planes are a multiple of 8 long, so whole groups of four are written).  Blocks walk over the jobs' pieces together.
+// planes are a multiple of 64 long, so whole groups of four are written).  Blocks walk over the jobs' pieces together.
 struct CopyJobs {
   CopyJob job[kCopyJobs];
   long long first[kCopyJobs + 1];
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(256) dense_copies(const __grid_constant__ Copy
           w[i] = a | (b << 16);
         }
       }
-      // (the copy's rows are a multiple of 8 long; what lies past the columns there is never read as a term)
+      // (the copy's rows are a multiple of 64 long; what lies past the columns there is never read as a term)
       *reinterpret_cast<uint4*>(dst) = make_uint4(w[0], w[1], w[2], w[3]);
     }
   }
@@ -409,7 +409,8 @@ __global__ void __launch_bounds__(256) dense_colsum(const float* part, T* out, i
   const long long c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (c >= cols) return;
   float s = 0.0f;
-  for (int b = 0; b < blocks; ++b) s += part[b * cols + c];
+#pragma unroll 8
+  for (int b = 0; b < blocks; ++b) s += part[b * cols + c];  // (eight loads in flight, added in order)
   out[c] = from_f32<T>(s);
 }
 

@@ -75,11 +75,11 @@ bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, long l
                    CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
-// An mn-major operand's matrix (rows of `inner` values, inner a multiple of 64) as a map of 64-wide column blocks: one
-// copy brings `blocks` of them, one after another.
+// An mn-major operand's matrix (rows of `inner` values, existing to a multiple of 64) as a map of 64-wide column blocks:
+// one copy brings `blocks` of them, one after another.
 bool encode_blocks(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long inner, long long rows,
                    long long ld, int blocks) {
-  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>(inner / 64)};
+  const cuuint64_t dims[3] = {64, static_cast<cuuint64_t>(rows), static_cast<cuuint64_t>((inner + 63) / 64)};
   const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * 2, 128};
   const cuuint32_t box[3] = {64, 64, static_cast<cuuint32_t>(blocks)};
   const cuuint32_t step[3] = {1, 1, 1};
@@ -241,8 +241,8 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype,
   const int as = std::max(g.segs, g.batch), bs = g.segs > 1 || g.batch > 1 || g.dual ? 2 : 1;
   p.a_rows = f32 ? 128 : std::min(128, (g.M + 7) / 8 * 8);
   // one copy per operand and stage where the blocks of 64 divide the matrix and the block's share of the tile
-  p.a_3d = g.a_mn && g.M % 64 == 0 && !f32;
-  p.b_3d = g.b_mn && g.N % 64 == 0 && b_rows % 64 == 0 && !f32;
+  p.a_3d = g.a_mn && (g.M % 64 == 0 || g.a_pad) && !f32;
+  p.b_3d = g.b_mn && (g.N % 64 == 0 || g.b_pad) && b_rows % 64 == 0 && !f32;
   bool ok = true;
   auto operand = [&](CUtensorMap* map, const void* base, int mn, bool blocks, long long rows, long long ld, int box_rows,
                      int box_blocks) {

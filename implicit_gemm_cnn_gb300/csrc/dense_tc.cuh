@@ -601,7 +601,7 @@ __global__ void __launch_bounds__(Cfg<CG, NT>::kThreads, 1)
           for (int i = 0; i < 16; ++i) w[i] = pack_pair<T>(v[2 * i] * g[2 * i], v[2 * i + 1] * g[2 * i + 1]);
           put16(w, static_cast<T*>(e.y), n, left, m_warp);
         } else if constexpr (MODE == EPI_GATED_BWD) {
-          // the library's own rows: a multiple of 16 long, so 8 values that begin below N exist
+          // the library's own rows: a multiple of 64 long, so 8 values that begin below N exist
           float g[32], u[32], slope[32];
           const long long at = static_cast<long long>(min(m, p.M - 1)) * e.ldp + n;
 #pragma unroll

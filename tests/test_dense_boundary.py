@@ -137,9 +137,9 @@ def test_gated_refusals(lib):
     assert b(ctypes.byref(p), x, g, u, d, s, None, dx, dg, du, dd, None, 0, None) == NULL
     assert b(ctypes.byref(p), None, g, u, d, s, dy, None, dg, None, None, None, 0, None) == NULL
     assert b(ctypes.byref(p), x, g, u, d, s, dy, dx, dg, dg, dd, None, 0, None) == ALIAS
-    # the block's saved state: g and u in float32 and h, rows of a multiple of 8 elements
+    # the block's saved state: g and u in float32 and h, rows of a multiple of 64 elements
     p = conv.make_gated_problem(10, 8, 13, 8, dtype="f16")
-    assert conv.conv_gated_saved_bytes(p) == 768 + 768 + 512
+    assert conv.conv_gated_saved_bytes(p) == 2 * 10 * 64 * 4 + 10 * 64 * 2
 
 
 def test_clip_refusals(lib):
