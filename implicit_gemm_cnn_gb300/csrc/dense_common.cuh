@@ -89,7 +89,14 @@ __device__ __forceinline__ float dense_act_fn(float t, float alpha, float beta) 
     return t * dense_sigmoid<FAST>(v2);
   } else if constexpr (ACT == ACT_SILU) return t * dense_sigmoid<FAST>(t);
   else if constexpr (ACT == ACT_SIGMOID) return dense_sigmoid<FAST>(t);
-  else return act_fn<ACT>(t, alpha, beta);
+  // (written so that a NaN stays one: a training step has to show it)
+  else if constexpr (ACT == ACT_RELU) return t < 0.0f ? 0.0f : t;
+  else if constexpr (ACT == ACT_CLIP) return t < alpha ? alpha : (t > beta ? beta : t);
+  else if constexpr (ACT == ACT_HARD_SIGMOID || ACT == ACT_HARD_SWISH) {
+    const float s = ACT == ACT_HARD_SWISH ? fmaf(t, 1.0f / 6.0f, 0.5f) : fmaf(alpha, t, beta);
+    const float c = s < 0.0f ? 0.0f : (s > 1.0f ? 1.0f : s);
+    return ACT == ACT_HARD_SWISH ? t * c : c;
+  } else return act_fn<ACT>(t, alpha, beta);
 }
 template <int ACT, bool FAST>
 __device__ __forceinline__ float dense_act_grad(float t, float alpha, float beta) {

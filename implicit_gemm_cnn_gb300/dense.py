@@ -8,6 +8,7 @@ outputs and scratch with torch."""
 from __future__ import annotations
 
 import ctypes
+import threading
 from array import array
 
 from . import ACTIVATIONS, DTYPES, _check, _dtype_name, _ptr, load
@@ -310,11 +311,12 @@ def _gated_problem(back, *key):
     return found
 
 
-# Scratch of up to _KEPT bytes is kept per stream: the calls of a stream run one after another, and an allocation from
-# torch's pool takes longer than a small call's own work.  A larger one, and one under graph capture (whose memory belongs
-# to the graph), is the call's own.
+# Scratch of up to _KEPT bytes is kept per stream: the calls of a stream run one after another (host threads that share a
+# stream take turns at a call: _turn), and an allocation from torch's pool takes longer than a small call's own work.  A
+# larger one, and one under graph capture (whose memory belongs to the graph), is the call's own.
 _KEPT = 32 << 20
 _kept: dict = {}
+_turn = threading.RLock()
 
 
 def _scratch(need, given, index, handle):
@@ -390,9 +392,13 @@ def linear(x, w, bias=None, residual=None, *, act="identity", alpha=0.0, beta=0.
         pre = torch.empty(y_shape, dtype=torch.float32, device=x.device) if save and act != "identity" else None
         _, ref, need = _linear_problem(False, rows, c_in, c_out, ldx, ldw, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, dt,
                                        0 if bp is None else 1, 0 if rp is None else 1, flags)
-        _, at, n = _scratch(need, scratch, index, handle) if need else (None, None, 0)
-        status = _load().conv_linear_forward(ref, xp, wp, bp, rp, out.data_ptr(), None if pre is None else pre.data_ptr(),
-                                             at, n, handle or None)
+        args = ref, xp, wp, bp, rp, out.data_ptr(), None if pre is None else pre.data_ptr()
+        if need:
+            with _turn:
+                _, at, n = _scratch(need, scratch, index, handle)
+                status = _load().conv_linear_forward(*args, at, n, handle or None)
+        else:
+            status = _load().conv_linear_forward(*args, None, 0, handle or None)
         if status:
             _check(status, "conv_linear_forward")
         return (out, pre) if save else out
@@ -436,9 +442,11 @@ def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, 
         dres = torch.empty(dy.shape, dtype=x.dtype, device=x.device) if need_dresidual else None
         _, ref, need = _linear_problem(True, rows, c_in, c_out, ldx, ldw, 0, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, dt,
                                        0, 0, flags)
-        buf, at, n = _scratch(need, scratch, index, handle)
-        _check(_load().conv_linear_backward(ref, xp, wp, _ptr(pre), dyp, _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dres), at, n,
-                                            handle or None), "conv_linear_backward")
+        with _turn:
+            buf, at, n = _scratch(need, scratch, index, handle)
+            status = _load().conv_linear_backward(ref, xp, wp, _ptr(pre), dyp, _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dres), at,
+                                                  n, handle or None)
+        _check(status, "conv_linear_backward")
         return dx, dw, dbias, dres
     return _run(call, index, stream, dx, dw)
 
@@ -484,8 +492,10 @@ def gated_ffn(x, w_gate, w_up, w_down, residual=None, *, act="silu", alpha=0.0, 
         _, ref, need, kept = _gated_problem(False, rows, c_in, hidden, c_out, ldx, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha,
                                             beta, dt, 0 if residual is None else 1, flags)
         saved = torch.empty(kept, dtype=torch.uint8, device=x.device) if save else None
-        buf, at, n = _scratch(need, scratch, index, handle)
-        status = _load().conv_gated_forward(ref, *ptrs, _ptr(residual), out.data_ptr(), _ptr(saved), at, n, handle or None)
+        with _turn:
+            buf, at, n = _scratch(need, scratch, index, handle)
+            status = _load().conv_gated_forward(ref, *ptrs, _ptr(residual), out.data_ptr(), _ptr(saved), at, n,
+                                                handle or None)
         if status:
             _check(status, "conv_gated_forward")
         return (out, saved) if save else out
@@ -518,9 +528,11 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
         dws = [torch.empty(w.shape, dtype=x.dtype, device=x.device) if need_dw else None
                for w in (w_gate, w_up, w_down)]
-        buf, at, n = _scratch(need, scratch, index, handle)
-        _check(_load().conv_gated_backward(ref, *ptrs, saved.data_ptr(), dy.data_ptr(), _ptr(dx), *[_ptr(t) for t in dws],
-                                           at, n, handle or None), "conv_gated_backward")
+        with _turn:
+            buf, at, n = _scratch(need, scratch, index, handle)
+            status = _load().conv_gated_backward(ref, *ptrs, saved.data_ptr(), dy.data_ptr(), _ptr(dx),
+                                                 *[_ptr(t) for t in dws], at, n, handle or None)
+        _check(status, "conv_gated_backward")
         return (dx, *dws)
     return _run(call, index, stream)
 
@@ -565,8 +577,10 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, scratch=None, stream=
         at_sizes = sizes.buffer_info()[0]
         need = ctypes.c_size_t()
         _check(lib.conv_clip_scratch_bytes(n, at_sizes, ctypes.byref(need)), "conv_clip_scratch_bytes")
-        buf, at, size = _scratch(need.value, scratch, index, handle)
-        _check(lib.conv_clip_grads(n, ins.buffer_info()[0], to.buffer_info()[0], at_sizes, types.buffer_info()[0],
-                                   max_norm, eps, norm.data_ptr(), at, size, handle or None), "conv_clip_grads")
+        with _turn:
+            buf, at, size = _scratch(need.value, scratch, index, handle)
+            status = lib.conv_clip_grads(n, ins.buffer_info()[0], to.buffer_info()[0], at_sizes, types.buffer_info()[0],
+                                         max_norm, eps, norm.data_ptr(), at, size, handle or None)
+        _check(status, "conv_clip_grads")
         return norm
     return _run(call, index, stream)

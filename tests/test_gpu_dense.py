@@ -56,7 +56,7 @@ def linear_case(rows, c_in, c_out, dtype, act="identity", alpha=0.0, beta=0.0, b
 # rows, c_in, c_out: one of everything, odd ones, sizes around tiles and ranges
 SIZES = [(1, 1, 1), (1, 8, 8), (1, 64, 129), (2, 7, 5), (3, 65, 64), (5, 200, 33), (8, 1024, 24), (12, 250, 301),
          (16, 264, 256), (17, 512, 40), (33, 96, 1000), (64, 72, 200), (100, 136, 120), (127, 320, 257),
-         (129, 129, 127), (200, 1000, 72), (256, 64, 256), (300, 257, 515), (513, 40, 384), (640, 520, 264)]
+         (129, 129, 127), (200, 1000, 72), (256, 64, 256), (300, 257, 515), (513, 40, 384), (640, 520, 264), (50, 1, 3), (40, 3, 1), (1000, 2, 2)]
 
 
 @pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
@@ -147,6 +147,20 @@ def test_linear_infinities_and_nan_stay_in_their_rows(rows):
         y = conv.linear(x, w)
         assert y[1].isnan().all() and not y[2].isfinite().any()
         assert y[0].isfinite().all() and y[3:].isfinite().all()
+
+
+@pytest.mark.parametrize("act", ACTS, ids=lambda a: a[0])
+def test_a_nan_shows_in_values_and_gradients(act):
+    name, alpha, beta = act
+    for rows, dtype in ((4, "bf16"), (4, "f32"), (70, "f16"), (70, "f32")):
+        x, w = rand(rows, 32, dtype=dtype, seed=1).cuda(), rand(24, 32, dtype=dtype, seed=2).cuda()
+        x[2, 3] = float("nan")
+        y, pre = conv.linear(x, w, act=name, alpha=alpha, beta=beta, save=True)
+        dx = conv.linear_backward(torch.ones_like(y), x, w, pre, act=name, alpha=alpha, beta=beta, need_dw=False)[0]
+        g = conv.gated_ffn(x, w, w.clone(), w.t().contiguous(), act=name, alpha=alpha, beta=beta)
+        assert y[2].isnan().all() and g[2].isnan().all() and (name == "identity" or dx[2].isnan().all())
+        for t in (y, dx, g):
+            assert t[:2].isfinite().all() and t[3:].isfinite().all()
 
 
 def test_linear_is_the_same_every_time():
@@ -433,6 +447,27 @@ def test_two_streams_at_once():
     torch.cuda.synchronize()
     for (_, _, want), o in zip(cases, outs):
         assert all(torch.equal(want, y) for y in o)
+
+
+def test_two_host_threads_on_one_stream():
+    """Their calls share the stream's scratch; each call's launches stay together."""
+    import threading
+    cases = [(rand(50, 6000, dtype="bf16", seed=i).cuda(), rand(64, 6000, dtype="bf16", seed=9 + i, scale=0.02).cuda())
+             for i in range(2)]
+    want = [conv.linear(x, w) for x, w in cases]
+    outs = [[], []]
+
+    def work(i):
+        for _ in range(100):
+            outs[i].append(conv.linear(*cases[i]))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for w, o in zip(want, outs):
+        assert len(o) == 100 and all(torch.equal(w, y) for y in o)
 
 
 def test_offsets_past_32_bits():
