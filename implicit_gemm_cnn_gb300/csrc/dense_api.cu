@@ -205,7 +205,24 @@ Mode mode_of(uint32_t flags, int dtype) {
   return m;
 }
 
-bool few_rows(long long rows) { return rows >= 1 && rows <= kFewRows; }
+// Whether the kernel for few rows takes a product: up to 8 rows always, from 9 to 16 (two MMAs a weight piece; 16 sums
+// in float32) unless the tensor-core kernel, if it may run, is the quicker one.  Measured, that kernel in brackets:
+//   float32 rows that are no whole 16-byte pieces are loaded one by one: 9 rows of 2047 -> 2048 27.5 us (21.1), of
+//   4095 -> 12289 193 (159); whole ones 16 of 4096 -> 4096 35.6 (59.6);
+//   16-bit products of rows * outputs from 90,000 on: every block reads all of x, and the tensor-core kernel's tiles
+//   fill the SMs without k ranges.  16 rows of 4096 -> 12288 25.0 us (21.4), 9 of 4096 -> 16384 29.7 (25.6); below,
+//   16 rows of 4096 -> 4096 9.7 (12.3), 9 of 2048 -> 8192 9.7 (10.1).  Not where that kernel would copy the weights.
+// `outputs`: of all products over the same x.  `pieces`: every operand's rows are whole 16-byte pieces.
+bool few_rows(const Mode& m, long long rows, long long outputs, int dtype, bool pieces) {
+  if (!m.few || rows < 1 || rows > kFewRows) return false;
+  if (rows <= 8 || !m.tc) return true;
+  if (dtype == CONV_F32) return pieces;
+  return !pieces || m.copies || rows * outputs < 90000;
+}
+bool whole_pieces(int dtype, std::initializer_list<long long> sizes) {
+  const int per = 16 / static_cast<int>(elem_size(dtype));
+  return std::all_of(sizes.begin(), sizes.end(), [&](long long n) { return n % per == 0; });
+}
 
 struct LinearPlan {
   Copy x, w, z;
@@ -220,7 +237,7 @@ struct LinearPlan {
 LinearPlan plan_linear(const conv_linear_problem* p, const LinearShape& sh, const Mode& mode, int sm) {
   LinearPlan r = {};
   Layout l;
-  const bool few = mode.few && few_rows(p->rows);
+  const bool few = few_rows(mode, p->rows, p->c_out, p->dtype, whole_pieces(p->dtype, {p->c_in, sh.ldx, sh.ldw}));
   const bool tc = mode.tc && !few;
   r.x = l.copy(tc, p->dtype, mode.copies, p->rows, p->c_in, sh.ldx);
   r.w = l.copy(tc, p->dtype, mode.copies, p->c_out, p->c_in, sh.ldw);
@@ -348,7 +365,7 @@ GatedSaved gated_saved(const conv_gated_problem* p, const GatedShape& sh) {
 GatedPlan plan_gated(const conv_gated_problem* p, const GatedShape& sh, const Mode& mode, int sm, bool saved) {
   GatedPlan r = {};
   Layout l;
-  const bool few = mode.few && few_rows(p->rows);
+  const bool few = few_rows(mode, p->rows, 2 * p->hidden, p->dtype, whole_pieces(p->dtype, {p->c_in, p->hidden, sh.ldx}));
   const bool tc = mode.tc && !few;
   r.x = l.copy(tc, p->dtype, mode.copies, p->rows, p->c_in, sh.ldx);
   r.wg = l.copy(tc, p->dtype, mode.copies, p->hidden, p->c_in, p->c_in);

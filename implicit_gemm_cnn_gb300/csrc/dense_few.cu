@@ -14,11 +14,11 @@
 //
 // Measured, back to back in a graph (the tcgen05 kernel, whose 128-row tiles
 // need barriers and k ranges through memory, in brackets): one row of 2048 ->
-// 8192 8.2 us (18), 16 rows 10.7 (17.3); one row of 1000 -> 512 1.9 (5.3).
-// From 17 rows on x, which every block reads whole, costs as much as the
-// weights, and the other kernel is as fast (32 rows of 4096 -> 4096: 14.6 us
-// against 12.3).  One row of a 4096 x 12288 gated block, two launches, the
-// second's first loads under the first's end: 51 us, 5.9 TB/s.
+// 8192 7.8 us (10.1), of 4096 -> 4096 7.5 (11.9), of 1024 -> 1024 2.4 (6.2); one
+// row of 4096 -> 12288 18.4, 5.5 TB/s.  From 9 rows on the two come together,
+// because every block reads all of x: few_rows in dense_api.cu has the rule.
+// One row of a 4096 x 12288 gated block, two launches, the second's first loads
+// under the first's end: 50 us, 6.0 TB/s.
 #include <algorithm>
 
 #include "dense_internal.h"

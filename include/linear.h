@@ -13,7 +13,7 @@
  * 16-bit results are rounded once, to nearest even.  No kernel uses atomics:
  * results are bit-identical from run to run on one device.
  *
- * float32 operands (of more than 16 rows) are multiplied as three bfloat16
+ * float32 operands (of more than 8 rows) are multiplied as three bfloat16
  * parts each (all 24 bits of their significands), with sums at least as exact as
  * float32 ones; an infinite operand may then give NaN where a plain product
  * gives an infinity.

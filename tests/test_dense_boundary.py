@@ -203,3 +203,19 @@ def test_plans(lib):
     assert "whole=0 split=" in plan(64, 8192, 256, dtype="bf16")
     for a in ((3, 5, 7), (100, 1000, 3), (5000, 70, 900), (64, 30000, 64)):
         assert plan(*a, dtype="f16") == plan(*a, dtype="f16")
+
+
+def test_plans_of_few_rows(lib):
+    """Up to 8 rows one kernel; to 16 it, unless the tensor cores are the quicker."""
+    def few(rows, c_in, c_out, dtype, **kw):
+        p = conv.make_linear_problem(rows, c_in, c_out, dtype=dtype, **kw)
+        return conv.conv_linear_describe_plan(p, 0, 152).startswith("few_rows")
+    for dtype in ("f32", "f16", "bf16"):
+        assert few(8, 1001, 20000, dtype) and few(8, 1000, 20000, dtype)
+        assert few(9, 1000, 1000, dtype) and not few(17, 1000, 1000, dtype)
+    for dtype in ("f16", "bf16"):
+        assert few(9, 1000, 9999, dtype) and not few(9, 1000, 10000, dtype)
+        assert few(16, 1001, 20000, dtype) and few(16, 1000, 20000, dtype, x_stride=1001)  # operands would be copied
+        assert few(16, 1000, 20000, dtype, flags=conv.FLAG_LINEAR_UNALIGNED)
+    assert few(16, 1000, 20000, "f32") and not few(9, 1001, 100, "f32")
+    assert not few(9, 1000, 100, "f32", w_stride=1002)

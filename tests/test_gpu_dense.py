@@ -218,6 +218,32 @@ def test_gated_other_kernels(flags):
     gated_case(150, 72, 136, 64, "f16", flags=flags)
 
 
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("rows", [8, 9, 16])
+def test_few_rows_on_both_sides_of_the_rule(rows, dtype):
+    """From 9 rows on, many outputs (16 bits) and rows of no whole 16-byte pieces (float32) go to the tensor cores."""
+    linear_case(rows, 72, 10008, dtype, act="silu", seed=31)
+    linear_case(rows, 72, 5000, dtype, seed=32)
+    linear_case(rows, 73, 200, dtype, seed=33)
+    gated_case(rows, 64, 5008, 40, dtype, seed=34)
+    gated_case(rows, 64, 5003, 40, dtype, seed=35)
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_few_rows_at_any_address(dtype):
+    """16 rows whose size alone would choose the tensor cores, at odd addresses, with scratch and without."""
+    x, w = rand(16, 81, dtype=dtype, seed=36).cuda()[:, 1:], rand(6001 * 80 + 1, dtype=dtype, seed=37, scale=0.1).cuda()
+    w = w[1:].view(6001, 80)
+    want = ref.linear64(*wide(x.cpu(), w.cpu(), None, None), "identity", 0, 0, False, dtype)["y"]
+    ref.check(conv.linear(x, w), want)
+    y = torch.empty(16, 6001, dtype=ref.TORCH[dtype], device="cuda")
+    dense = x.contiguous()
+    p = conv.make_linear_problem(16, 80, 6001, dtype=dtype)
+    n = conv.conv_linear_scratch_bytes(p)
+    conv.conv_linear_forward(p, dense, w, None, None, y, None, torch.empty(n, dtype=torch.uint8, device="cuda") if n else None, n)
+    ref.check(y, want)
+
+
 def test_gated_some_gradients_and_no_rows():
     x, wg, wu, wd = (t.cuda() for t in (rand(70, 48, dtype="bf16", seed=1), rand(96, 48, dtype="bf16", seed=2),
                                         rand(96, 48, dtype="bf16", seed=3), rand(48, 96, dtype="bf16", seed=4)))
