@@ -209,11 +209,11 @@ def _rows(t, width, what):
     if n == 2 and strides[0] >= width:
         rows, stride = shape[0], strides[0]
         return rows, stride if rows > 1 else 0
-    rows, stride = 1, 0
+    rows, stride = 1, None
     for i in range(n - 2, -1, -1):
         if shape[i] == 1:
             continue
-        if stride == 0:
+        if stride is None:  # (0 is a stride: a broadcast dimension, whose rows are one row)
             stride = strides[i]
         elif strides[i] != stride * rows:
             raise ValueError(f"{what}: rows must be evenly spaced")

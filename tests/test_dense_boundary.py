@@ -219,3 +219,42 @@ def test_plans_of_few_rows(lib):
         assert few(16, 1000, 20000, dtype, flags=conv.FLAG_LINEAR_UNALIGNED)
     assert few(16, 1000, 20000, "f32") and not few(9, 1001, 100, "f32")
     assert not few(9, 1000, 100, "f32", w_stride=1002)
+
+
+def test_rows_of_broadcast_dimensions_are_refused():
+    """A dimension of stride 0 anywhere among the leading ones: its rows lie over each other, not one after another."""
+    for bad in (torch.zeros(3, 1, 8).expand(3, 4, 8), torch.zeros(2, 1, 1, 8).expand(2, 3, 4, 8),
+                torch.zeros(2, 3, 1, 8).expand(2, 3, 4, 8), torch.zeros(2, 1, 4, 8).expand(2, 3, 4, 8),
+                torch.zeros(1, 4, 8).expand(3, 4, 8), torch.zeros(1, 1, 8).expand(3, 4, 8),
+                torch.zeros(3, 1, 20)[:, :, :8].expand(3, 4, 8)):
+        for rows in (dense._rows, dense._rows_dense):
+            with pytest.raises(ValueError):
+                rows(bad, 8, "x")
+    with pytest.raises(ValueError):
+        dense._rows(torch.zeros(3, 1, 1).expand(3, 4, 1), 1, "x")  # rows of one value
+    # dimensions of one element have no stride
+    assert dense._rows(torch.zeros(1, 8).expand(1, 8), 8, "x") == (1, 0)
+    assert dense._rows(torch.zeros(3, 1, 8).expand(3, 1, 8), 8, "x") == (3, 8)
+
+
+class _OnDevice(torch.Tensor):
+    """A host tensor that says it is on device 0: what is refused before anything is enqueued can be tried without one."""
+
+    def get_device(self):
+        return 0
+
+
+@pytest.mark.skipif(torch.cuda.is_available(), reason="host addresses: for machines that could not use them")
+def test_broadcast_operands_are_refused():
+    def on(t):
+        return t.as_subclass(_OnDevice)
+    x, w = on(torch.zeros(3, 4, 8)), on(torch.zeros(6, 8))
+    wide, row = on(torch.zeros(3, 1, 8).expand(3, 4, 8)), on(torch.zeros(3, 1, 6).expand(3, 4, 6))
+    g, d = on(torch.zeros(12, 8)), on(torch.zeros(6, 12))
+    for call in (lambda: conv.linear(wide, w), lambda: conv.linear(x, w, residual=row), lambda: conv.linear(x, w, out=row),
+                 lambda: conv.linear_backward(row, x, w), lambda: conv.linear_backward(on(torch.zeros(3, 4, 6)), wide, w),
+                 lambda: conv.gated_ffn(wide, g, g, d), lambda: conv.gated_ffn(x, g, g, d, row),
+                 lambda: conv.gated_ffn(x, g, g, d, out=row), lambda: conv.gated_ffn_backward(row, x, g, g, d, None),
+                 lambda: conv.gated_ffn_backward(on(torch.zeros(3, 4, 6)), wide, g, g, d, None)):
+        with pytest.raises(ValueError, match="rows must not overlap|rows must be evenly spaced"):
+            call()
