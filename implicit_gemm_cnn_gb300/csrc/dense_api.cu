@@ -79,6 +79,12 @@ conv_status validate(const conv_gated_problem* p, GatedShape* s) {
 }
 
 bool aligned16(const void* p) { return reinterpret_cast<uintptr_t>(p) % 16 == 0; }
+// Whether an address is no multiple of its element's size (a typed access there would be a fault).
+bool misplaced(size_t size, std::initializer_list<const void*> list) {
+  uintptr_t all = 0;
+  for (const void* p : list) all |= reinterpret_cast<uintptr_t>(p);
+  return all % size != 0;
+}
 
 // ---- one product: which kernel, and its scratch ------------------------------
 enum Variant { V_FFMA = 0, V_TC = 1, V_FEW = 2 };
@@ -538,6 +544,8 @@ conv_status conv_linear_forward(const conv_linear_problem* p, const void* x, con
   ranges.add_out(y, p->rows, p->c_out * es, sh.ldy * es);
   ranges.add_out(pre, static_cast<size_t>(p->rows) * p->c_out * 4);
   if (ranges.clash()) return CONV_ERR_ALIAS;
+  if (misplaced(es, {x, w, p->has_bias ? bias : nullptr, p->has_residual ? residual : nullptr, y}) || misplaced(4, {pre}))
+    return CONV_ERR_ARG;
   int dev, sm;
   st = current_device(&dev, &sm);
   if (st != CONV_OK) return st;
@@ -583,6 +591,7 @@ conv_status conv_linear_backward(const conv_linear_problem* p, const void* x, co
   ranges.add_out(dbias, p->c_out * es);
   ranges.add_out(dresidual, static_cast<size_t>(p->rows) * p->c_out * es);
   if (ranges.clash()) return CONV_ERR_ALIAS;
+  if (misplaced(es, {x, w, dy, dx, dw, dbias, dresidual}) || misplaced(4, {pre})) return CONV_ERR_ARG;
   int dev, sm;
   st = current_device(&dev, &sm);
   if (st != CONV_OK) return st;
@@ -685,6 +694,7 @@ conv_status conv_gated_forward(const conv_gated_problem* p, const void* x, const
   ranges.add_out(y, p->rows, p->c_out * es, sh.ldy * es);
   ranges.add_out(saved, keep.total);
   if (ranges.clash()) return CONV_ERR_ALIAS;
+  if (misplaced(es, {x, w_gate, w_up, w_down, p->has_residual ? residual : nullptr, y})) return CONV_ERR_ARG;
   int dev, sm;
   st = current_device(&dev, &sm);
   if (st != CONV_OK) return st;
@@ -750,6 +760,7 @@ conv_status conv_gated_backward(const conv_gated_problem* p, const void* x, cons
   ranges.add_out(dw_up, wbytes);
   ranges.add_out(dw_down, wdbytes);
   if (ranges.clash()) return CONV_ERR_ALIAS;
+  if (misplaced(es, {x, w_gate, w_up, w_down, dy, dx, dw_gate, dw_up, dw_down})) return CONV_ERR_ARG;
   int dev, sm;
   st = current_device(&dev, &sm);
   if (st != CONV_OK) return st;
@@ -842,7 +853,7 @@ conv_status conv_clip_grads(int64_t count, const void* const* in, void* const* o
   size_t need;
   conv_status st = conv_clip_scratch_bytes(count, sizes, &need);
   if (st != CONV_OK) return st;
-  if (!(max_norm >= 0.0f) || !(eps >= 0.0f)) return CONV_ERR_ARG;
+  if (!(max_norm >= 0.0f) || !(eps >= 0.0f) || misplaced(4, {norm})) return CONV_ERR_ARG;
   try {  // the list of ranges is host memory
     st = clip_check(count, in, out, sizes, dtypes, norm, scratch, scratch_bytes, need);
   } catch (...) {

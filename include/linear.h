@@ -19,8 +19,9 @@
  * gives an infinity.
  *
  * Matrices are row-major.  A row stride counts elements from one row to the
- * next; 0 stands for dense rows (stride = width).  Pointers and strides of any
- * alignment are legal.  16-bit operands whose address or row stride in bytes is
+ * next; 0 stands for dense rows (stride = width).  Strides of any size, and
+ * addresses at any multiple of the element's size, are legal (others are
+ * CONV_ERR_ARG).  16-bit operands whose address or row stride in bytes is
  * no multiple of 16 are first copied into scratch rows that are; the scratch
  * queries go by the strides, and by CONV_LINEAR_FLAG_UNALIGNED for addresses
  * (without that flag, or the scratch it asks for, an unaligned address is read
@@ -82,8 +83,9 @@ CONV_API conv_status conv_linear_describe_plan(const conv_linear_problem* p, int
  * (z; with CONV_LINEAR_FLAG_RESIDUAL_LAST, z without the residual) in float32,
  * [rows][c_out] dense, for conv_linear_backward: float32, because 16 bits here
  * would add a rounding error of the size of the result's own to every gradient.
- * Errors: those of conv_linear_scratch_bytes; CONV_ERR_NULL, CONV_ERR_SCRATCH
- * (too small, or not 256-byte aligned), CONV_ERR_ALIAS (y, pre or scratch
+ * Errors: those of conv_linear_scratch_bytes; CONV_ERR_NULL, CONV_ERR_ARG (an
+ * address no multiple of its element's size), CONV_ERR_SCRATCH (too small, or
+ * not 256-byte aligned), CONV_ERR_ALIAS (y, pre or scratch
  * overlaps an operand; columns side by side in one wider matrix do not),
  * CONV_ERR_CUDA. */
 CONV_API conv_status conv_linear_forward(const conv_linear_problem* p, const void* x, const void* w,

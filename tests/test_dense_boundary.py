@@ -258,3 +258,31 @@ def test_broadcast_operands_are_refused():
                  lambda: conv.gated_ffn_backward(on(torch.zeros(3, 4, 6)), wide, g, g, d, None)):
         with pytest.raises(ValueError, match="rows must not overlap|rows must be evenly spaced"):
             call()
+
+
+def test_addresses_inside_an_element_are_refused(lib):
+    """Every operand and output, each type, off its element's boundary: refused before a device is asked for."""
+    at = [0x1000000 * i for i in range(1, 12)]
+    for dtype, offs in (("f32", (1, 2, 3)), ("f16", (1,)), ("bf16", (1,))):
+        linear = conv.make_linear_problem(20, 64, 64, dtype=dtype, act="relu", has_bias=True, has_residual=True)
+        gated = conv.make_gated_problem(20, 64, 64, 64, dtype=dtype, has_residual=True)
+        for fn, p, n, aligned in ((lib.conv_linear_forward, linear, 6, ()), (lib.conv_linear_backward, linear, 8, ()),
+                                  (lib.conv_gated_forward, gated, 7, (6,)), (lib.conv_gated_backward, gated, 10, (5,))):
+            def call(args):
+                return fn(ctypes.byref(p), *args, None, 0, None)
+            for i in range(n):
+                for off in offs:
+                    args = at[:n]
+                    args[i] += off
+                    assert call(args) == ARG, (fn.__name__, dtype, i, off)
+            if not torch.cuda.is_available():
+                assert call(at[:n]) == DEVICE
+    # float32 beside 16-bit operands: the activation's argument, and the norm
+    p = conv.make_linear_problem(20, 64, 64, dtype="f16", act="relu")
+    assert lib.conv_linear_forward(ctypes.byref(p), *at[:2], None, None, at[4], at[5] + 2, None, 0, None) == ARG
+    assert lib.conv_linear_backward(ctypes.byref(p), *at[:2], at[2] + 2, *at[3:8], None, 0, None) == ARG
+    one = (ctypes.c_int64 * 1)(64)
+    need = conv.conv_clip_scratch_bytes([64])
+    for off in (1, 2, 3):
+        assert lib.conv_clip_grads(1, (ctypes.c_void_p * 1)(at[0]), None, one, (ctypes.c_int32 * 1)(1), 1.0, 0.0, at[1] + off,
+                                   at[2], need, None) == ARG
