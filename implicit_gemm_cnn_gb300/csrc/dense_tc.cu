@@ -111,6 +111,7 @@ DenseTcPlan search(const DenseGemm& g, int f32, int sm) {
   double best_t = 0.0;
   for (int cg = f32 ? 1 : 2; cg >= 1; --cg) {
     const long long slots = sm / cg;
+    if (slots < 1) continue;  // (one SM has no pair)
     for (int nt = cg == 2 ? 256 : 128; nt >= 64; nt -= 32) {
       if ((g.dual || f32) && nt % 64) continue;
       if (g.b_mn && nt / cg % 64) continue;  // copied in blocks of 64 columns: other widths would load more than they use

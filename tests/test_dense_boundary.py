@@ -3,6 +3,8 @@ before anything touches a device, and the Python checks of arguments."""
 import ctypes
 import os
 import re
+import subprocess
+import sys
 
 import pytest
 import torch
@@ -286,3 +288,23 @@ def test_addresses_inside_an_element_are_refused(lib):
     for off in (1, 2, 3):
         assert lib.conv_clip_grads(1, (ctypes.c_void_p * 1)(at[0]), None, one, (ctypes.c_int32 * 1)(1), 1.0, 0.0, at[1] + off,
                                    at[2], need, None) == ARG
+
+
+def test_plans_for_any_sm_count():
+    """In a process of its own: a division by zero would end it.  Every SM count has a plan that keeps to its SMs."""
+    code = """
+import sys
+sys.path.insert(0, %r)
+import implicit_gemm_cnn_gb300 as conv
+for dtype in ("f32", "f16", "bf16"):
+    for size in ((64, 1024, 1024), (1, 64, 64), (300, 70, 900), (5000, 2000, 3)):
+        for flags in (0, conv.FLAG_LINEAR_FORCE_FFMA, conv.FLAG_LINEAR_NO_FEW_ROWS):
+            p = conv.make_linear_problem(*size, dtype=dtype, flags=flags)
+            for which in (0, 1, 2):
+                for sm in (1, 2, 3, 151, 2**31 - 1):
+                    d = conv.conv_linear_describe_plan(p, which, sm)
+                    assert f"sms={sm} " in d and not (sm == 1 and "sms_per_tile=2" in d), d
+print("planned")
+""" % ROOT
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "planned", (r.returncode, r.stderr[-500:])
