@@ -87,6 +87,22 @@ bool misplaced(size_t size, std::initializer_list<const void*> list) {
 }
 
 // ---- one product: which kernel, and its scratch ------------------------------
+// Which kernels a call may run.
+struct Mode {
+  bool copies;   // every 16-bit operand is copied
+  bool tc;       // the tensor-core kernels may run
+  bool few;      // the kernel for few rows may run (it takes any alignment)
+  bool ranges;   // the CUDA-core kernel may sum in k ranges (it needs scratch then)
+};
+Mode mode_of(uint32_t flags, int dtype) {
+  Mode m;
+  m.tc = !(flags & CONV_LINEAR_FLAG_FORCE_FFMA);
+  m.copies = m.tc && dtype != CONV_F32 && (flags & CONV_LINEAR_FLAG_UNALIGNED);
+  m.few = !(flags & (CONV_LINEAR_FLAG_FORCE_FFMA | CONV_LINEAR_FLAG_NO_FEW_ROWS));
+  m.ranges = true;
+  return m;
+}
+
 enum Variant { V_FFMA = 0, V_TC = 1, V_FEW = 2 };
 struct Product {
   Variant variant;
@@ -97,21 +113,21 @@ struct Product {
   int launches, sm;
 };
 
-// `g` without addresses.  `tc`: 16-bit operands with rows a tensor-core copy can take.
-Product plan_product(const DenseGemm& g, int dtype, bool tc, bool few, int sm) {
+// `g` without addresses.  `few`: the kernel for few rows takes it.
+Product plan_product(const DenseGemm& g, int dtype, const Mode& mode, bool few, int sm) {
   Product r = {};
   r.sm = sm;
   if (few) {
     r.variant = V_FEW;
     r.split = 1;
-  } else if (tc) {
+  } else if (mode.tc) {
     r.variant = V_TC;
     r.tc = dense_tc_plan(g, dtype, sm);
     r.split = r.tc.split;
     r.part_bytes = r.tc.part_bytes;
   } else {
     r.variant = V_FFMA;
-    r.ffma = dense_ffma_plan(g, sm);
+    r.ffma = dense_ffma_plan(g, sm, mode.ranges);
     r.split = r.ffma.split;
   }
   if (r.variant == V_FFMA && r.split > 1)
@@ -197,20 +213,6 @@ DenseGemm make_gemm(long long m, long long n, long long k, int a_mn, int b_mn, l
 }
 
 // ---- linear -----------------------------------------------------------------
-// Whether copies are planned for unaligned addresses, or the CUDA-core kernel reads them.
-struct Mode {
-  bool copies;   // every 16-bit operand is copied
-  bool tc;       // the tensor-core kernels may run
-  bool few;      // the kernel for few rows may run (it takes any alignment)
-};
-Mode mode_of(uint32_t flags, int dtype) {
-  Mode m;
-  m.tc = !(flags & CONV_LINEAR_FLAG_FORCE_FFMA);
-  m.copies = m.tc && dtype != CONV_F32 && (flags & CONV_LINEAR_FLAG_UNALIGNED);
-  m.few = !(flags & (CONV_LINEAR_FLAG_FORCE_FFMA | CONV_LINEAR_FLAG_NO_FEW_ROWS));
-  return m;
-}
-
 // Whether the kernel for few rows takes a product: up to 8 rows always, from 9 to 16 (two MMAs a weight piece; 16 sums
 // in float32) unless the tensor-core kernel, if it may run, is the quicker one.  Measured, that kernel in brackets:
 //   float32 rows that are no whole 16-byte pieces are loaded one by one: 9 rows of 2047 -> 2048 27.5 us (21.1), of
@@ -252,7 +254,7 @@ LinearPlan plan_linear(const conv_linear_problem* p, const LinearShape& sh, cons
   e.act = p->act; e.alpha = p->act_alpha; e.beta = p->act_beta;
   e.residual_last = (p->flags & CONV_LINEAR_FLAG_RESIDUAL_LAST) != 0;
   e.ldr = sh.ldr; e.ldy = sh.ldy; e.ldp = p->c_out;
-  if (p->rows > 0) r.pfwd = plan_product(r.fwd, p->dtype, mode.tc, few, sm);
+  if (p->rows > 0) r.pfwd = plan_product(r.fwd, p->dtype, mode, few, sm);
   r.part_off = l.take(r.pfwd.part_bytes);
   r.total = l.total;
   return r;
@@ -277,12 +279,12 @@ LinearPlan plan_linear_backward(const conv_linear_problem* p, const LinearShape&
     r.dx = make_gemm(p->rows, p->c_in, p->c_out, 0, 1, ldz, r.w.ld);
     r.dx.b_pad = r.w.on;
     r.dx.epi.ldy = p->c_in;
-    r.pdx = plan_product(r.dx, p->dtype, mode.tc, false, sm);
+    r.pdx = plan_product(r.dx, p->dtype, mode, false, sm);
     r.dw = make_gemm(p->c_out, p->c_in, p->rows, 1, 1, ldz, r.x.ld);
     r.dw.a_pad = r.dz || r.z.on;
     r.dw.b_pad = r.x.on;
     r.dw.epi.ldy = p->c_in;
-    r.pdw = plan_product(r.dw, p->dtype, mode.tc, false, sm);
+    r.pdw = plan_product(r.dw, p->dtype, mode, false, sm);
   }
   r.part_off = l.take(std::max(r.pdx.part_bytes, r.pdw.part_bytes));
   r.total = l.total;
@@ -325,7 +327,8 @@ bool scratch_bad(const void* scratch, size_t have, size_t need) {
 }
 
 // The mode for these addresses: where one is unaligned, copies if the scratch
-// has room for them, else the CUDA-core kernel.
+// has room for them, else the CUDA-core kernel, its sums whole where there is no room
+// for ranges of them.
 template <typename PlanFn>
 auto plan_for(uint32_t flags, int dtype, std::initializer_list<const void*> operands, size_t have, PlanFn plan)
     -> decltype(plan(Mode{})) {
@@ -337,6 +340,9 @@ auto plan_for(uint32_t flags, int dtype, std::initializer_list<const void*> oper
     auto r = plan(m);
     if (r.total <= have) return r;
     m.copies = m.tc = false;  // (the kernel for few rows stays)
+    r = plan(m);
+    if (r.total <= have) return r;
+    m.ranges = false;  // what is left is within the scratch that the query asked for without copies
   }
   return plan(m);
 }
@@ -385,10 +391,10 @@ GatedPlan plan_gated(const conv_gated_problem* p, const GatedShape& sh, const Mo
     r.up.epi.mode = EPI_GATED;
     r.up.epi.act = p->act; r.up.epi.alpha = p->act_alpha; r.up.epi.beta = p->act_beta;
     r.up.epi.ldy = sh.ldh; r.up.epi.ldp = sh.ldh;
-    r.pup = plan_product(r.up, p->dtype, mode.tc, few, sm);
+    r.pup = plan_product(r.up, p->dtype, mode, few, sm);
     r.down = make_gemm(p->rows, p->c_out, p->hidden, 0, 0, r.h.ld, r.wd.ld);
     r.down.epi.ldr = sh.ldr; r.down.epi.ldy = sh.ldy;
-    r.pdown = plan_product(r.down, p->dtype, mode.tc, few, sm);
+    r.pdown = plan_product(r.down, p->dtype, mode, few, sm);
   }
   r.part_off = l.take(std::max(r.pup.part_bytes, r.pdown.part_bytes));
   r.total = l.total;
@@ -416,26 +422,26 @@ GatedPlan plan_gated_backward(const conv_gated_problem* p, const GatedShape& sh,
     r.dh.epi.mode = EPI_GATED_BWD;
     r.dh.epi.act = p->act; r.dh.epi.alpha = p->act_alpha; r.dh.epi.beta = p->act_beta;
     r.dh.epi.ldy = sh.ldh; r.dh.epi.ldp = sh.ldh;
-    r.pdh = plan_product(r.dh, p->dtype, mode.tc, false, sm);
+    r.pdh = plan_product(r.dh, p->dtype, mode, false, sm);
     r.dx = make_gemm(p->rows, p->c_in, p->hidden, 0, 1, r.dg.ld, r.wg.ld);
     r.dx.b_pad = r.wg.on;
     r.dx.segs = 2;
     r.dx.epi.ldy = p->c_in;
-    r.pdx = plan_product(r.dx, p->dtype, mode.tc, false, sm);
+    r.pdx = plan_product(r.dx, p->dtype, mode, false, sm);
     r.dwgu = make_gemm(p->hidden, p->c_in, p->rows, 1, 1, r.dg.ld, r.x.ld);
     r.dwgu.a_pad = 1;
     r.dwgu.b_pad = r.x.on;
     r.dwgu.batch = 2;
     r.dwgu.epi.ldy = p->c_in;
-    r.pdwgu = plan_product(r.dwgu, p->dtype, mode.tc, false, sm);
+    r.pdwgu = plan_product(r.dwgu, p->dtype, mode, false, sm);
     DenseGemm one = r.dwgu;
     one.batch = 1;
-    r.pdw1 = plan_product(one, p->dtype, mode.tc, false, sm);
+    r.pdw1 = plan_product(one, p->dtype, mode, false, sm);
     r.dwd = make_gemm(p->c_out, p->hidden, p->rows, 1, 1, r.dy.ld, r.h.ld);
     r.dwd.a_pad = r.dy.on;
     r.dwd.b_pad = 1;
     r.dwd.epi.ldy = p->hidden;
-    r.pdwd = plan_product(r.dwd, p->dtype, mode.tc, false, sm);
+    r.pdwd = plan_product(r.dwd, p->dtype, mode, false, sm);
   }
   r.part_off = l.take(std::max({r.pdh.part_bytes, r.pdx.part_bytes, r.pdwgu.part_bytes, r.pdw1.part_bytes, r.pdwd.part_bytes}));
   r.total = l.total;

@@ -448,7 +448,7 @@ cudaError_t dz_go(const void* dy, long long ld_dy, const float* pre, void* dz, l
 
 }  // namespace
 
-DenseFfmaPlan dense_ffma_plan(const DenseGemm& g, int sm) {
+DenseFfmaPlan dense_ffma_plan(const DenseGemm& g, int sm, bool ranges) {
   DenseFfmaPlan p;
   auto tiles = [&](int bm, int bnl) {
     return ((g.M + bm - 1LL) / bm) * ((g.N + bnl - 1LL) / bnl) * g.batch;
@@ -460,7 +460,7 @@ DenseFfmaPlan dense_ffma_plan(const DenseGemm& g, int sm) {
   const long long t = tiles(p.bm, p.bn), k = static_cast<long long>(g.segs) * g.K;
   // two blocks per SM; k in ranges of at least 128 terms where the tiles are fewer
   long long split = 1;
-  if (t < 2LL * sm && k >= 256) split = std::min<long long>({(2LL * sm) / t, k / 128, 16});
+  if (ranges && t < 2LL * sm && k >= 256) split = std::min<long long>({(2LL * sm) / t, k / 128, 16});
   if (split < 1) split = 1;
   p.k_per_split = ((k + split - 1) / split + kBK - 1) / kBK * kBK;
   p.split = static_cast<int>((k + p.k_per_split - 1) / p.k_per_split);

@@ -40,7 +40,7 @@ struct DenseFfmaPlan {
   int split;             // k ranges
   long long k_per_split;
 };
-DenseFfmaPlan dense_ffma_plan(const DenseGemm& g, int sm);
+DenseFfmaPlan dense_ffma_plan(const DenseGemm& g, int sm, bool ranges);
 cudaError_t launch_dense_ffma(const DenseFfmaPlan& p, const DenseGemm& g, int dtype, cudaStream_t s);
 
 // Tensor-core product: 16-bit operands on 16-byte boundaries (dense_tc.cuh), or

@@ -25,7 +25,8 @@
  * no multiple of 16 are first copied into scratch rows that are; the scratch
  * queries go by the strides, and by CONV_LINEAR_FLAG_UNALIGNED for addresses
  * (without that flag, or the scratch it asks for, an unaligned address is read
- * by the CUDA-core kernel, which is slower).
+ * by the CUDA-core kernel, which is slower; the scratch of an aligned call is
+ * enough for it).
  */
 #ifndef CONV_GB300_LINEAR_H
 #define CONV_GB300_LINEAR_H

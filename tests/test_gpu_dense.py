@@ -572,3 +572,48 @@ def test_refusals_of_tensors():
         conv.clip_grad_norm([x, x], 1.0)
     with pytest.raises(conv.ConvError, match="ARG"):
         conv.clip_grad_norm([x], -1.0)
+
+
+def queried(n):
+    return (torch.empty(n, dtype=torch.uint8, device="cuda") if n else None), n
+
+
+@pytest.mark.parametrize("rows", [16, 64])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_unaligned_operands_with_the_scratch_of_aligned_ones(dtype, rows):
+    """Sums long enough for the CUDA-core kernel to cut, which it must not without scratch: each pass, with exactly what
+    its query asks for an aligned call."""
+    k, n, hidden = 1024, 1024, 640
+
+    def off(*shape, seed, scale=1.0):  # one value off a 16-byte boundary
+        t = rand(shape[0] * shape[1] + 1, dtype=dtype, seed=seed, scale=scale).cuda()
+        return t[1:].view(shape)
+    x, w, dy = off(rows, k, seed=1), off(n, k, seed=2, scale=k ** -0.5), off(rows, n, seed=3, scale=0.1)
+    new = lambda *shape: torch.full(shape, 7.0, dtype=ref.TORCH[dtype], device="cuda")  # noqa: E731
+    for act in ("identity", "silu"):
+        p = conv.make_linear_problem(rows, k, n, dtype=dtype, act=act)
+        y, pre = new(rows, n), torch.empty(rows, n, device="cuda")
+        conv.conv_linear_forward(p, x, w, None, None, y, pre, *queried(conv.conv_linear_scratch_bytes(p)))
+        want = ref.linear64(*wide(x.cpu(), w.cpu(), None, None), act, 0, 0, False, dtype)
+        ref.check(y, want["y"], "y")
+        ref.check(pre, want["z"], "pre")
+        outs = new(rows, k), new(n, k), new(n), new(rows, n)
+        conv.conv_linear_backward(p, x, w, pre, dy, *outs, *queried(conv.conv_linear_backward_scratch_bytes(p)))
+        back = ref.linear_backward64(*wide(dy.cpu(), x.cpu(), w.cpu()), *want["z"], act, 0, 0, False, dtype)
+        for name, got in zip(("dx", "dw", "dbias", "dresidual"), outs):
+            ref.check(got, back[name], (act, name))
+    p = conv.make_gated_problem(rows, k, hidden, n, dtype=dtype)
+    wg, wu, wd = (off(hidden, k, seed=4, scale=k ** -0.5), off(hidden, k, seed=5, scale=k ** -0.5),
+                  off(n, hidden, seed=6, scale=hidden ** -0.5))
+    want = ref.gated64(*wide(x.cpu(), wg.cpu(), wu.cpu(), wd.cpu()), None, "silu", 0, 0, dtype, dy.cpu().double())
+    saved = torch.empty(conv.conv_gated_saved_bytes(p), dtype=torch.uint8, device="cuda")
+    for keep in (None, saved):
+        y = new(rows, n)
+        conv.conv_gated_forward(p, x, wg, wu, wd, None, y, keep, *queried(conv.conv_gated_scratch_bytes(p)))
+        ref.check(y, want["y"], "y")
+    outs = new(rows, k), new(hidden, k), new(hidden, k), new(n, hidden)
+    conv.conv_gated_backward(p, x, wg, wu, wd, saved, dy, *outs, *queried(conv.conv_gated_backward_scratch_bytes(p)))
+    for name, got in zip(("dx", "dw_gate", "dw_up", "dw_down"), outs):
+        ref.check(got, want[name], name)
+    torch.cuda.synchronize()
+    assert conv.conv_linear_device_error() == 0
