@@ -210,18 +210,21 @@ __global__ void __launch_bounds__(256) dense_reduce(const DenseGemm g) {
   dense_epilogue<T, 4>(g.epi, which, m, col, ok, v, u);
 }
 
-// The three planes of 4 values: v = p0 + p1 + p2, exactly (for |v| above 2^-110; below, to 2^-133).  An infinity or a
-// NaN is its own first plane; a value that would round up to infinity is cut instead.
+// The three planes of 4 values: v = p0 + 2^-kPlaneScale1 p1 + 2^-kPlaneScale2 p2, exactly, for every float32 down to the
+// smallest subnormal: unscaled, p1 and p2 of values below 2^-110 would end where bfloat16's range does (2^-133).  |p1| and
+// |p2| stay below |v| / 2.  An infinity or a NaN is its own first plane; a value that would round up to infinity is cut
+// instead.
 __device__ __forceinline__ void put_planes(const float (&v)[4], __nv_bfloat16* out, long long plane) {
+  constexpr float kUp1 = 1u << kPlaneScale1, kUp2 = 1u << (kPlaneScale2 - kPlaneScale1);
   uint16_t h[3][4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     __nv_bfloat16 p0 = __float2bfloat16_rn(v[j]);
     const bool finite = fabsf(v[j]) <= 3.402823466e38f;
     if (finite && __hisinf(p0)) p0 = __float2bfloat16_rz(v[j]);
-    const float r1 = finite ? v[j] - __bfloat162float(p0) : 0.0f;
+    const float r1 = finite ? (v[j] - __bfloat162float(p0)) * kUp1 : 0.0f;
     const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
-    const __nv_bfloat16 p2 = __float2bfloat16_rn(r1 - __bfloat162float(p1));
+    const __nv_bfloat16 p2 = __float2bfloat16_rn((r1 - __bfloat162float(p1)) * kUp2);
     h[0][j] = __bfloat16_as_ushort(p0);
     h[1][j] = __bfloat16_as_ushort(p1);
     h[2][j] = __bfloat16_as_ushort(p2);

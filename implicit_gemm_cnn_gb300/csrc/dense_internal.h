@@ -68,7 +68,9 @@ cudaError_t launch_dense_reduce(const DenseGemm& g, int dtype, cudaStream_t s);
 
 // Operands' copies, in one launch: 16-bit rows copied to a pitch of `ld`
 // elements, or (planes) the three bfloat16 planes of float32 rows, rows of ld (a
-// multiple of 64) elements, planes rows * ld elements apart.
+// multiple of 64) elements, planes rows * ld elements apart, the second and third
+// multiplied by these powers of two.
+constexpr int kPlaneScale1 = 7, kPlaneScale2 = 16;
 struct CopyJob {
   const void* in;
   void* out;

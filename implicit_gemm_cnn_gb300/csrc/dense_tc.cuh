@@ -207,10 +207,18 @@ __device__ __forceinline__ void mma_stage(uint32_t d, uint64_t a, uint64_t b, ui
   else CONV_MMA_STAGE("1", ".b64 [%7]");
 #undef CONV_MMA_STAGE
 }
-// The MMAs of 64 terms alone (one SM).
-template <int A_STEP, int B_STEP>
-__device__ __forceinline__ void mma_terms(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t acc) {
-  mma_f16(d, a, b, idesc, acc);
+// One MMA onto the accumulator's values divided by 2^DOWN (one SM).
+template <int DOWN>
+__device__ __forceinline__ void mma_onto(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  asm volatile("{\n .reg .pred p;\n setp.eq.b32 p, 0, 0;\n tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p, %4;\n}\n" ::"r"(d),
+               "l"(a), "l"(b), "r"(idesc), "n"(DOWN)
+               : "memory");
+}
+// The MMAs of 64 terms alone (one SM).  DOWN < 0: a new sum; else onto the one that is there, divided by 2^DOWN.
+template <int DOWN, int A_STEP, int B_STEP>
+__device__ __forceinline__ void mma_terms(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc) {
+  if constexpr (DOWN > 0) mma_onto<DOWN>(d, a, b, idesc);
+  else mma_f16(d, a, b, idesc, DOWN == 0);
   mma_f16(d, a + A_STEP, b + B_STEP, idesc, 1);
   mma_f16(d, a + 2 * A_STEP, b + 2 * B_STEP, idesc, 1);
   mma_f16(d, a + 3 * A_STEP, b + 3 * B_STEP, idesc, 1);

@@ -2,10 +2,15 @@
 //
 // A float32 value is the exact sum of three bfloat16 values, each the rounding
 // of what the ones before leave (8 significand bits each, 24 in all).  A pass
-// over the operands writes the three as planes; a product then is
-//   a b = a0 b0 + (a0 b1 + a1 b0) + (a1 b1 + a0 b2 + a2 b0)
-// without a1 b2, a2 b1 and a2 b2, which are below 2^-24 of |a b|: six bfloat16
-// products, still three times the CUDA cores' float32 rate and more.
+// over the operands writes the three as planes, the second times 2^7 and the
+// third times 2^16: bfloat16 has float32's exponents, so the remainders of small
+// values would have no room.  (2^8 for the second would let sums of parts
+// overflow that the whole sum does not.)  A product then is
+//   a b = a0 b0 + 2^-7 (a0 b1 + a1 b0 + 2^-7 a1 b1) + 2^-16 (a0 b2 + a2 b0)
+// without a1 b2, a2 b1 and a2 b2, which are below 2^-24 of |a b| (of a factor
+// below 2^-124, 1.5 * 2^-149 of the other): six bfloat16 products, still three
+// times the CUDA cores' float32 rate and more.  The accumulator is divided by
+// the powers of two as the MMAs go on (scale-input-d), at no cost in time.
 //
 // The tensor cores cut their float32 accumulator instead of rounding it (the
 // sum of 1024 positive terms came out 2.2e-6 low, 64 terms 8e-8), so no
@@ -155,13 +160,13 @@ __global__ void __launch_bounds__(kThreads32, 1)
           for (int h = 0; h < kHalves; ++h) {
             const uint32_t d = tmem + buf * 128 + h * cols;
             const uint64_t a = a0 + off, b = b0 + off + h * 3 * b_plane;
-            // the small products first, the large one last
-            mma_terms<kAStep, kBStep>(d, a, b + 2 * b_plane, idesc, 0);
-            mma_terms<kAStep, kBStep>(d, a + 2 * a_plane, b, idesc, 1);
-            mma_terms<kAStep, kBStep>(d, a + a_plane, b + b_plane, idesc, 1);
-            mma_terms<kAStep, kBStep>(d, a, b + b_plane, idesc, 1);
-            mma_terms<kAStep, kBStep>(d, a + a_plane, b, idesc, 1);
-            mma_terms<kAStep, kBStep>(d, a, b, idesc, 1);
+            // the small products first, the large one last; each order's scale is taken off as the next one begins
+            mma_terms<-1, kAStep, kBStep>(d, a, b + 2 * b_plane, idesc);
+            mma_terms<0, kAStep, kBStep>(d, a + 2 * a_plane, b, idesc);
+            mma_terms<kPlaneScale2 - 2 * kPlaneScale1, kAStep, kBStep>(d, a + a_plane, b + b_plane, idesc);
+            mma_terms<kPlaneScale1, kAStep, kBStep>(d, a, b + b_plane, idesc);
+            mma_terms<0, kAStep, kBStep>(d, a + a_plane, b, idesc);
+            mma_terms<kPlaneScale1, kAStep, kBStep>(d, a, b, idesc);
           }
           commit<1>(empty(s));
           commit<1>(acc_full(buf));

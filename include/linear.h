@@ -13,10 +13,11 @@
  * 16-bit results are rounded once, to nearest even.  No kernel uses atomics:
  * results are bit-identical from run to run on one device.
  *
- * float32 operands (of more than 8 rows) are multiplied as three bfloat16
- * parts each (all 24 bits of their significands), with sums at least as exact as
- * float32 ones; an infinite operand may then give NaN where a plain product
- * gives an infinity.
+ * float32 operands (of more than 16 rows; of more than 8 where rows are no whole
+ * 16-byte pieces) are multiplied as three bfloat16 parts each (all 24 bits of
+ * their significands), with sums at least as exact as float32 ones; of a
+ * subnormal operand two units of its last place (2^-148) may be lost.  An
+ * infinite operand may then give NaN where a plain product gives an infinity.
  *
  * Matrices are row-major.  A row stride counts elements from one row to the
  * next; 0 stands for dense rows (stride = width).  Strides of any size, and

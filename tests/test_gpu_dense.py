@@ -617,3 +617,71 @@ def test_unaligned_operands_with_the_scratch_of_aligned_ones(dtype, rows):
         ref.check(got, want[name], name)
     torch.cuda.synchronize()
     assert conv.conv_linear_device_error() == 0
+
+
+def tiny_operands(low, rows, more):
+    """linear and its gradients with operands of 2^-low beside large ones, whose products are of ordinary size; `more`: of
+    two factors, what is added to the bound of their product."""
+    e, high = 2.0 ** -low, 2.0 ** min(low, 122)
+    x, w = rand(rows, 200, dtype="f32", seed=low, scale=e), rand(90, 200, dtype="f32", seed=low + 1, scale=high)
+    dy = rand(rows, 90, dtype="f32", seed=low + 2, scale=e)
+    X, W, DY = cuda(x, w, dy)
+    x, w, dy = wide(x, w, dy)
+    y, pre = conv.linear(X, W, act="relu", save=True)
+    want = ref.linear64(x, w, None, None, "relu", 0, 0, False, "f32")
+    z = want["z"][0], want["z"][1] + more(x, w)
+    ref.check(pre, z, (rows, "pre"))
+    ref.check(y, (want["y"][0], want["y"][1] + 2 * more(x, w)), (rows, "y"))
+    grads = conv.linear_backward(DY, X, W, pre, act="relu", need_dw=False, need_dbias=True)
+    back = ref.linear_backward64(dy, x, w, *z, "relu", 0, 0, False, "f32")
+    ref.check(grads[0], (back["dx"][0], back["dx"][1] + 2 * more(dy, w.T)), (rows, "dx"))
+    ref.check(grads[2], back["dbias"], (rows, "dbias"))
+    big = rand(rows, 90, dtype="f32", seed=low + 3, scale=high)
+    back = ref.linear_backward64(big.double(), x, w, *z, "identity", 0, 0, False, "f32")
+    ref.check(conv.linear_backward(big.cuda(), X, W, need_dx=False)[1],
+              (back["dw"][0], back["dw"][1] + 2 * more(big.double().T, x.T)), (rows, "dw"))
+
+
+@pytest.mark.parametrize("low", [100, 112, 118, 122])
+def test_float32_operands_of_every_magnitude(low):
+    """The bound of float32 sums holds for small operands as for others, in each pass and on both sides of the kernel for
+    few rows."""
+    for rows in (5, 70):
+        tiny_operands(low, rows, lambda a, b: 0.0)
+    scale, e = 2.0 ** min(low, 118), 2.0 ** -low
+    x, dy = rand(70, 64, dtype="f32", seed=1, scale=e), rand(70, 40, dtype="f32", seed=2, scale=e)
+    wg, wu = (rand(136, 64, dtype="f32", seed=i, scale=scale / 8) for i in (3, 4))
+    wd = rand(40, 136, dtype="f32", seed=5, scale=2.0 ** 110)
+    args = cuda(x, wg, wu, wd)
+    y, saved = conv.gated_ffn(*args, save=True)
+    grads = conv.gated_ffn_backward(dy.cuda(), *args, saved)
+    want = ref.gated64(*wide(x, wg, wu, wd), None, "silu", 0, 0, "f32", dy.double())
+    for name, got in zip(("y", "dx", "dw_gate", "dw_up", "dw_down"), (y,) + grads):
+        ref.check(got, want[name], name)
+
+
+@pytest.mark.parametrize("low", [126, 132, 140, 149])
+def test_float32_subnormal_operands(low):
+    """Subnormal operands count to two units of their last place: 2^-148 of the other factors' absolute values."""
+    for rows in (5, 70):
+        tiny_operands(low, rows, lambda a, b: 2.0 ** -148 * (a.abs().sum(1)[:, None] + b.abs().sum(1)))
+
+
+@pytest.mark.parametrize("terms", [1, 2])
+def test_float32_products_near_the_top_of_the_range(terms):
+    """Products up to a half of the range's end (one term) and sums that stay below it (two): nothing of the parts'
+    products overflows where the sum does not.  Values at the very end, which round up to infinity as bfloat16."""
+    g = torch.Generator().manual_seed(terms)
+
+    def signed(rows, scale):
+        v = 1 + torch.rand(rows, terms, generator=g, dtype=torch.float64)
+        v[: rows // 2] = 1 + 2.0 ** -8 * torch.randint(1, 4, (rows // 2, terms), generator=g)  # the largest remainders
+        return (v * scale * (2 * torch.randint(0, 2, (rows, terms), generator=g) - 1)).float()
+    x, w = signed(60, 2.0 ** 63), signed(50, 2.0 ** (63 - terms))
+    want = ref.linear64(*wide(x, w, None, None), "identity", 0, 0, False, "f32")["y"]
+    ref.check(conv.linear(*cuda(x, w)), want)
+    top = torch.finfo(torch.float32).max
+    x = (top * (1 - 2.0 ** -torch.arange(1, 25, dtype=torch.float64))).float().repeat(3)[:, None].repeat(1, terms)
+    x[1::2] *= -1
+    w = rand(30, terms, dtype="f32", seed=7).clamp(-1, 1) / terms
+    ref.check(conv.linear(*cuda(x, w)), ref.linear64(*wide(x, w, None, None), "identity", 0, 0, False, "f32")["y"])
