@@ -212,8 +212,9 @@ __global__ void __launch_bounds__(256) dense_reduce(const DenseGemm g) {
 
 // The three planes of 4 values: v = p0 + 2^-kPlaneScale1 p1 + 2^-kPlaneScale2 p2, exactly, for every float32 down to the
 // smallest subnormal: unscaled, p1 and p2 of values below 2^-110 would end where bfloat16's range does (2^-133).  |p1| and
-// |p2| stay below |v| / 2.  An infinity or a NaN is its own first plane; a value that would round up to infinity is cut
-// instead.
+// |p2| stay below |v| / 2 (of a value below 2^-134, below 2^-126).  An infinity or a NaN is its own first plane; a value that
+// would round up to infinity is cut instead, and one that would round to zero becomes the smallest p0 (an infinity times it is
+// one, not NaN).
 __device__ __forceinline__ void put_planes(const float (&v)[4], __nv_bfloat16* out, long long plane) {
   constexpr float kUp1 = 1u << kPlaneScale1, kUp2 = 1u << (kPlaneScale2 - kPlaneScale1);
   uint16_t h[3][4];
@@ -222,6 +223,8 @@ __device__ __forceinline__ void put_planes(const float (&v)[4], __nv_bfloat16* o
     __nv_bfloat16 p0 = __float2bfloat16_rn(v[j]);
     const bool finite = fabsf(v[j]) <= 3.402823466e38f;
     if (finite && __hisinf(p0)) p0 = __float2bfloat16_rz(v[j]);
+    if (__bfloat162float(p0) == 0.0f && v[j] != 0.0f)
+      p0 = __ushort_as_bfloat16(static_cast<uint16_t>((__float_as_uint(v[j]) >> 16) & 0x8000u | 1u));
     const float r1 = finite ? (v[j] - __bfloat162float(p0)) * kUp1 : 0.0f;
     const __nv_bfloat16 p1 = __float2bfloat16_rn(r1);
     const __nv_bfloat16 p2 = __float2bfloat16_rn((r1 - __bfloat162float(p1)) * kUp2);

@@ -14,16 +14,19 @@
 //
 // The tensor cores cut their float32 accumulator instead of rounding it (the
 // sum of 1024 positive terms came out 2.2e-6 low, 64 terms 8e-8), so no
-// accumulator lives long: each 64 terms start a new one, the five small
-// products go first, while the accumulator is some 2^-8 of its final size, and
-// the epilogue warps add the finished 64-term sums up in registers, rounding to
-// nearest.  That work overlaps the next stage's MMAs (two accumulators).
+// accumulator lives long: each 64 terms start a new one, and the epilogue warps
+// add the finished 64-term sums up in registers, rounding to nearest.  That work
+// overlaps the next stage's MMAs (two pairs of accumulators).  The five small
+// products have an accumulator of their own: an infinity's remainders are zero,
+// and where a0 b0 is infinite or NaN it alone is the result.  (One accumulator
+// for all six took 2% less time, and gave NaN for infinity times anything; its
+// sums of positive terms were 4e-8 low on the average, these are not.)
 //
-// Measured: 4096 x 4096 x 4096 542 us, 253 TFLOP/s (4.2 times the CUDA cores'
-// rate; the six products alone are 1.5 PFLOP/s of bfloat16), relative error
-// 1.2e-7 where a float32 sum on the CUDA cores had 1.1e-6.  A stage's MMAs take
-// 1536 clocks, its copies 96 KB.  Small products wait for the launches and the
-// epilogue (1001 x 515 -> 1030 with gelu: 26 us, of which the MMAs 8).
+// Measured: 4096 x 4096 x 4096 551 us, 249 TFLOP/s (4.1 times the CUDA cores'
+// rate; the six products alone are 1.5 PFLOP/s of bfloat16); 1024 positive terms
+// at most 1.8e-7 off.  A stage's MMAs take 1536 clocks, its copies 96 KB.  Small
+// products wait for the launches and the epilogue (1001 x 515 -> 1030 with gelu:
+// 26 us, of which the MMAs 8).
 //
 // Otherwise as dense_tc.cuh, with tiles of 128 x 64 or 128 x 128 on one SM: a
 // stage is three planes of both operands, 96 KB, for 24 MMAs.
@@ -43,6 +46,8 @@ constexpr int kPlaneBytes = 128 * 128;          // one plane of a 128-row operan
 constexpr int kStage32 = 6 * kPlaneBytes;
 constexpr int kStages32 = 2;
 constexpr int kBuf32 = 4096;                    // a staging tile of 32 rows of 32 float32
+constexpr int kLarge32 = 128;                   // columns from an accumulator's small products to its large one
+constexpr int kAcc32 = 2 * kLarge32;
 constexpr int kStaging32 = kEpiWarps * 2 * kBuf32;
 constexpr int kSmem32 = kStages32 * kStage32 + kStaging32 + 2032;
 
@@ -74,7 +79,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
     asm volatile("fence.mbarrier_init.release.cluster;\n" ::: "memory");
     fence_proxy_async();
   }
-  if (warp == 1) alloc_tmem<1>(smem_u32(&tmem_slot), 256);
+  if (warp == 1) alloc_tmem<1>(smem_u32(&tmem_slot), 2 * kAcc32);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -158,15 +163,15 @@ __global__ void __launch_bounds__(kThreads32, 1)
           const uint64_t off = static_cast<uint64_t>(s) * (kStage32 >> 4);
 #pragma unroll
           for (int h = 0; h < kHalves; ++h) {
-            const uint32_t d = tmem + buf * 128 + h * cols;
+            const uint32_t d = tmem + buf * kAcc32 + h * cols;
             const uint64_t a = a0 + off, b = b0 + off + h * 3 * b_plane;
-            // the small products first, the large one last; each order's scale is taken off as the next one begins
+            // the small products, each order's scale taken off as the next one begins; beside them the large one
             mma_terms<-1, kAStep, kBStep>(d, a, b + 2 * b_plane, idesc);
             mma_terms<0, kAStep, kBStep>(d, a + 2 * a_plane, b, idesc);
             mma_terms<kPlaneScale2 - 2 * kPlaneScale1, kAStep, kBStep>(d, a + a_plane, b + b_plane, idesc);
             mma_terms<kPlaneScale1, kAStep, kBStep>(d, a, b + b_plane, idesc);
             mma_terms<0, kAStep, kBStep>(d, a + a_plane, b, idesc);
-            mma_terms<kPlaneScale1, kAStep, kBStep>(d, a, b, idesc);
+            mma_terms<-1, kAStep, kBStep>(d + kLarge32, a, b, idesc);
           }
           commit<1>(empty(s));
           commit<1>(acc_full(buf));
@@ -247,15 +252,19 @@ __global__ void __launch_bounds__(kThreads32, 1)
         }
         __syncwarp();
         tc_fence_after();
-        const uint32_t at = tmem + buf * 128 + (static_cast<uint32_t>(quarter * 32) << 16);
+        const uint32_t at = tmem + buf * kAcc32 + (static_cast<uint32_t>(quarter * 32) << 16);
 #pragma unroll
         for (int c = 0; c < 4; ++c)
           if (32 * c < nt) {
-            float v[32];
-            tmem_ld32(at + 32 * c, v);
+            float small[32], v[32];
+            tmem_ld32(at + 32 * c, small);
+            tmem_ld32(at + kLarge32 + 32 * c, v);
+            tmem_arrived(small);
             tmem_arrived(v);
+            // (an infinite or NaN large product is the sum: infinity times a remainder of zero would be NaN)
 #pragma unroll
-            for (int i = 0; i < 32; ++i) acc[c][i] += v[i];
+            for (int i = 0; i < 32; ++i)
+              acc[c][i] += fabsf(v[i]) <= 3.402823466e38f ? fmaf(small[i], 1.0f / (1u << kPlaneScale1), v[i]) : v[i];
           }
         tc_fence_before();
         __syncwarp();
@@ -330,7 +339,7 @@ __global__ void __launch_bounds__(kThreads32, 1)
   __syncthreads();
   if (warp == 1) {
     tc_fence_after();
-    free_tmem<1>(tmem, 256);
+    free_tmem<1>(tmem, 2 * kAcc32);
   }
 }
 

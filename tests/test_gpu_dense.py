@@ -685,3 +685,51 @@ def test_float32_products_near_the_top_of_the_range(terms):
     x[1::2] *= -1
     w = rand(30, terms, dtype="f32", seed=7).clamp(-1, 1) / terms
     ref.check(conv.linear(*cuda(x, w)), ref.linear64(*wide(x, w, None, None), "identity", 0, 0, False, "f32")["y"])
+
+
+def same_specials(got, want, size, terms, what):
+    """NaN and infinities where float64, rounded to float32, has them; elsewhere within the bound of a float32 sum of
+    `terms` terms, whose absolute values' sum is `size` (within 1% of the range's end, it may be infinite)."""
+    want = want.float().double()
+    got, finite = got.cpu().double(), want.isfinite() & (size < 0.99 * torch.finfo(torch.float32).max)
+    assert torch.equal(got.isnan(), want.isnan()), what
+    assert torch.equal(got[want.isinf()], want[want.isinf()]), what
+    bound = (terms + 3) * 2.0 ** -23 * size + 2.0 ** -149
+    assert finite.any() and ((got - want).abs() <= bound)[finite].all(), what
+
+
+@pytest.mark.parametrize("rows", [5, 12, 70, 200])
+@pytest.mark.parametrize("k", [64, 200, 77])
+def test_float32_infinities_are_those_of_the_formula(rows, k):
+    """An infinity among the operands times anything but zero is one, whatever the kernel: 12 rows of 77 and 70 rows go to
+    the tensor cores.  Factors of every size down to the smallest subnormal, and zeros, which make NaN."""
+    inf = float("inf")
+    x, w = rand(rows, k, dtype="f32", seed=1), rand(90, k, dtype="f32", seed=2)
+    w[3, 5], w[4, 5], w[5, 5], w[6, 5], w[7, 5] = 2.0 ** -149, -(2.0 ** -140), 0.0, 1e-30, -3e38
+    w[8, 5] = w[8, 60] = 1.0
+    x[1, 5], x[2, 5], x[3, 60] = inf, -inf, inf
+    x[4, 5], x[4, 60] = inf, -inf
+    w[9, 7], w[10, 7], w[11, 7] = inf, -inf, float("nan")
+    x[:, 7] = x[:, 7].abs() + 0.5
+    dy = rand(rows, 90, dtype="f32", seed=3)
+    dy[0, 9], dy[1, 30], dy[2, 40] = 0.0, -inf, inf
+    X, W, DY = cuda(x, w, dy)
+    x, w, dy = wide(x, w, dy)
+    finite = lambda t: torch.nan_to_num(t, 0.0, 0.0, 0.0).abs()  # noqa: E731
+    z, size = x @ w.T, finite(x) @ finite(w).T
+    same_specials(conv.linear(X, W), z, size, k, "y")
+    same_specials(conv.linear(X, W, act="relu"), torch.where(z < 0, torch.zeros_like(z), z), size, k, "relu")
+    dx, dw, _, _ = conv.linear_backward(DY, X, W)
+    same_specials(dw, dy.T @ x, finite(dy).T @ finite(x), rows, "dw")
+    w[9:12, 7], x[1:5, 5], x[3:5, 60] = 1.0, 1.0, 1.0
+    dx = conv.linear_backward(DY, x.float().cuda(), w.float().cuda(), need_dw=False)[0]
+    same_specials(dx, dy @ w, finite(dy) @ finite(w), 90, "dx")
+    # the gated block: an infinite g or u, then an infinite row of h
+    wg, wu, wd = rand(80, k, dtype="f32", seed=4), rand(80, k, dtype="f32", seed=5), rand(50, 80, dtype="f32", seed=6)
+    x[1, 5], x[2, 5] = inf, -inf
+    got = conv.gated_ffn(x.float().cuda(), *cuda(wg, wu, wd), act="leaky_relu", alpha=0.5)
+    wg, wu, wd = wide(wg, wu, wd)
+    g, u = x @ wg.T, x @ wu.T
+    a = torch.where(g >= 0, g, 0.5 * g)
+    size = ((finite(x) @ wg.abs().T) * (finite(x) @ wu.abs().T)) @ wd.abs().T
+    same_specials(got, (a * u) @ wd.T, size, 2 * k + 80, "gated")
