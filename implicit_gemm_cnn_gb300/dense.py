@@ -227,7 +227,7 @@ def _rows(t, width, what):
 
 def _rows_dense(t, width, what):
     """_rows, quicker for the dense tensors that most calls have."""
-    if t.is_contiguous() and t.dim() and t.shape[-1] == width:
+    if width and t.is_contiguous() and t.dim() and t.shape[-1] == width:  # (width 0: the C function refuses it)
         return t.numel() // width, 0
     return _rows(t, width, what)
 

@@ -308,3 +308,21 @@ print("planned")
 """ % ROOT
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0 and r.stdout.strip() == "planned", (r.returncode, r.stderr[-500:])
+
+
+def test_a_sum_of_no_terms_is_refused(monkeypatch):
+    """c_in, hidden or c_out of 0: the library's own status, at whatever function meets it first."""
+    def on(*shape):
+        return torch.zeros(*shape).as_subclass(_OnDevice)
+    # what runs on a device does not: the problem is refused before
+    monkeypatch.setattr(dense, "_run", lambda call, index, stream, *args: call(0, *args))
+    monkeypatch.setattr(dense, "_dense_out", lambda *a: None)
+    dense._torch()
+    assert dense._rows_dense(torch.zeros(4, 0), 0, "x")[0] == 4 and dense._rows_dense(torch.zeros(2, 3, 0), 0, "x")[0] == 6
+    for call in (lambda: conv.linear(on(4, 0), on(6, 0)), lambda: conv.linear(on(2, 3, 0), on(6, 0)),
+                 lambda: conv.linear(on(4, 8), on(0, 8)), lambda: conv.linear_backward(on(4, 6), on(4, 0), on(6, 0)),
+                 lambda: conv.gated_ffn(on(4, 0), on(5, 0), on(5, 0), on(6, 5)),
+                 lambda: conv.gated_ffn(on(4, 8), on(0, 8), on(0, 8), on(6, 0)),
+                 lambda: conv.gated_ffn_backward(on(4, 6), on(4, 0), on(5, 0), on(5, 0), on(6, 5), on(0))):
+        with pytest.raises(conv.ConvError, match="SHAPE"):
+            call()
