@@ -204,11 +204,13 @@ def _rows(t, width, what):
     n = len(shape)
     if n == 0 or shape[-1] != width:
         raise ValueError(f"{what} must be [..., {width}], not {tuple(shape)}")
-    if width > 1 and strides[-1] != 1:
+    if width > 1 and strides[-1] != 1 and t.numel():
         raise ValueError(f"{what}: the elements of a row must be adjacent")
     if n == 2 and strides[0] >= width:
         rows, stride = shape[0], strides[0]
         return rows, stride if rows > 1 else 0
+    if 0 in shape[:-1]:
+        return 0, 0  # (the strides of an empty tensor say nothing)
     rows, stride = 1, None
     for i in range(n - 2, -1, -1):
         if shape[i] == 1:
@@ -218,8 +220,6 @@ def _rows(t, width, what):
         elif strides[i] != stride * rows:
             raise ValueError(f"{what}: rows must be evenly spaced")
         rows *= shape[i]
-    if rows == 0:
-        return 0, 0
     if rows > 1 and stride < width:
         raise ValueError(f"{what}: rows must not overlap")
     return rows, stride if rows > 1 else 0

@@ -326,3 +326,12 @@ def test_a_sum_of_no_terms_is_refused(monkeypatch):
                  lambda: conv.gated_ffn_backward(on(4, 6), on(4, 0), on(5, 0), on(5, 0), on(6, 5), on(0))):
         with pytest.raises(conv.ConvError, match="SHAPE"):
             call()
+
+
+def test_empty_tensors_have_no_rows():
+    for empty in (torch.zeros(2, 0, 8), torch.zeros(0, 3, 8), torch.zeros(2, 3, 0, 5, 8), torch.zeros(0, 8),
+                  torch.zeros(4, 3, 20)[:, :0, 4:12], torch.zeros(0, 1, 8).expand(0, 3, 8),
+                  torch.zeros(8, 0).t(), torch.zeros(2, 8, 0).transpose(1, 2)):
+        assert dense._rows(empty, 8, "x") == (0, 0) and dense._rows_dense(empty, 8, "x") == (0, 0)
+    with pytest.raises(ValueError):
+        dense._rows(torch.zeros(2, 0, 7), 8, "x")

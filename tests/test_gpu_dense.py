@@ -733,3 +733,14 @@ def test_float32_infinities_are_those_of_the_formula(rows, k):
     a = torch.where(g >= 0, g, 0.5 * g)
     size = ((finite(x) @ wg.abs().T) * (finite(x) @ wu.abs().T)) @ wd.abs().T
     same_specials(got, (a * u) @ wd.T, size, 2 * k + 80, "gated")
+
+
+def test_no_rows_among_leading_dimensions():
+    x, w, dy = (torch.zeros(*s, device="cuda") for s in ((2, 0, 8), (6, 8), (2, 0, 6)))
+    assert conv.linear(x, w).shape == (2, 0, 6)
+    dx, dw, db, _ = conv.linear_backward(dy, x, w, need_dbias=True)
+    assert dx.shape == x.shape and dw.shape == w.shape and not dw.any() and not db.any()
+    g, d = torch.ones(12, 8, device="cuda"), torch.ones(6, 12, device="cuda")
+    y, saved = conv.gated_ffn(x, g, g.clone(), d, save=True)
+    grads = conv.gated_ffn_backward(dy, x, g, g.clone(), d, saved)
+    assert y.shape == dy.shape and grads[0].shape == x.shape and not any(t.any() for t in grads[1:])
