@@ -284,30 +284,31 @@ def _run(call, index, stream, *args):
         return call(handle, *args)
 
 
-# Problems and their scratch sizes by shape, so that a call of a shape seen before marshals nothing anew.
+# Problems and their scratch sizes by device (plans go by its SM count) and shape, so that a call of a shape seen before
+# marshals nothing anew.
 _linear_cache: dict = {}
 _gated_cache: dict = {}
 
 
-def _linear_problem(back, *key):
-    found = _linear_cache.get((back, key))
+def _linear_problem(index, back, *key):
+    found = _linear_cache.get((index, back, key))
     if found is None:
         p = LinearProblem(*key)
         need = (conv_linear_backward_scratch_bytes if back else conv_linear_scratch_bytes)(p)
         if len(_linear_cache) >= 4096:
             _linear_cache.clear()
-        found = _linear_cache[(back, key)] = (p, ctypes.byref(p), need)
+        found = _linear_cache[(index, back, key)] = (p, ctypes.byref(p), need)
     return found
 
 
-def _gated_problem(back, *key):
-    found = _gated_cache.get((back, key))
+def _gated_problem(index, back, *key):
+    found = _gated_cache.get((index, back, key))
     if found is None:
         p = GatedProblem(*key)
         need = (conv_gated_backward_scratch_bytes if back else conv_gated_scratch_bytes)(p)
         if len(_gated_cache) >= 4096:
             _gated_cache.clear()
-        found = _gated_cache[(back, key)] = (p, ctypes.byref(p), need, conv_gated_saved_bytes(p))
+        found = _gated_cache[(index, back, key)] = (p, ctypes.byref(p), need, conv_gated_saved_bytes(p))
     return found
 
 
@@ -390,8 +391,8 @@ def linear(x, w, bias=None, residual=None, *, act="identity", alpha=0.0, beta=0.
             out = torch.empty_like(residual) if rp is not None and ldr == 0 and residual.is_contiguous() else \
                 torch.empty(y_shape, dtype=x.dtype, device=x.device)
         pre = torch.empty(y_shape, dtype=torch.float32, device=x.device) if save and act != "identity" else None
-        _, ref, need = _linear_problem(False, rows, c_in, c_out, ldx, ldw, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, dt,
-                                       0 if bp is None else 1, 0 if rp is None else 1, flags)
+        _, ref, need = _linear_problem(index, False, rows, c_in, c_out, ldx, ldw, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha,
+                                       beta, dt, 0 if bp is None else 1, 0 if rp is None else 1, flags)
         args = ref, xp, wp, bp, rp, out.data_ptr(), None if pre is None else pre.data_ptr()
         if need:
             with _turn:
@@ -440,8 +441,8 @@ def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, 
         dw = _dense_out(dw, w.shape, x, "dw") if need_dw else None
         dbias = torch.empty(c_out, dtype=x.dtype, device=x.device) if need_dbias else None
         dres = torch.empty(dy.shape, dtype=x.dtype, device=x.device) if need_dresidual else None
-        _, ref, need = _linear_problem(True, rows, c_in, c_out, ldx, ldw, 0, ldy, LINEAR_ACTIVATIONS[act], alpha, beta, dt,
-                                       0, 0, flags)
+        _, ref, need = _linear_problem(index, True, rows, c_in, c_out, ldx, ldw, 0, ldy, LINEAR_ACTIVATIONS[act], alpha,
+                                       beta, dt, 0, 0, flags)
         with _turn:
             buf, at, n = _scratch(need, scratch, index, handle)
             status = _load().conv_linear_backward(ref, xp, wp, _ptr(pre), dyp, _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dres), at,
@@ -489,8 +490,8 @@ def gated_ffn(x, w_gate, w_up, w_down, residual=None, *, act="silu", alpha=0.0, 
         if out is None:
             out = torch.empty_like(residual) if residual is not None and residual.is_contiguous() else \
                 torch.empty(y_shape, dtype=x.dtype, device=x.device)
-        _, ref, need, kept = _gated_problem(False, rows, c_in, hidden, c_out, ldx, ldr, ldy, LINEAR_ACTIVATIONS[act], alpha,
-                                            beta, dt, 0 if residual is None else 1, flags)
+        _, ref, need, kept = _gated_problem(index, False, rows, c_in, hidden, c_out, ldx, ldr, ldy, LINEAR_ACTIVATIONS[act],
+                                            alpha, beta, dt, 0 if residual is None else 1, flags)
         saved = torch.empty(kept, dtype=torch.uint8, device=x.device) if save else None
         with _turn:
             buf, at, n = _scratch(need, scratch, index, handle)
@@ -521,7 +522,7 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=
         flags |= FLAG_LINEAR_UNALIGNED
 
     def call(handle):
-        _, ref, need, kept = _gated_problem(True, rows, c_in, hidden, c_out, ldx, 0, ldy, LINEAR_ACTIVATIONS[act], alpha,
+        _, ref, need, kept = _gated_problem(index, True, rows, c_in, hidden, c_out, ldx, 0, ldy, LINEAR_ACTIVATIONS[act], alpha,
                                             beta, dt, 0, flags)
         if saved.dtype != torch.uint8 or saved.get_device() != index or saved.numel() != kept:
             raise ValueError("saved must be what gated_ffn(..., save=True) returned for this problem")

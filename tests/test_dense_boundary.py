@@ -335,3 +335,42 @@ def test_empty_tensors_have_no_rows():
         assert dense._rows(empty, 8, "x") == (0, 0) and dense._rows_dense(empty, 8, "x") == (0, 0)
     with pytest.raises(ValueError):
         dense._rows(torch.zeros(2, 0, 7), 8, "x")
+
+
+def test_scratch_sizes_are_kept_per_device(monkeypatch):
+    """Plans go by the SM count: what one device's query said is not taken for another's."""
+    now = []
+
+    class On1(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    def run(call, index, stream, *args):
+        now.append(index)
+        return call(0, *args)
+
+    class Library:
+        def __getattr__(self, name):
+            return lambda *a: 0
+
+    asked = []
+    monkeypatch.setattr(dense, "_run", run)
+    monkeypatch.setattr(dense, "_load", lambda: Library())
+    monkeypatch.setattr(dense, "_dense_out", lambda *a: None)
+    monkeypatch.setattr(dense, "_scratch", lambda need, given, index, handle: (asked.append(need), None, 0))
+    monkeypatch.setattr(dense, "conv_gated_saved_bytes", lambda p: 0)
+    for name in ("linear", "linear_backward", "gated", "gated_backward"):
+        monkeypatch.setattr(dense, f"conv_{name}_scratch_bytes", lambda p: 1000 + now[-1])
+    monkeypatch.setattr(dense, "_linear_cache", {})
+    monkeypatch.setattr(dense, "_gated_cache", {})
+    dense._torch()
+    for _ in range(2):
+        for cls, want in ((_OnDevice, 1000), (On1, 1001)):
+            x, w, dy, g, d = (torch.zeros(*s).as_subclass(cls) for s in ((4, 8), (6, 8), (4, 6), (12, 8), (6, 12)))
+            saved = torch.zeros(0, dtype=torch.uint8).as_subclass(cls)
+            del asked[:]
+            conv.linear(x, w)
+            conv.linear_backward(dy, x, w)
+            conv.gated_ffn(x, g, g, d)
+            conv.gated_ffn_backward(dy, x, g, g, d, saved)
+            assert asked == [want] * 4
