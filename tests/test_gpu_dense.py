@@ -744,3 +744,41 @@ def test_no_rows_among_leading_dimensions():
     y, saved = conv.gated_ffn(x, g, g.clone(), d, save=True)
     grads = conv.gated_ffn_backward(dy, x, g, g.clone(), d, saved)
     assert y.shape == dy.shape and grads[0].shape == x.shape and not any(t.any() for t in grads[1:])
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_dresidual_of_rows_far_apart(dtype):
+    """dy's rows more than 2^31 bytes apart, every output: what is dy itself comes out bit for bit."""
+    size = 4 if dtype == "f32" else 2
+    stride = (1 << 31) // size + 8
+    flat = torch.zeros(stride + 24, dtype=ref.TORCH[dtype], device="cuda")
+    dy = torch.as_strided(flat, (2, 24), (stride, 1))
+    dy.copy_(rand(2, 24, dtype=dtype, seed=1))
+    x, w = rand(2, 40, dtype=dtype, seed=2).cuda(), rand(24, 40, dtype=dtype, seed=3, scale=0.2).cuda()
+    for last, act in ((False, "identity"), (True, "relu"), (False, "relu")):
+        r = rand(2, 24, dtype=dtype, seed=4).cuda()
+        _, pre = conv.linear(x, w, None, r, act=act, residual_last=last, save=True)
+        grads = conv.linear_backward(dy, x, w, pre, act=act, residual_last=last, need_dbias=True, need_dresidual=True)
+        host = wide(*(t.cpu() for t in (dy, x, w, r)))
+        want = ref.linear64(host[1], host[2], None, host[3], act, 0, 0, last, dtype)
+        back = ref.linear_backward64(host[0], host[1], host[2], *want["z"], act, 0, 0, last, dtype)
+        for name, got in zip(("dx", "dw", "dbias", "dresidual"), grads):
+            ref.check(got, back[name], (act, last, name))
+        if last or act == "identity":
+            assert torch.equal(grads[3], dy)
+    del flat, dy
+
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+def test_dresidual_of_the_identity_is_dy(dtype):
+    """Every value of 16 bits but NaN, and strided rows of odd widths."""
+    if dtype != "f32":
+        values = torch.arange(-32768, 32768, dtype=torch.int32).to(torch.int16).view(ref.TORCH[dtype])
+        values = values[~values.isnan()]
+    else:
+        values = rand(70000, dtype="f32", seed=5) * 2.0 ** torch.randint(-149, 127, (70000,), generator=torch.Generator().manual_seed(1))
+    for rows, cols, pad in ((100, 300, 0), (77, 301, 5), (5, 1000, 24), (1, 33, 0)):
+        dy = values[:rows * (cols + pad)].view(rows, cols + pad)[:, :cols].cuda()
+        x, w = torch.zeros(rows, 8, dtype=dy.dtype, device="cuda"), torch.zeros(cols, 8, dtype=dy.dtype, device="cuda")
+        got = conv.linear_backward(dy, x, w, need_dx=False, need_dw=False, need_dresidual=True)[3]
+        assert torch.equal(got, dy) and torch.equal(got.signbit(), dy.signbit())
