@@ -7,6 +7,7 @@ only marshal arguments; ``linear``, ``linear_backward``, ``gated_ffn``,
 outputs and scratch with torch."""
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import threading
 from array import array
@@ -312,12 +313,23 @@ def _gated_problem(index, back, *key):
     return found
 
 
-# Scratch of up to _KEPT bytes is kept per stream: the calls of a stream run one after another (host threads that share a
-# stream take turns at a call: _turn), and an allocation from torch's pool takes longer than a small call's own work.  A
-# larger one, and one under graph capture (whose memory belongs to the graph), is the call's own.
+# Scratch of up to _KEPT bytes is kept per stream: the calls of a stream run one after another, and an allocation from
+# torch's pool takes longer than a small call's own work.  A larger one, and one under graph capture (whose memory belongs to
+# the graph), is the call's own.
 _KEPT = 32 << 20
 _kept: dict = {}
-_turn = threading.RLock()
+_turns: dict = {}
+_no_turn = contextlib.nullcontext()
+
+
+def _turn(need, given, index, handle):
+    """Held from the choice of the scratch to the call's last launch: host threads that share a stream take turns at its
+    kept scratch.  Streams have a turn each (a launch waits where a stream's queue is full), and a call whose scratch is
+    its own, or the caller's, waits for nobody."""
+    if need == 0 or given is not None or need > _KEPT:
+        return _no_turn
+    turn = _turns.get((index, handle))
+    return turn if turn is not None else _turns.setdefault((index, handle), threading.RLock())
 
 
 def _scratch(need, given, index, handle):
@@ -395,7 +407,7 @@ def linear(x, w, bias=None, residual=None, *, act="identity", alpha=0.0, beta=0.
                                        beta, dt, 0 if bp is None else 1, 0 if rp is None else 1, flags)
         args = ref, xp, wp, bp, rp, out.data_ptr(), None if pre is None else pre.data_ptr()
         if need:
-            with _turn:
+            with _turn(need, scratch, index, handle):
                 _, at, n = _scratch(need, scratch, index, handle)
                 status = _load().conv_linear_forward(*args, at, n, handle or None)
         else:
@@ -443,7 +455,7 @@ def linear_backward(dy, x, w, pre=None, *, act="identity", alpha=0.0, beta=0.0, 
         dres = torch.empty(dy.shape, dtype=x.dtype, device=x.device) if need_dresidual else None
         _, ref, need = _linear_problem(index, True, rows, c_in, c_out, ldx, ldw, 0, ldy, LINEAR_ACTIVATIONS[act], alpha,
                                        beta, dt, 0, 0, flags)
-        with _turn:
+        with _turn(need, scratch, index, handle):
             buf, at, n = _scratch(need, scratch, index, handle)
             status = _load().conv_linear_backward(ref, xp, wp, _ptr(pre), dyp, _ptr(dx), _ptr(dw), _ptr(dbias), _ptr(dres), at,
                                                   n, handle or None)
@@ -493,7 +505,7 @@ def gated_ffn(x, w_gate, w_up, w_down, residual=None, *, act="silu", alpha=0.0, 
         _, ref, need, kept = _gated_problem(index, False, rows, c_in, hidden, c_out, ldx, ldr, ldy, LINEAR_ACTIVATIONS[act],
                                             alpha, beta, dt, 0 if residual is None else 1, flags)
         saved = torch.empty(kept, dtype=torch.uint8, device=x.device) if save else None
-        with _turn:
+        with _turn(need, scratch, index, handle):
             buf, at, n = _scratch(need, scratch, index, handle)
             status = _load().conv_gated_forward(ref, *ptrs, _ptr(residual), out.data_ptr(), _ptr(saved), at, n,
                                                 handle or None)
@@ -529,7 +541,7 @@ def gated_ffn_backward(dy, x, w_gate, w_up, w_down, saved, *, act="silu", alpha=
         dx = torch.empty(x.shape, dtype=x.dtype, device=x.device) if need_dx else None
         dws = [torch.empty(w.shape, dtype=x.dtype, device=x.device) if need_dw else None
                for w in (w_gate, w_up, w_down)]
-        with _turn:
+        with _turn(need, scratch, index, handle):
             buf, at, n = _scratch(need, scratch, index, handle)
             status = _load().conv_gated_backward(ref, *ptrs, saved.data_ptr(), dy.data_ptr(), _ptr(dx),
                                                  *[_ptr(t) for t in dws], at, n, handle or None)
@@ -578,7 +590,7 @@ def clip_grad_norm(grads, max_norm, *, eps=1e-6, out=None, scratch=None, stream=
         at_sizes = sizes.buffer_info()[0]
         need = ctypes.c_size_t()
         _check(lib.conv_clip_scratch_bytes(n, at_sizes, ctypes.byref(need)), "conv_clip_scratch_bytes")
-        with _turn:
+        with _turn(need.value, scratch, index, handle):
             buf, at, size = _scratch(need.value, scratch, index, handle)
             status = lib.conv_clip_grads(n, ins.buffer_info()[0], to.buffer_info()[0], at_sizes, types.buffer_info()[0],
                                          max_norm, eps, norm.data_ptr(), at, size, handle or None)

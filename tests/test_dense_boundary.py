@@ -5,6 +5,7 @@ import os
 import re
 import subprocess
 import sys
+import threading
 
 import pytest
 import torch
@@ -374,3 +375,70 @@ def test_scratch_sizes_are_kept_per_device(monkeypatch):
             conv.gated_ffn(x, g, g, d)
             conv.gated_ffn_backward(dy, x, g, g, d, saved)
             assert asked == [want] * 4
+
+
+@pytest.mark.parametrize("op", ["linear", "linear_backward", "gated", "gated_backward"])
+def test_only_calls_that_share_a_scratch_take_turns(monkeypatch, op):
+    """One call stands in its launch (a full queue).  Calls on another stream or device, and calls on its own stream whose
+    scratch is not the kept one, go on; a call on its stream that shares the scratch waits."""
+    inside, go = threading.Event(), threading.Event()
+
+    class On1(torch.Tensor):
+        def get_device(self):
+            return 1
+
+    class Library:
+        def __getattr__(self, name):
+            def call(*args):
+                if threading.current_thread().name == "first" and name in (f"conv_{op}", f"conv_{op}_forward"):
+                    inside.set()
+                    assert go.wait(30)
+                return 0
+            return call
+
+    size = [4096]
+    monkeypatch.setattr(dense, "_load", lambda: Library())
+    monkeypatch.setattr(dense, "_run", lambda call, index, stream, *args: call(stream, *args))
+    monkeypatch.setattr(dense, "_scratch", lambda need, given, index, handle: (given, 256, need))
+    monkeypatch.setattr(dense, "_dense_out", lambda *a: None)
+    for name in ("linear", "linear_backward", "gated", "gated_backward"):
+        monkeypatch.setattr(dense, f"conv_{name}_scratch_bytes", lambda p: size[0])
+    monkeypatch.setattr(dense, "conv_gated_saved_bytes", lambda p: 0)
+    empty = torch.empty
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **kw: empty(*a, **kw))
+    dense._torch()
+
+    def run(stream, cls=_OnDevice, need=4096, **kw):
+        size[0] = need
+        dense._linear_cache.clear()
+        dense._gated_cache.clear()
+        x, w, dy, g, d = (torch.zeros(*s).as_subclass(cls) for s in ((4, 8), (6, 8), (4, 6), (12, 8), (6, 12)))
+        saved = torch.zeros(0, dtype=torch.uint8).as_subclass(cls)
+        {"linear": lambda: conv.linear(x, w, stream=stream, **kw),
+         "linear_backward": lambda: conv.linear_backward(dy, x, w, stream=stream, **kw),
+         "gated": lambda: conv.gated_ffn(x, g, g, d, stream=stream, **kw),
+         "gated_backward": lambda: conv.gated_ffn_backward(dy, x, g, g, d, saved, stream=stream, **kw)}[op]()
+
+    def start(name, *args, **kw):
+        t = threading.Thread(target=run, name=name, args=args, kwargs=kw, daemon=True)
+        t.start()
+        return t
+    try:
+        first = start("first", 7)
+        assert inside.wait(30)
+        for name, args, kw in (("other stream", (8,), {}), ("other device", (7, On1), {}), ("large", (7,), dict(need=dense._KEPT + 1)),
+                               ("own", (7,), dict(scratch=empty(64, dtype=torch.uint8))), ("none", (7,), dict(need=0))):
+            t = start(name, *args, **kw)
+            t.join(10)
+            assert not t.is_alive(), name
+        second = start("second", 7)
+        second.join(0.2)
+        assert second.is_alive() and first.is_alive()
+        go.set()
+        for t in (first, second):
+            t.join(10)
+            assert not t.is_alive()
+    finally:
+        go.set()
+        dense._linear_cache.clear()
+        dense._gated_cache.clear()
