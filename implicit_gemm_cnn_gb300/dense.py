@@ -256,7 +256,12 @@ class _On:
             self.ctx = torch.cuda.device(index)
             self.handle = torch.cuda.current_stream(index).cuda_stream
         else:
-            s = stream if hasattr(stream, "cuda_stream") else torch.cuda.ExternalStream(int(stream), device=index)
+            if hasattr(stream, "cuda_stream"):
+                s = stream
+            elif int(stream) == 0:  # the legacy default stream (torch takes the address 0 for a stream of its pool)
+                s = torch.cuda.default_stream(index)
+            else:
+                s = torch.cuda.ExternalStream(int(stream), device=index)
             self.ctx = torch.cuda.stream(s)
             self.handle = s.cuda_stream
 

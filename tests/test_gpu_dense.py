@@ -782,3 +782,22 @@ def test_dresidual_of_the_identity_is_dy(dtype):
         x, w = torch.zeros(rows, 8, dtype=dy.dtype, device="cuda"), torch.zeros(cols, 8, dtype=dy.dtype, device="cuda")
         got = conv.linear_backward(dy, x, w, need_dx=False, need_dw=False, need_dresidual=True)[3]
         assert torch.equal(got, dy) and torch.equal(got.signbit(), dy.signbit())
+
+
+def test_the_default_stream_by_its_number():
+    """stream=0 is the legacy default stream, as a handle and as a stream object: work before and after it keeps its order."""
+    from implicit_gemm_cnn_gb300 import dense
+    big = torch.randn(8192, 8192, device="cuda")
+    values, w = rand(64, 256, dtype="bf16", seed=1).cuda(), rand(40, 256, dtype="bf16", seed=2, scale=0.1).cuda()
+    want = conv.linear(values, w)
+    for stream in (0, torch.cuda.default_stream(), torch.cuda.default_stream().cuda_stream):
+        assert dense._On(0, stream).handle == 0
+    x = torch.zeros_like(values)
+    torch.cuda.synchronize()
+    for _ in range(10):
+        big = big @ big * 1e-3  # some milliseconds before x is written
+    x.copy_(values)
+    y = conv.linear(x, w, stream=0)
+    norm = conv.clip_grad_norm([x], 0.0, stream=0)  # x is read, then made zero
+    torch.cuda.synchronize()
+    assert torch.equal(y, want) and norm.item() > 0 and not x.any()
