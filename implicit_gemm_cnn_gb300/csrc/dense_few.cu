@@ -181,8 +181,7 @@ __global__ void __launch_bounds__(kThreads, 2) few_mma(const DenseGemm g, const 
 // float32: a warp multiplies pieces of 128 terms (four per lane) of the block's outputs with every row.  ROWS: rows
 // compiled for (at least g.M).  Outputs are taken OG at a time, so that their sums stay in registers.
 template <int ROWS, bool DUAL, bool VEC>
-__global__ void __launch_bounds__(kThreads) few_f32(const DenseGemm g, const int early) {
-  (void)early;
+__global__ void __launch_bounds__(kThreads) few_f32(const DenseGemm g) {
   constexpr int P = DUAL ? 2 : 1;
   constexpr int OG = (ROWS > 8 ? 4 : 8) / P;
   __shared__ float red[P * kWarps * kOuts * ROWS];
@@ -242,22 +241,19 @@ __global__ void __launch_bounds__(kThreads) few_f32(const DenseGemm g, const int
   finish<float, ROWS, DUAL>(g, red, n0);
 }
 
-template <typename K>
-cudaError_t start(K kern, const DenseGemm& g, bool follows, int blocks, cudaStream_t s) {
-  return launch_overlapped(kern, dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, s, g, follows ? 1 : 0);
-}
 int groups_of(const DenseGemm& g) { return static_cast<int>((static_cast<long long>(g.N) + kOuts - 1) / kOuts); }
 template <typename T, bool DUAL>
 cudaError_t go16(const DenseGemm& g, bool vec, bool follows, int sm, cudaStream_t s) {
   // two blocks per SM at most, each with as many groups of outputs as any other
   const int groups = groups_of(g), rounds = (groups + 2 * sm - 1) / (2 * sm), blocks = (groups + rounds - 1) / rounds;
-  if (g.M <= 8) return vec ? start(few_mma<T, 1, DUAL, true>, g, follows, blocks, s) : start(few_mma<T, 1, DUAL, false>, g, follows, blocks, s);
-  return vec ? start(few_mma<T, 2, DUAL, true>, g, follows, blocks, s) : start(few_mma<T, 2, DUAL, false>, g, follows, blocks, s);
+  auto kern = g.M <= 8 ? (vec ? few_mma<T, 1, DUAL, true> : few_mma<T, 1, DUAL, false>)
+                       : (vec ? few_mma<T, 2, DUAL, true> : few_mma<T, 2, DUAL, false>);
+  return launch_overlapped(kern, dim3(static_cast<unsigned>(blocks)), kThreads, 0, 1, s, g, follows ? 1 : 0);
 }
 template <int ROWS, bool DUAL>
-cudaError_t go32(const DenseGemm& g, bool vec, bool follows, cudaStream_t s) {
-  return vec ? start(few_f32<ROWS, DUAL, true>, g, follows, groups_of(g), s)
-             : start(few_f32<ROWS, DUAL, false>, g, follows, groups_of(g), s);
+cudaError_t go32(const DenseGemm& g, bool vec, cudaStream_t s) {
+  return launch_overlapped(vec ? few_f32<ROWS, DUAL, true> : few_f32<ROWS, DUAL, false>,
+                           dim3(static_cast<unsigned>(groups_of(g))), kThreads, 0, 1, s, g);
 }
 
 }  // namespace
@@ -271,10 +267,10 @@ cudaError_t launch_dense_few(const DenseGemm& g, int dtype, bool follows, int sm
   if (dtype == CONV_F16) return g.dual ? go16<__half, true>(g, vec, follows, sm, s) : go16<__half, false>(g, vec, follows, sm, s);
   if (dtype == CONV_BF16)
     return g.dual ? go16<__nv_bfloat16, true>(g, vec, follows, sm, s) : go16<__nv_bfloat16, false>(g, vec, follows, sm, s);
-  if (g.M <= 1) return g.dual ? go32<1, true>(g, vec, follows, s) : go32<1, false>(g, vec, follows, s);
-  if (g.M <= 4) return g.dual ? go32<4, true>(g, vec, follows, s) : go32<4, false>(g, vec, follows, s);
-  if (g.M <= 8) return g.dual ? go32<8, true>(g, vec, follows, s) : go32<8, false>(g, vec, follows, s);
-  return g.dual ? go32<16, true>(g, vec, follows, s) : go32<16, false>(g, vec, follows, s);
+  if (g.M <= 1) return g.dual ? go32<1, true>(g, vec, s) : go32<1, false>(g, vec, s);
+  if (g.M <= 4) return g.dual ? go32<4, true>(g, vec, s) : go32<4, false>(g, vec, s);
+  if (g.M <= 8) return g.dual ? go32<8, true>(g, vec, s) : go32<8, false>(g, vec, s);
+  return g.dual ? go32<16, true>(g, vec, s) : go32<16, false>(g, vec, s);
 }
 
 }  // namespace conv

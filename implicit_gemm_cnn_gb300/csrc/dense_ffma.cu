@@ -1,6 +1,7 @@
-// dense_ffma.cu -- the dense products on the CUDA cores: float32 layers, and
-// 16-bit operands of an alignment that the tensor-core kernel's copies cannot
-// take.  Also the ordered sum of k ranges, and the elementwise helpers of the
+// dense_ffma.cu -- the dense products on the CUDA cores: 16-bit operands off
+// 16-byte boundaries where there is no scratch for their copies, and any problem
+// that asks for this kernel (CONV_LINEAR_FLAG_FORCE_FFMA).  Also the ordered sum
+// of its k ranges, the operands' copies, and the elementwise helpers of the
 // backward passes.
 //
 // A block computes a BM x BN tile of D = A B^T in register tiles of TM x TN per
@@ -13,8 +14,7 @@
 // the same positions, so g and u of one element meet in one thread.
 //
 // Measured: 1001 x 515 -> 1030 float32 51 us (20.7 TFLOP/s, 272 tiles of 64 x
-// 64 on 152 SMs); the tensor-core kernel takes 26, so that this one is left
-// with FORCE_FFMA and with unaligned 16-bit operands whose copies have no room.
+// 64 on 152 SMs), where the tensor-core kernel takes 26.
 #include <algorithm>
 
 #include "dense_internal.h"
@@ -238,8 +238,9 @@ __device__ __forceinline__ void put_planes(const float (&v)[4], __nv_bfloat16* o
         make_uint2(h[q][0] | (static_cast<uint32_t>(h[q][1]) << 16), h[q][2] | (static_cast<uint32_t>(h[q][3]) << 16));
 }
 
-// Operands' copies, bound by their bytes (30 MB of weights with odd rows 13 us).  A warp takes 256 columns of a row at a time: 16-bit rows as they are, or float32 rows as three planes (rows of the
-// planes are a multiple of 64 long, so whole groups of four are written).  Blocks walk over the jobs' pieces together.
+// Operands' copies, bound by their bytes (30 MB of weights with odd rows 13 us).  A warp takes 256 columns of a row at a
+// time: 16-bit rows as they are, or float32 rows as three planes (rows of the planes are a multiple of 64 long, so whole
+// groups of four are written).  Blocks walk over the jobs' pieces together.
 struct CopyJobs {
   CopyJob job[kCopyJobs];
   long long first[kCopyJobs + 1];
@@ -313,9 +314,10 @@ __global__ void __launch_bounds__(256) dense_copies(const __grid_constant__ Copy
   }
 }
 
-// dz and the column sums of a row block, bound by the bytes (dy, pre in; dz out: 8192 x 8192 bfloat16 102 us, 5.2 TB/s).  A warp takes 32 * V columns of every
-// eighth row of the block (V columns per lane: 16 bytes of 16-bit values, or of float32), two rows in flight; the
-// eight warps' partial sums are added in order.  VEC: every row of dy, pre and dz begins on a 16-byte boundary.
+// dz and the column sums of a row block, bound by the bytes (dy, pre in; dz out: 8192 x 8192 bfloat16 102 us, 5.2 TB/s).
+// A warp takes 32 * V columns of every eighth row of the block (V columns per lane: 16 bytes of 16-bit values, or of
+// float32), two rows in flight; the eight warps' partial sums are added in order.  VEC: every row of dy, pre and dz begins
+// on a 16-byte boundary.
 template <typename T, bool VEC, bool PLANES>
 __global__ void __launch_bounds__(256, 3) dense_dz(const T* dy, long long ld_dy, const float* pre, void* dz, long long ld_dz,
                                                    float* part, int rows_per_block, long long rows, long long cols,

@@ -59,20 +59,17 @@ uint32_t* error_word() {
   return at[dev];
 }
 
-// A row-major matrix (planes of them, if planes > 0) as a tensor map with boxes
-// of `box_bytes` (128 or 64) of a row x box_rows rows, swizzled over as many bytes, zeros outside.
+// A row-major matrix as a tensor map with boxes of 128 bytes of a row x box_rows rows, swizzled over as many bytes, zeros
+// outside.
 bool encode(CUtensorMap* map, CUtensorMapDataType type, const void* base, long long inner, long long rows, long long ld,
-            int planes, int box_rows, int box_bytes = 128) {
+            int box_rows) {
   const size_t es = type == CU_TENSOR_MAP_DATA_TYPE_FLOAT32 ? 4 : 2;
-  const cuuint64_t dims[3] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows),
-                              static_cast<cuuint64_t>(std::max(planes, 1))};
-  const cuuint64_t strides[2] = {static_cast<cuuint64_t>(ld) * es, static_cast<cuuint64_t>(ld) * es * rows};
-  const cuuint32_t box[3] = {static_cast<cuuint32_t>(box_bytes / es), static_cast<cuuint32_t>(box_rows), 1};
-  const cuuint32_t step[3] = {1, 1, 1};
-  return encoder()(map, type, planes > 0 ? 3 : 2, const_cast<void*>(base), dims, strides, box, step,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE,
-                   box_bytes == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+  const cuuint64_t dims[2] = {static_cast<cuuint64_t>(inner), static_cast<cuuint64_t>(rows)};
+  const cuuint64_t strides[1] = {static_cast<cuuint64_t>(ld) * es};
+  const cuuint32_t box[2] = {static_cast<cuuint32_t>(128 / es), static_cast<cuuint32_t>(box_rows)};
+  const cuuint32_t step[2] = {1, 1};
+  return encoder()(map, type, 2, const_cast<void*>(base), dims, strides, box, step, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                   CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 // An mn-major operand's matrix (rows of `inner` values, existing to a multiple of 64) as a map of 64-wide column blocks:
@@ -250,7 +247,7 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype,
     if (f32)
       return mn ? encode_planes(map, base, rows, g.K, ld, 64) : encode_planes(map, base, g.K, rows, ld, box_rows);
     if (blocks) return encode_blocks(map, type, base, rows, g.K, ld, box_blocks);
-    return mn ? encode(map, type, base, rows, g.K, ld, 0, 64) : encode(map, type, base, g.K, rows, ld, 0, box_rows);
+    return mn ? encode(map, type, base, rows, g.K, ld, 64) : encode(map, type, base, g.K, rows, ld, box_rows);
   };
   for (int i = 0; i < as; ++i) ok = ok && operand(&maps.a[i], g.a[i], g.a_mn, p.a_3d, g.M, g.lda, p.a_rows, 2);
   for (int i = 0; i < bs; ++i) ok = ok && operand(&maps.b[i], g.b[i], g.b_mn, p.b_3d, g.N, g.ldb, b_rows, b_rows / 64);
@@ -268,7 +265,7 @@ cudaError_t launch_dense_tc(const DenseTcPlan& t, const DenseGemm& g, int dtype,
   p.part = static_cast<float*>(part);
   if (f32) {
     auto out = [&](CUtensorMap* map, const void* base, long long cols, long long rows, long long ld) {
-      return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, cols, rows, ld, 0, 32);
+      return encode(map, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, base, cols, rows, ld, 32);
     };
     if (cut > 0) ok = ok && out(&maps.part, part, t.nt, static_cast<long long>(cut) * t.split * tile_rows, t.nt);
     if (p.align_y) {
