@@ -1,8 +1,8 @@
 // dense_api.cu -- the C ABI of the dense operators (linear.h): validation,
 // planning and dispatch.  Everything here runs on the host; a call only
 // enqueues.  A plan is a function of the problem and the SM count (and of
-// whether the operands' addresses are 16-byte aligned), so the order of every
-// sum is too.
+// whether the operands' addresses are 16-byte aligned; where one is not, of the
+// scratch given too), so the order of every sum is too.
 #include <math.h>
 #include <stdio.h>
 #include <string.h>
