@@ -13,13 +13,15 @@
  * 16-bit results are rounded once, to nearest even.  No kernel uses atomics:
  * results are bit-identical from run to run on one device.
  *
- * float32 operands (of more than 16 rows; of more than 8 where rows are no whole
- * 16-byte pieces) are multiplied as three bfloat16 parts each (all 24 bits of
- * their significands), with sums at least as exact as float32 ones; of a
- * subnormal operand two units of its last place (2^-148) may be lost.
+ * float32 products of more than 16 rows (of more than 8 where rows are no whole
+ * 16-byte pieces; all of a backward pass) multiply their operands as three
+ * bfloat16 parts each (all 24 bits of their significands), with sums at least as
+ * exact as float32 ones; of a subnormal operand two units of its last place
+ * (2^-148) may be lost.
  * Infinities and NaN come out as the formula gives them, whatever the kernel;
  * a sum of products whose absolute values come within 1% of the end of float32's
- * range may be infinite (the product of the first parts may pass the whole one by 2^-7).
+ * range may be infinite there (the product of the first parts may pass the whole
+ * one by 2^-7).
  *
  * Matrices are row-major.  A row stride counts elements from one row to the
  * next; 0 stands for dense rows (stride = width).  Strides of any size, and
