@@ -85,17 +85,16 @@ __global__ void __maxnreg__(registers(B, N)) norm_forward(const NormArgs a) {
     T* y = static_cast<T*>(a.y) + r * a.ldy + t * V;
     const T* w = static_cast<const T*>(a.w) + t * V;
     const T* b = static_cast<const T*>(a.b) + t * V;
-    // 16-bit results: the rounded mean is exact enough.  (Its rounding, 2^-24 of the mean, is 2^-16 of the last place of
-    // values of its size, and of y no more than that.)  float32 takes the two parts off one after the other.
-    constexpr bool TWO = sizeof(T) == 4;
-    const Same<V> centre(TWO ? -mean : -(mean + off)), rest(-off), scale(rstd);
+    // The mean's two parts are taken off one after the other: their rounded sum is off by 2^-24 of the mean, and a value's
+    // distance from the mean may be less than that (16384 halves of 1024 but for one of 1025: 2^-14).
+    const Same<V> centre(-mean), rest(-off), scale(rstd);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float v[V], f[V];
       if constexpr (N >= 4) keep_packed<B>(raw[i]);
       raw_to_f32<T, B>(raw[i], v);
       add_n(v, v, centre.v);
-      if constexpr (TWO) add_n(v, v, rest.v);
+      add_n(v, v, rest.v);
       if (AFFINE || a.w) {
         raw_to_f32<T, B>(load_raw<B>(w + i * G * V, i, n), f);
         mul_n(f, f, scale.v);

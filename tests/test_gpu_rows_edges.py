@@ -1,0 +1,49 @@
+"""The row operators where float32 runs out of bits or range: means far from the
+values' spread, rows at the ends of float32."""
+import pytest
+import torch
+
+import implicit_gemm_cnn_gb300 as conv
+import rows_ref as ref
+from dense_ref import TORCH, check, rounded
+
+pytestmark = pytest.mark.gpu
+
+if not torch.cuda.is_available():
+    pytest.skip("needs a CUDA device", allow_module_level=True)
+
+TYPES = ["f32", "f16", "bf16"]
+U = ref.U
+
+
+def normal(*shape, dtype, seed, scale=1.0, shift=0.0):
+    g = torch.Generator().manual_seed(seed)
+    return (torch.randn(*shape, generator=g, dtype=torch.float64) * scale + shift).to(TORCH[dtype])
+
+
+def nearly_constant(rows, width, dtype):
+    """Rows of one value but for a few that are its last place larger: the mean lies between two float32 values, and what
+    is left of the other values is far below the mean's rounding."""
+    value, place = {"f32": (4096.0, 2.0 ** -11), "f16": (1024.0, 1.0), "bf16": (256.0, 2.0)}[dtype]
+    x = torch.full((rows, width), value, dtype=torch.float64)
+    for r in range(rows):
+        x[r, (37 * r) % width] += place
+        x[r, (11 * r + 5) % width] += place
+    return x.to(TORCH[dtype])
+
+
+# a warp to a row, a block, accesses of one value, rows too wide for registers (no powers of two: their means are exact)
+NEARLY = [(700, 520, 0), (3, 4104, 0), (3, 1003, 0), (2, 16376, 0), (2, 40000, 0), (3, 2056, conv.FLAG_NORM_STREAM)]
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width,flags", NEARLY)
+def test_norm_of_nearly_constant_rows(rows, width, flags, dtype):
+    """Both means are taken off one after the other in every type, so the bound is float32's (that of 16-bit results in
+    rows_ref has U |mean| for one rounded mean), and a rounding to the type."""
+    x = nearly_constant(rows, width, dtype)
+    w, b = (normal(width, dtype=dtype, seed=s, scale=0.3, shift=1.0) for s in (1, 2))
+    for weight, bias in ((None, None), (w, b)):
+        y = conv.layer_norm(x.cuda(), *(None if t is None else t.cuda() for t in (weight, bias)), flags=flags)
+        want, err = ref.norm64(x.double(), *(None if t is None else t.double() for t in (weight, bias)), 1e-5, "f32")["y"]
+        check(y, rounded(want, err, dtype), "y")
