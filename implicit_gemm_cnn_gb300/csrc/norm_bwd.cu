@@ -196,8 +196,8 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const NormArgs a, c
       const long long r = base + group + k * step;
       const float c1 = __shfl_sync(0xffffffffu, sum, 2 * k) * inv, c2 = __shfl_sync(0xffffffffu, sum, 2 * k + 1) * inv;
       T* dx = dx0 + r * a.width;
-      // rstd (g - c1 - (x - mean) rstd c2)
-      const Same<V> minus(-mean[k]), scale(rstd[k]), slope(-rstd[k] * rstd[k] * c2), shift(-rstd[k] * c1);
+      // rstd (g - c1 - (x - mean) rstd c2); (rstd^2 c2 as one factor would leave float32's range where rstd is 1e18)
+      const Same<V> minus(-mean[k]), scale(rstd[k]), slope(-rstd[k] * c2), shift(-rstd[k] * c1);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         float x[V], g[V];
@@ -212,6 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const NormArgs a, c
         raw_to_f32<T, B>(rd[k][i], g);
         times_weight(i, g);
         add_n(x, x, minus.v);
+        mul_n(x, x, scale.v);
         fma_n(x, x, slope.v, shift.v);
         fma_n(g, g, scale.v, x);
         if (r < a.rows && i < n) store_raw<B>(dx + i * G * V, f32_to_raw<T, B>(g));

@@ -31,7 +31,7 @@ extern "C" {
  * x, y [rows][width]; weight, bias [width], each used iff has_* is nonzero. The
  * variance is summed from the differences to the mean, and the rounding of the
  * mean is taken out of them, so that a mean far larger than the spread costs no
- * bits of y.  (Squares of the differences have to fit float32.) */
+ * bits of y.  (A row's sum of squared differences has to fit float32.) */
 typedef struct conv_norm_problem {
   int64_t rows, width;              /* rows >= 0, width >= 1                   */
   int64_t x_stride, y_stride;       /* row strides, 0: dense; y_stride is dy's in the backward pass */

@@ -47,3 +47,21 @@ def test_norm_of_nearly_constant_rows(rows, width, flags, dtype):
         y = conv.layer_norm(x.cuda(), *(None if t is None else t.cuda() for t in (weight, bias)), flags=flags)
         want, err = ref.norm64(x.double(), *(None if t is None else t.double() for t in (weight, bias)), 1e-5, "f32")["y"]
         check(y, rounded(want, err, dtype), "y")
+
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("size,grad", [(1e-18, 1e4), (1e18, 1e-7)])
+@pytest.mark.parametrize("rows,width,flags", [(5, 64, 0), (700, 96, 0), (3, 1500, 0), (4, 77, 0), (3, 300, conv.FLAG_NORM_STREAM)])
+def test_norm_gradients_of_tiny_and_huge_rows(rows, width, flags, size, grad, dtype):
+    """rstd of 1e18 and 1e-18: its square, times c2, is no factor that float32 has, while every gradient is.  (A row's sum of
+    squared differences has to fit float32: that of 1500 values of 1e18, 1.5e39, is past 2^128.)"""
+    if size > 1:
+        size = size * min(1.0, 100 / width) ** 0.5
+    x, dy = (normal(rows, width, dtype=dtype, seed=s, scale=k) for s, k in ((1, size), (2, grad)))
+    w = normal(width, dtype=dtype, seed=3, scale=0.3, shift=1.0)
+    _, stats = conv.layer_norm(x.cuda(), w.cuda(), eps=0.0, save=True, flags=flags)
+    got = conv.layer_norm_backward(dy.cuda(), x.cuda(), w.cuda(), stats, flags=flags)
+    f = ref.norm64(x.double(), w.double(), None, 0.0, dtype)
+    want = ref.norm_backward64(dy.double(), f, w.double(), dtype)
+    for name, g in zip(("dx", "dweight", "dbias"), got):
+        check(g, want[name], name)
