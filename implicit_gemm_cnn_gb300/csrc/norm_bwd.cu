@@ -1,19 +1,24 @@
 // norm_bwd.cu -- layer norm, backward.
 //
-// dx needs two sums over a row, dweight and dbias sums over columns.  A block of
+// dx needs two sums over a row, dweight and dbias sums over columns.  A third sum
+// over the row, of the differences to the saved mean, is what that mean's rounding
+// left in them; it is taken out of xhat before dweight and dx are made of it.  A block of
 // 512 threads keeps the columns' sums in registers: a group of threads spans the
 // row, 8 to 32 values each (float32: 4 to 16), and where the row is short a
 // block has several groups.  A group takes R rows at a time and reduces their
 // sums in one go (a barrier and some 20 shuffles for all of them).  Rows of
 // whole 16-byte pieces come through shared memory, two batches of 64 KB ahead
 // (cp.async; a thread reads back only what it copied itself, so no barrier
-// stands between): the memory works under the arithmetic, some 110 instructions
+// stands between): the memory works under the arithmetic, some 115 instructions
 // for 8 values.  Other rows are loaded straight into registers.  Groups and
 // blocks leave their columns' sums to a second kernel, which adds them in order.
 //
 // What bounds it is memory, two reads and a write.  Measured with the second
-// kernel: 16384 x 8192 bfloat16 136 us (5.9 TB/s; without the batches ahead 172),
-// 8192 x 4096 43.6 (4.6), 1001 x 515 float32 7.0, 5000 x 1003 bfloat16 19.2.
+// kernel: 16384 x 8192 bfloat16 140 us (5.7 TB/s; with the mean's rounding left in
+// 135, without the batches ahead 172), 8192 x 4096 45.3 (4.4; 42.8), 1001 x 515
+// float32 7.2, 5000 x 1003 bfloat16 19.0.  Rows too wide for registers go value by
+// value, dx and the columns' sums in kernels of their own: 4096 x 16384 float32 305
+// (floor 120), 2000 x 20000 bfloat16 165.
 #include <algorithm>
 
 #include "norm.cuh"
@@ -28,14 +33,14 @@ constexpr int kColumns = 32;      // of a block that adds the partial sums
 constexpr int kRanges = 32;       // and the ranges of parts that it adds at once
 constexpr int kStreamRows = 64;   // rows of a block of the wide rows' column sums, at least
 
-// 2 * R sums (R a power of two) over the warp, halving the values with each step: afterwards v[0] of lane l is the sum of
-// value l % (2 R).
-template <int R>
-__device__ __forceinline__ void warp_sums(float (&v)[2 * R]) {
+// C sums (C a power of two) over the warp, halving the values with each step: afterwards v[0] of lane l is the sum of
+// value l % C.
+template <int C>
+__device__ __forceinline__ void warp_sums(float (&v)[C]) {
   const int lane = threadIdx.x % 32;
   int bit = 1;
 #pragma unroll
-  for (int n = 2 * R; n > 1; n /= 2, bit *= 2) {
+  for (int n = C; n > 1; n /= 2, bit *= 2) {
     const bool high = lane & bit;
 #pragma unroll
     for (int i = 0; i < n / 2; ++i) {  // even values stay with the lanes whose bit is clear
@@ -60,8 +65,9 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const NormArgs a, c
   constexpr int V = B / sizeof(T), N = E / V;
   constexpr bool HOLD = E * sizeof(T) <= 32;               // the weights in registers; else from the cache, row by row
   constexpr bool AHEAD = B == 16;
+  constexpr int C = 4 * R;                                 // sums of R rows: three each, and none
   extern __shared__ uint4 ahead[];                         // batches [kStages][R][x, dy][N][threads]; then the groups' sums
-  __shared__ float red[2][kThreads / 32][2 * R];
+  __shared__ float red[2][kThreads / 32][C];
   int turn = 0;
   const int G = warps * 32, group = threadIdx.x / G, groups = blockDim.x / G, t = threadIdx.x - group * G;
   const int lane = threadIdx.x % 32, warp0 = group * warps;
@@ -155,11 +161,11 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const NormArgs a, c
         }
       }
     }
-    float s[2 * R];
+    float s[C];
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const Same<V> scale(rstd[k]);
-      Sum<V> s1, s2;
+      Sum<V> s1, s2, s3;
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         float h[V], g[V];
@@ -167,37 +173,41 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const NormArgs a, c
         raw_to_f32<T, B>(rd[k][i], g);
         const Same<V> minus(i < n ? -mean[k] : 0.0f);  // (values that are not there stay zeros)
         add_n(h, h, minus.v);
-        mul_n(h, h, scale.v);
-        fma_n(dw[i], g, h, dw[i]);
+        if constexpr (V == 1) h[0] = __fmul_rn(h[0], rstd[k]);  // (no part of the sum's addition: every variant has the same sum)
+        else mul_n(h, h, scale.v);
+        s3.add(h);
         add_n(db[i], db[i], g);
         times_weight(i, g);
         s1.add(g);
         s2.add(g, h);
       }
-      s[2 * k] = s1.value();
-      s[2 * k + 1] = s2.value();
+      s[4 * k] = s1.value();
+      s[4 * k + 1] = s2.value();
+      s[4 * k + 2] = s3.value();
+      s[4 * k + 3] = 0.0f;
     }
     const int now = stage;
     stage = stage == kStages - 1 ? 0 : stage + 1;
-    if (!a.dx) continue;
-    warp_sums<R>(s);
-    float sum = s[0];  // of value lane % (2 R)
+    warp_sums<C>(s);
+    float sum = s[0];  // of value lane % C
     if (warps > 1) {
-      if (lane < 2 * R) red[turn][threadIdx.x / 32][lane] = sum;
+      if (lane < C) red[turn][threadIdx.x / 32][lane] = sum;
       __syncthreads();
       sum = 0.0f;
-      for (int k = lane / (2 * R); k < warps; k += 32 / (2 * R)) sum += red[turn][warp0 + k][lane % (2 * R)];
+      for (int k = lane / C; k < warps; k += 32 / C) sum += red[turn][warp0 + k][lane % C];
 #pragma unroll
-      for (int d = 2 * R; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+      for (int d = C; d < 32; d *= 2) sum += __shfl_xor_sync(0xffffffffu, sum, d);
       turn ^= 1;
     }
 #pragma unroll
     for (int k = 0; k < R; ++k) {
       const long long r = base + group + k * step;
-      const float c1 = __shfl_sync(0xffffffffu, sum, 2 * k) * inv, c2 = __shfl_sync(0xffffffffu, sum, 2 * k + 1) * inv;
+      const float c1 = __shfl_sync(0xffffffffu, sum, 4 * k) * inv, off = __shfl_sync(0xffffffffu, sum, 4 * k + 2) * inv;
+      const float c2 = fmaf(-off, c1, __shfl_sync(0xffffffffu, sum, 4 * k + 1) * inv);
       T* dx = dx0 + r * a.width;
-      // rstd (g - c1 - (x - mean) rstd c2); (rstd^2 c2 as one factor would leave float32's range where rstd is 1e18)
-      const Same<V> minus(-mean[k]), scale(rstd[k]), slope(-rstd[k] * c2), shift(-rstd[k] * c1);
+      // xhat = (x - mean) rstd - off,  dx = rstd (g - c1 - xhat c2); (rstd^2 c2 as one factor would leave float32's range
+      // where rstd is 1e18)
+      const Same<V> minus(-mean[k]), scale(rstd[k]), less(-off), slope(-rstd[k] * c2), shift(-rstd[k] * c1);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         float x[V], g[V];
@@ -210,12 +220,13 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const NormArgs a, c
         }
         raw_to_f32<T, B>(rx[k][i], x);
         raw_to_f32<T, B>(rd[k][i], g);
-        times_weight(i, g);
         add_n(x, x, minus.v);
-        mul_n(x, x, scale.v);
+        fma_n(x, x, scale.v, less.v);
+        fma_n(dw[i], g, x, dw[i]);  // (of values that are not there g is zero, or nobody reads dw)
+        times_weight(i, g);
         fma_n(x, x, slope.v, shift.v);
         fma_n(g, g, scale.v, x);
-        if (r < a.rows && i < n) store_raw<B>(dx + i * G * V, f32_to_raw<T, B>(g));
+        if (a.dx && r < a.rows && i < n) store_raw<B>(dx + i * G * V, f32_to_raw<T, B>(g));
       }
     }
   }
@@ -245,46 +256,61 @@ __global__ void __launch_bounds__(kThreads, 1) norm_backward(const NormArgs a, c
   }
 }
 
-// Rows of any width, dx: two passes over the row.
-template <typename T>
-__global__ void __launch_bounds__(1024) norm_backward_stream(const NormArgs a) {
-  __shared__ float red[2][2][32];
+// Rows of any width: two passes over the row, one over x alone where dx is not wanted.  `rows` (if not nullptr) receives for
+// the columns' sums a row's mean, rstd, and what the mean's rounding left in its xhat.  (No early launch of what follows: that
+// kernel's blocks, waiting among this one's, cost 40 us of 4096 rows of 16384 float32.)
+template <typename T, bool WEIGHT>
+__global__ void __launch_bounds__(1024) norm_backward_stream(const NormArgs a, float4* const rows) {
+  __shared__ float red[2][3][32];
   int turn = 0;
   griddep_wait();
-  griddep_launch();
+  const int width = static_cast<int>(a.width);
   for (long long r = blockIdx.x; r < a.rows; r += gridDim.x) {
     const T* x = static_cast<const T*>(a.x) + r * a.ldx;
     const T* dy = static_cast<const T*>(a.dy) + r * a.ldy;
     T* dx = static_cast<T*>(a.dx) + r * a.width;
-    const float mean = a.stats[2 * r], rstd = a.stats[2 * r + 1];
-    float s[2] = {0.0f, 0.0f};
-    for (long long c = threadIdx.x; c < a.width; c += blockDim.x) {
-      float g = to_f32(dy[c]);
-      if (a.w) g *= to_f32(static_cast<const T*>(a.w)[c]);
-      s[0] += g;
-      s[1] = fmaf(g, (to_f32(x[c]) - mean) * rstd, s[1]);
+    const float2 stats = *reinterpret_cast<const float2*>(a.stats + 2 * r);
+    const float mean = stats.x, rstd = stats.y;
+    auto gradient = [&](int c) {
+      const float g = to_f32(dy[c]);
+      return WEIGHT ? g * to_f32(static_cast<const T*>(a.w)[c]) : g;
+    };
+    float s[3] = {0.0f, 0.0f, 0.0f};
+    if (a.dx) {
+#pragma unroll 4
+      for (int c = threadIdx.x; c < width; c += 1024) {
+        const float g = gradient(c), h = __fmul_rn(to_f32(x[c]) - mean, rstd);  // (rounded by itself: the same sum below)
+        s[0] += g;
+        s[1] = fmaf(g, h, s[1]);
+        s[2] += h;
+      }
+    } else {
+#pragma unroll 4
+      for (int c = threadIdx.x; c < width; c += 1024) s[2] += __fmul_rn(to_f32(x[c]) - mean, rstd);
     }
-    block_sum<2>(s, red, turn);
-    const float n = static_cast<float>(a.width), c1 = s[0] / n, c2 = s[1] / n;
-    for (long long c = threadIdx.x; c < a.width; c += blockDim.x) {
-      float g = to_f32(dy[c]);
-      if (a.w) g *= to_f32(static_cast<const T*>(a.w)[c]);
-      dx[c] = from_f32<T>(rstd * (g - c1 - (to_f32(x[c]) - mean) * rstd * c2));
-    }
+    block_sum<3>(s, red, turn);
+    const float n = static_cast<float>(width), c1 = s[0] / n, off = s[2] / n, c2 = fmaf(-off, c1, s[1] / n);
+    if (rows && threadIdx.x == 0) rows[r] = make_float4(mean, rstd, off, 0.0f);
+    if (!a.dx) continue;
+#pragma unroll 4
+    for (int c = threadIdx.x; c < width; c += 1024)
+      dx[c] = from_f32<T>(rstd * (gradient(c) - c1 - fmaf(to_f32(x[c]) - mean, rstd, -off) * c2));
   }
 }
 // The column sums of wide rows: a block has 256 columns of one range of rows.
 template <typename T>
-__global__ void __launch_bounds__(256) norm_columns_stream(const NormArgs a, const long long per) {
+__global__ void __launch_bounds__(256) norm_columns_stream(const NormArgs a, const float4* const rows, const long long per) {
   griddep_wait();
   griddep_launch();
   const long long c = static_cast<long long>(blockIdx.x) * 256 + threadIdx.x;
   if (c >= a.width) return;
   const long long r0 = blockIdx.y * per, r1 = min(a.rows, r0 + per);
   float dw = 0.0f, db = 0.0f;
+#pragma unroll 8
   for (long long r = r0; r < r1; ++r) {
+    const float4 f = rows[r];
     const float g = to_f32(static_cast<const T*>(a.dy)[r * a.ldy + c]);
-    dw = fmaf(g, (to_f32(static_cast<const T*>(a.x)[r * a.ldx + c]) - a.stats[2 * r]) * a.stats[2 * r + 1], dw);
+    dw = fmaf(g, fmaf(to_f32(static_cast<const T*>(a.x)[r * a.ldx + c]) - f.x, f.y, -f.z), dw);
     db += g;
   }
   float* part = a.part + static_cast<long long>(blockIdx.y) * 2 * a.width;
@@ -338,6 +364,15 @@ BackShape back_shape(long long rows, long long width, int es, int sm) {
   return s;
 }
 bool streams(long long width, int es, bool stream) { return stream || back_shape(1, width, es, 1).values == 0; }
+// Blocks of rows whose sums of dweight and dbias go to `part`.
+long long parts_of(long long rows, long long width, int es, bool stream, int sm) {
+  if (streams(width, es, stream)) {
+    const long long strips = (width + 255) / 256;
+    return std::max<long long>(1, std::min({8LL * sm / strips, (rows + kStreamRows - 1) / kStreamRows, 65535LL}));
+  }
+  return back_shape(rows, width, es, sm).blocks;
+}
+size_t part_floats(long long parts, long long width) { return (static_cast<size_t>(parts) * 2 * width + 3) / 4 * 4; }
 
 template <typename T, int B, int E, int R>
 cudaError_t go(const NormArgs& a, const BackShape& sh, int sums, cudaStream_t s) {
@@ -361,15 +396,16 @@ cudaError_t by_values(const NormArgs& a, const BackShape& sh, int sums, cudaStre
 template <typename T>
 cudaError_t by_type(const NormArgs& a, bool stream, int sm, cudaStream_t s) {
   const int sums = a.dw || a.db;
-  const int parts = static_cast<int>(norm_backward_parts(a.rows, a.width, sizeof(T), stream, sm));
+  const int parts = static_cast<int>(parts_of(a.rows, a.width, sizeof(T), stream, sm));
   cudaError_t err = cudaSuccess;
   if (streams(a.width, sizeof(T), stream)) {
-    if (a.dx)
-      err = launch_overlapped(norm_backward_stream<T>, dim3(static_cast<unsigned>(std::min<long long>(a.rows, 2LL * sm))), 1024, 0,
-                              1, s, a);
+    float4* const rows = sums ? reinterpret_cast<float4*>(a.part + part_floats(parts, a.width)) : nullptr;
+    if (a.dx || sums)
+      err = launch_overlapped(a.w ? norm_backward_stream<T, true> : norm_backward_stream<T, false>,
+                              dim3(static_cast<unsigned>(std::min<long long>(a.rows, 2LL * sm))), 1024, 0, 1, s, a, rows);
     if (err == cudaSuccess && sums)
       err = launch_overlapped(norm_columns_stream<T>, dim3(static_cast<unsigned>((a.width + 255) / 256), static_cast<unsigned>(parts)),
-                              256, 0, 1, s, a, (a.rows + parts - 1) / parts);
+                              256, 0, 1, s, a, rows, (a.rows + parts - 1) / parts);
   } else if (a.dx || sums) {
     const BackShape sh = back_shape(a.rows, a.width, sizeof(T), sm);
     const int bytes = access_bytes(sizeof(T), a.width, {a.x, a.w, a.dy, a.dx},
@@ -386,12 +422,9 @@ cudaError_t by_type(const NormArgs& a, bool stream, int sm, cudaStream_t s) {
 
 }  // namespace
 
-long long norm_backward_parts(long long rows, long long width, int es, bool stream, int sm) {
-  if (streams(width, es, stream)) {
-    const long long strips = (width + 255) / 256;
-    return std::max<long long>(1, std::min({8LL * sm / strips, (rows + kStreamRows - 1) / kStreamRows, 65535LL}));
-  }
-  return back_shape(rows, width, es, sm).blocks;
+size_t norm_backward_scratch(long long rows, long long width, int es, bool stream, int sm) {
+  return part_floats(parts_of(rows, width, es, stream, sm), width) * sizeof(float) +
+         (streams(width, es, stream) ? static_cast<size_t>(rows) * sizeof(float4) : 0);
 }
 
 cudaError_t launch_norm_backward(const NormArgs& a, int dtype, bool stream, int sm, cudaStream_t s) {

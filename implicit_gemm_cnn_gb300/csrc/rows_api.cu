@@ -33,7 +33,7 @@ conv_status validate(const conv_norm_problem* p, NormShape* s) {
 }
 bool norm_streams(const conv_norm_problem* p) { return (p->flags & CONV_NORM_FLAG_STREAM) != 0; }
 size_t norm_scratch(const conv_norm_problem* p, int sm) {
-  return p->rows == 0 ? 0 : align256(static_cast<size_t>(norm_backward_parts(p->rows, p->width, static_cast<int>(elem_size(p->dtype)), norm_streams(p), sm)) * 2 * p->width * sizeof(float));
+  return p->rows == 0 ? 0 : align256(norm_backward_scratch(p->rows, p->width, static_cast<int>(elem_size(p->dtype)), norm_streams(p), sm));
 }
 
 // ---- dropout ------------------------------------------------------------------

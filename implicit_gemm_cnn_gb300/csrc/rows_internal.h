@@ -212,13 +212,12 @@ struct NormArgs {
   const void *x, *w, *b, *dy;
   void *y, *dx, *dw, *db;
   float* stats;             // [rows][2]: written forward (or nullptr), read backward
-  float* part;              // backward: float32 [blocks][2][width]
+  float* part;              // backward: the scratch, float32 [blocks][2][width] and, of wide rows, [rows][4]
   long long rows, width, ldx, ldy;
   float eps;
 };
 cudaError_t launch_norm_forward(const NormArgs& a, int dtype, bool stream, int sm, cudaStream_t s);
-// Blocks of rows whose sums of dweight and dbias go to `part`.
-long long norm_backward_parts(long long rows, long long width, int es, bool stream, int sm);
+size_t norm_backward_scratch(long long rows, long long width, int es, bool stream, int sm);  // bytes
 cudaError_t launch_norm_backward(const NormArgs& a, int dtype, bool stream, int sm, cudaStream_t s);
 
 // Dropout (dropout.cu).

@@ -51,12 +51,13 @@ typedef struct conv_norm_problem {
 CONV_API conv_status conv_norm_forward(const conv_norm_problem* p, const void* x, const void* weight, const void* bias,
                                        void* y, float* stats, void* stream);
 
-/* The gradients for dy (row stride p->y_stride), with xhat = (x - mean) * rstd and g = dy * weight:
+/* The gradients for dy (row stride p->y_stride), with xhat = (x - mean) * rstd and g = dy * weight (the saved mean is
+ * rounded; what that leaves in xhat is summed over the row and taken out again):
  *   dx = rstd (g - sum_i g / width - xhat sum_i (g xhat) / width)
  *   dweight = sum over rows of dy xhat,   dbias = sum over rows of dy
  * Outputs are dense, of the problem's element type; NULL ones are not computed.  weight is read iff
  * p->has_weight and dx is wanted.  With rows = 0, dweight and dbias are set to zero.  Scratch: the sums of blocks of
- * rows, 256-byte aligned.  Errors: as above, and CONV_ERR_SCRATCH. */
+ * rows (and 16 bytes for each row too wide for registers), 256-byte aligned.  Errors: as above, and CONV_ERR_SCRATCH. */
 CONV_API conv_status conv_norm_backward_scratch_bytes(const conv_norm_problem* p, size_t* bytes);
 CONV_API conv_status conv_norm_backward(const conv_norm_problem* p, const void* x, const void* weight, const float* stats,
                                         const void* dy, void* dx, void* dweight, void* dbias, void* scratch,

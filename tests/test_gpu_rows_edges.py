@@ -65,3 +65,57 @@ def test_norm_gradients_of_tiny_and_huge_rows(rows, width, flags, size, grad, dt
     want = ref.norm_backward64(dy.double(), f, w.double(), dtype)
     for name, g in zip(("dx", "dweight", "dbias"), got):
         check(g, want[name], name)
+
+
+def gradients64(x, dy, w, eps, dtype):
+    """The gradients, with bounds for a backward pass that takes the saved mean's rounding out of xhat again: the mean of the
+    differences to that mean is summed as the two other sums are, and taken off."""
+    n = x.shape[1]
+    k = ref.depth(n)
+    f = ref.norm64(x, w, None, eps, "f32")
+    (h, _), (r, er) = f["h"], f["r"]
+    mean = x.mean(1, keepdim=True)
+    spread = (x - mean).abs() + U * mean.abs() + k * U * x.abs().mean(1, keepdim=True)
+    # of a difference: its own rounding and its product's, then what was taken off: the sum's, and the differences' in it
+    ec = 3 * U * spread + (k + 5) * U * spread.mean(1, keepdim=True)
+    eh = r * ec + spread * er + 2 * U * h.abs()
+    return ref.norm_backward64(dy, {"h": (h, eh), "r": (r, er)}, w, dtype)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width,flags", NEARLY)
+def test_norm_gradients_of_nearly_constant_rows(rows, width, flags, dtype):
+    x, dy = nearly_constant(rows, width, dtype), normal(rows, width, dtype=dtype, seed=3, scale=0.5, shift=0.2)
+    w = normal(width, dtype=dtype, seed=1, scale=0.3, shift=1.0)
+    _, stats = conv.layer_norm(x.cuda(), w.cuda(), save=True, flags=flags)
+    want = gradients64(x.double(), dy.double(), w.double(), 1e-5, dtype)
+    for name, g in zip(("dx", "dweight", "dbias"), conv.layer_norm_backward(dy.cuda(), x.cuda(), w.cuda(), stats, flags=flags)):
+        check(g, want[name], name)
+    alone = conv.layer_norm_backward(dy.cuda(), x.cuda(), w.cuda(), stats, need_dx=False, need_dbias=False, flags=flags)[1]
+    check(alone, want["dweight"], "dweight alone")
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width,flags", [(9, 101, 0), (300, 1003, 0), (5, 4099, 0), (5, 8191, 0), (5, 17001, 0),
+                                              (300, 260, 0), (200, 700, conv.FLAG_NORM_STREAM)])
+def test_norm_gradients_alone_and_together_are_the_same_bits(rows, width, flags, dtype):
+    x, dy = (normal(rows, width, dtype=dtype, seed=s, shift=1.0).cuda() for s in (1, 2))
+    w = normal(width, dtype=dtype, seed=3).cuda()
+    _, stats = conv.layer_norm(x, w, save=True, flags=flags)
+    every = conv.layer_norm_backward(dy, x, w, stats, flags=flags)
+    for i in range(3):
+        need = [j == i for j in range(3)]
+        some = conv.layer_norm_backward(dy, x, w, stats, need_dx=need[0], need_dweight=need[1], need_dbias=need[2], flags=flags)
+        assert torch.equal(some[i], every[i])
+
+
+@pytest.mark.parametrize("rows,width,shift,flags", [
+    (1, 768, 3e4, 0), (20, 768, 1000.0, 0), (20, 5000, -3e4, 0), (3, 20000, 500.0, 0), (700, 200, 3e4, 0), (5, 1003, 3e4, 0),
+    (150, 700, 3e4, conv.FLAG_NORM_STREAM)])
+def test_norm_gradients_of_a_mean_far_from_zero(rows, width, shift, flags):
+    x, dy = normal(rows, width, dtype="f32", seed=4, shift=shift), normal(rows, width, dtype="f32", seed=5, scale=0.5, shift=0.2)
+    w = normal(width, dtype="f32", seed=6, scale=0.3, shift=1.0)
+    _, stats = conv.layer_norm(x.cuda(), w.cuda(), save=True, flags=flags)
+    want = gradients64(x.double(), dy.double(), w.double(), 1e-5, "f32")
+    for name, g in zip(("dx", "dweight", "dbias"), conv.layer_norm_backward(dy.cuda(), x.cuda(), w.cuda(), stats, flags=flags)):
+        check(g, want[name], name)
