@@ -132,6 +132,7 @@ typedef struct conv_int8_problem {
 #define CONV_INT8_FLAG_MID 0x20u   /* testing: that for some tens to hundreds (at most 2^20,
                                       weights in rows on 16-byte boundaries) */
 #define CONV_INT8_FLAG_MANY 0x40u  /* testing: that for many                                    */
+/* A flag whose kernel cannot run the call is passed over (conv_int8_describe_plan says what runs). */
 
 /* Scratch bytes on the current device.  Errors: as conv_linear_scratch_bytes. */
 CONV_API conv_status conv_int8_scratch_bytes(const conv_int8_problem* p, size_t* bytes);
