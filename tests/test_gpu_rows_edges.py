@@ -119,3 +119,22 @@ def test_norm_gradients_of_a_mean_far_from_zero(rows, width, shift, flags):
     want = gradients64(x.double(), dy.double(), w.double(), 1e-5, "f32")
     for name, g in zip(("dx", "dweight", "dbias"), conv.layer_norm_backward(dy.cuda(), x.cuda(), w.cuda(), stats, flags=flags)):
         check(g, want[name], name)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("rows,width", [(700, 264), (300, 4096), (40, 5001), (3, 40000)])
+def test_quantised_rows_beside_those_of_a_divided_scale(rows, width, dtype):
+    """The scale is the product of a row's largest value with 1 / 127 rounded; the quotient by 127, rounded once, is another
+    definition.  What tells them apart: a scale's bits by the rounding of 1 / 127 (U / 16 here) and the two results' (U each),
+    so a quotient of at most 127 by less than 127 (2 + 1 / 16) U, and an 8-bit value by one, where the quotient lies so near a
+    half.  (In 16 bits such quotients are common: both numbers are short.)"""
+    x = normal(rows, width, dtype=dtype, seed=rows + width)
+    q, scale = (t.cpu().double() for t in conv.quantize_rows(x.cuda()))
+    wide = x.double()
+    divided = (wide.abs().amax(1) / 127).float().double()
+    apart = (2 + 1 / 16) * U * 1.001
+    assert ((scale - divided).abs() <= apart * divided).all()
+    exact = wide / divided[:, None]
+    moved = q != exact.round().clamp(-127, 127)
+    assert ((q - exact.round()).abs()[moved] == 1).all()
+    assert (((exact - exact.floor())[moved] - 0.5).abs() <= 127 * apart).all()
