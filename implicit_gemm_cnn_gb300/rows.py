@@ -8,6 +8,7 @@ keep the C names and only marshal arguments; ``layer_norm``,
 from __future__ import annotations
 
 import ctypes
+from operator import index as _whole
 
 from . import DTYPES, _check, _dtype_name, _ptr, load
 from .dense import (FLAG_LINEAR_RESIDUAL_LAST, LINEAR_ACTIVATIONS, _dense_out, _rows_dense, _run, _same, _scratch,
@@ -330,6 +331,9 @@ def _dropout_plan(x, residual, out, seed):
 
 def _dropout(back, x, p, seed, offset, residual, out, stream):
     state = hasattr(seed, "data_ptr")
+    offset = _whole(offset)  # (numpy's whole numbers refuse 64-bit masks)
+    if not state:
+        seed = _whole(seed)
     key = ("dropout", x.shape, x.dtype, x.get_device(), x.is_contiguous(),
            residual if residual is None else _tag(residual), out if out is None else _tag(out), _tag(seed) if state else None)
     found = _seen.get(key)

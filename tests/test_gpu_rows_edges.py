@@ -138,3 +138,17 @@ def test_quantised_rows_beside_those_of_a_divided_scale(rows, width, dtype):
     moved = q != exact.round().clamp(-127, 127)
     assert ((q - exact.round()).abs()[moved] == 1).all()
     assert (((exact - exact.floor())[moved] - 0.5).abs() <= 127 * apart).all()
+
+
+def test_dropout_takes_seeds_and_offsets_of_any_whole_number_type():
+    import numpy
+    x = torch.ones(6, 40, device="cuda")
+    want, back = conv.dropout(x, 0.5, 7, 3), conv.dropout_backward(x, 0.5, 7, 3)
+    for seed, offset in ((numpy.int64(7), 3), (7, numpy.int64(3)), (numpy.uint64(7), numpy.int32(3))):
+        assert torch.equal(conv.dropout(x, 0.5, seed, offset), want)
+        assert torch.equal(conv.dropout_backward(x, 0.5, seed, offset), back)
+    assert torch.equal(conv.dropout(x, 0.5, numpy.int64(-1), numpy.int64(-2)), conv.dropout(x, 0.5, -1, -2))
+    assert torch.equal(conv.dropout(x, 0.5, numpy.uint64(2 ** 64 - 1)), conv.dropout(x, 0.5, -1))
+    for bad in ((7.0, 0), (7, 1.5), ("7", 0)):
+        with pytest.raises(TypeError):
+            conv.dropout(x, 0.5, *bad)
