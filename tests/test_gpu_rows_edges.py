@@ -152,3 +152,31 @@ def test_dropout_takes_seeds_and_offsets_of_any_whole_number_type():
     for bad in ((7.0, 0), (7, 1.5), ("7", 0)):
         with pytest.raises(TypeError):
             conv.dropout(x, 0.5, *bad)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("xs,qs,at", [(264, 264, 0), (272, 300, 4), (301, 265, 1), (266, 266, 2), (280, 264, 8)])
+def test_quantised_rows_of_any_stride_and_address(xs, qs, at, dtype):
+    """conv_quantize_rows into rows of their own stride, from any address; what lies between the rows stays."""
+    for rows, width in ((1, 257), (40, 264), (700, 256), (9, 3)):
+        flat = normal(at + rows * xs + width, dtype=dtype, seed=rows).cuda()
+        x = flat[at:].as_strided((rows, width), (xs, 1))
+        q = torch.full((at + rows * qs + width,), 99, dtype=torch.int8, device="cuda")
+        scale = torch.empty(rows, device="cuda")
+        conv.conv_quantize_rows(conv.make_quantize_problem(rows, width, dtype=dtype, x_stride=xs, q_stride=qs), x, q[at:], scale)
+        want, s = ref.quantize64(x.cpu().double())
+        assert torch.equal(scale.cpu(), s)
+        full = torch.full_like(q, 99).cpu()
+        full[at:].as_strided((rows, width), (qs, 1)).copy_(want)
+        assert torch.equal(q.cpu(), full)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_dropout_backward_into_strided_rows(dtype):
+    for rows, width, off, pad in ((40, 301, 3, 5), (40, 304, 8, 8), (5, 17, 0, 1)):
+        dy = normal(rows, width + 6, dtype=dtype, seed=1).cuda()[:, 2:2 + width]
+        full = torch.full((rows, off + width + pad), 77.0, dtype=TORCH[dtype], device="cuda")
+        out = full[:, off:off + width]
+        assert conv.dropout_backward(dy, 0.3, 5, 6, out=out) is out
+        assert torch.equal(out, conv.dropout_backward(dy.contiguous(), 0.3, 5, 6))
+        assert (full[:, :off] == 77).all() and (full[:, off + width:] == 77).all()
