@@ -1,5 +1,6 @@
 // int8_few.cu -- the 8-bit product for few rows (one row is one generated
-// token): the weights, a byte each, are read once, straight into registers.
+// token): the weights, a byte each, go straight into registers, once for each
+// tile of at most 32 rows of x (128 rows: four times, mostly out of L2).
 //
 // sm_103's 8-bit tensor-core kinds are gone (tcgen05 has no kind::i8 here), its
 // CUDA cores' dp4a is slow, but 16-bit floats hold every 8-bit integer: a byte u
@@ -9,17 +10,24 @@
 // most 256 terms) then move into int32.
 //
 // A block takes 16 output features at a time, its eight warps every eighth piece
-// of k.  The weights are the 16-row operand, the rows of x the 8 columns; a lane
-// loads 16 consecutive bytes of a weight row and of an x row, which are the k's
-// of four MMAs (both operands in the same order, so which k is which does not
-// matter).  The warps' sums meet in shared memory.
+// of k.  The weights are the 16-row operand, the rows of x the 8 columns (a tile
+// has NB = 1, 2 or 4 groups of 8 rows); a lane loads 16 consecutive bytes of a
+// weight row and of an x row, which are the k's of four MMAs (both operands in the
+// same order, so which k is which does not matter).  The warps' sums meet in shared
+// memory.
+//
+// A piece is CH chunks of 64 terms: four of them (256 terms of 16 outputs, 4 KB a
+// warp in flight and as much at work) for tiles of at most 16 rows, two for tiles of
+// 32, whose sums take the registers; half as many where the weights' rows are no whole
+// 16-byte pieces, since each chunk is then two loads (put together on arrival).
 //
 // What bounds it: the weights' loads, and the barriers of each 16 outputs.  One
 // row of 4096 -> 12288 14.4 us (50 MB: 3.5 TB/s), 16 rows 17.4, 32 rows 25.6;
 // 2048 -> 8192 6.8, 8.1, 10.9; 4003 -> 12288, x quantised by the call, 25, 31, 42.
-// A piece of 256 terms (two 64-byte chunks of each of 32 rows in flight, twice
-// over) and two blocks an SM are the quickest for one row: pieces of 64 terms
-// took 18.7 us, of 512 17.9; 32 or 64 outputs a block 16.7 and 17.7.
+// (linear's kernel for few rows reads the same layer in 16 bits at 5.6 TB/s, so one
+// row in 8 bits saves a sixth of its 18.0 us, not half.)
+// Pieces of 256 terms and two blocks an SM are the quickest for one row: pieces of
+// 64 terms took 18.7 us, of 512 17.9; 32 or 64 outputs a block 16.7 and 17.7.
 #include <algorithm>
 
 #include "int8.cuh"

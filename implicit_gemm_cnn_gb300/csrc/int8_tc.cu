@@ -13,7 +13,10 @@
 //
 // What bounds it is the tensor pipe: 77% of its rate (4864 x 4096 -> 4096 97 us,
 // 1.68 PFLOP/s), where the one accumulator of a 16-bit product leaves 84.  With the
-// passes before it 2048 x 4096 -> 4096 takes 58 us, 8192 x 4096 -> 12288 492.
+// passes before it 2048 x 4096 -> 4096 takes 58 us, 8192 x 4096 -> 12288 492 at full
+// clock and 540 to 585 in longer runs, at the power limit.  (linear, whose operands are
+// halves already: 40 and 414 beside 60 and 540, one after the other on one machine.)
+// A pair's variants spill: 300 bytes for 16-bit results, 180 for float32.
 #include <string.h>
 
 #include <algorithm>

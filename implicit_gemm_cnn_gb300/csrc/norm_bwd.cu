@@ -18,7 +18,10 @@
 // 135, without the batches ahead 172), 8192 x 4096 45.3 (4.4; 42.8), 1001 x 515
 // float32 7.2, 5000 x 1003 bfloat16 19.0.  Rows too wide for registers go value by
 // value, dx and the columns' sums in kernels of their own: 4096 x 16384 float32 305
-// (floor 120), 2000 x 20000 bfloat16 165.
+// (floor 120), 2000 x 20000 bfloat16 165.  Rows of no whole 16-byte pieces go value
+// by value as well, 15370 x 1003 float32 49 (28); from 8193 to 16384 values of 16
+// bits, 32 a thread, such a kernel spills 550 bytes with a weight and 170 without
+// (pairs of values: 80 and none), 5000 x 12001 bfloat16 275 (54).
 #include <algorithm>
 
 #include "norm.cuh"

@@ -8,8 +8,14 @@
 // squared distances), so no sum of squares is about a mean far from its values.
 // What bounds it is memory, a read and a write of each value, and the some 130
 // instructions for 8 values nearly as much (ncu: issue slots 60%).  Measured:
-// 8192 x 4096 bfloat16 27.8 us (4.8 TB/s), 16384 x 8192 100 (5.4), 1 x 4096 2.0;
-// 1001 x 515 float32 4.2; 5000 x 1003 bfloat16, which goes value by value, 16.0.
+// 8192 x 4096 bfloat16 28 us (4.8 TB/s), 16384 x 8192 102 (5.3), 1 x 4096 2.1;
+// float32 8192 x 4096 46 (5.8), 4096 x 16384 108 (5.0), 1001 x 515 4.3.  Rows of no
+// whole 16-byte pieces go value by value: 5000 x 1003 bfloat16 16, 5000 x 12001 158,
+// 15370 x 1003 float32 33 (floors 3, 36, 18); rows too wide for registers too, in
+// three walks: 1000 x 9001 float32 38, 2000 x 20000 bfloat16, in registers, 54
+// (floors 11 and 24).  At the limit of 64 registers the variants of four 16-byte
+// accesses a thread spill 16 to 48 bytes, those of 16 values 4 to 48, and those of
+// 32 values, at 128 registers, some 100.
 #include <algorithm>
 
 #include "norm.cuh"

@@ -3,7 +3,9 @@
 //
 // A row is read once, into registers (norm.cuh).  What bounds it is the issue of
 // instructions as much as memory (ncu: 64 to 70% of the slots).  Measured:
-// 8192 x 4096 bfloat16 to bytes 23.4 us (4.3 TB/s), 1 x 4096 1.6.  Cold: 2048 x
+// 8192 x 4096 bfloat16 to bytes 23.4 us (4.3 TB/s), float32 32.7 (5.1), 1 x 4096 1.6;
+// value by value 15370 x 1003 bfloat16 22.6 (2.0), float32 25.8 (3.0); 2000 x 20000
+// bfloat16 44 (2.7), 2000 x 40000, too wide for registers, 141 (1.7).  Cold: 2048 x
 // 4096 to halves 10.7 us, 4096 x 4096 bytes to halves 9.6 (5.2 TB/s).
 #include <algorithm>
 

@@ -110,7 +110,10 @@ conv_status validate(const conv_int8_problem* p, Int8Shape* s) {
 // Which kernel: the weights straight into registers (few rows), through shared memory (mid), or as halves first (many).
 // The second takes weights in rows on 16-byte boundaries only (TMA).  The first works on 32 rows and 16 outputs at a time, two
 // blocks an SM.  From 17 rows on the choice goes by what these take (fitted to the measurements): the first, in r rounds of such
-// blocks, 0.6 + 1.5 r (k + 1) us for k times 1024 terms, the second 9.2 + 0.8 k.
+// blocks, 0.6 + 1.5 r (k + 1) us for k times 1024 terms, the second 9.2 + 0.8 k.  The fit ends at 128 rows, a tile of the
+// second, and so does the choice: above, small layers would still be quicker without a pass over the weights (x quantised by
+// the call, few / mid / many: 129 rows 1024->1024 6.6 / 10.8 / 9.5, 2048->2048 14.3 / 12.9 / 13.3; 256 rows 8.5 / 12.9 / 9.7
+// and 21.3 / 15.8 / 13.8).
 // Measured (us, few / mid / many):
 //              16 rows        32             64             96             128            256
 //   1024->1024                                3 /  9 /  9    4 / 11 /  9    4 / 12 /  9
@@ -318,6 +321,7 @@ conv_status conv_int8_scratch_bytes(const conv_int8_problem* p, size_t* bytes) {
   int dev, sm;
   if (st == CONV_OK) st = current_device(&dev, &sm);
   if (st != CONV_OK) return st;
+  // (addresses are not known: the most of all.  Weights off 16-byte boundaries may need halves where others do not.)
   *bytes = 0;
   for (int i = 0; i < 4; ++i) *bytes = std::max(*bytes, plan_int8(p, sh, i & 1, i & 2, sm).total);
   return CONV_OK;

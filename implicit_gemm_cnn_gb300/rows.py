@@ -472,7 +472,9 @@ def linear_int8(x, w, w_scale, bias=None, residual=None, *, x_scale=None, dtype=
     quantised by the call, or int8 with its x_scale [...] float32.  bias [c_out],
     residual and y [..., c_out] have x's element type, or ``dtype`` for an int8 x.
     The integer sums are exact.  Activations and ``residual_last`` as in
-    ``linear``."""
+    ``linear``.  Half the weights' memory; quicker than ``linear`` for up to some
+    16 rows, as quick for some tens in a wide layer, slower from some hundreds on
+    (2048 rows of 4096 -> 4096 60 us beside 40)."""
     key = ("int8", x.shape, x.dtype, x.get_device(), x.is_contiguous(), _tag(w), _tag(w_scale),
            bias if bias is None else _tag(bias), residual if residual is None else _tag(residual),
            x_scale if x_scale is None else _tag(x_scale), dtype, act, alpha, beta, residual_last,

@@ -116,7 +116,9 @@ CONV_API conv_status conv_quantize_rows(const conv_quantize_problem* p, const vo
  * int8 with x_scale [rows] float32, or (x_quantized = 0) the rows of x, of the
  * problem's type, quantised as by conv_quantize_rows first.  The sum is the exact
  * integer, for every operand; what follows is float32.  Activations, residual,
- * order and flags as conv_linear_forward. */
+ * order and flags as conv_linear_forward.  What 8 bits save is memory; time only
+ * for some tens of rows and fewer, where reading the weights is the work (the
+ * products run at the 16-bit rate, and many rows' operands are widened first). */
 typedef struct conv_int8_problem {
   int64_t rows, c_in, c_out;        /* rows >= 0, 1 <= c_in <= 131071 (the sum fits 32 bits), c_out >= 1 */
   int64_t x_stride, w_stride, residual_stride, y_stride; /* row strides, 0: dense */
@@ -134,7 +136,9 @@ typedef struct conv_int8_problem {
 #define CONV_INT8_FLAG_MANY 0x40u  /* testing: that for many                                    */
 /* A flag whose kernel cannot run the call is passed over (conv_int8_describe_plan says what runs). */
 
-/* Scratch bytes on the current device.  Errors: as conv_linear_scratch_bytes. */
+/* Scratch bytes on the current device, enough for operands at any address: between 17 and 128 rows that may be 2 c_in c_out
+ * bytes for weights off 16-byte boundaries (64 rows of 4096 -> 12288: 101 MB, of which weights on such boundaries use half a
+ * megabyte).  Errors: as conv_linear_scratch_bytes. */
 CONV_API conv_status conv_int8_scratch_bytes(const conv_int8_problem* p, size_t* bytes);
 /* One line on the kernels that a device with `sm_count` SMs runs, weights 16-byte
  * aligned.  Host only. */
