@@ -30,7 +30,7 @@ struct RowScale {
   bool small;
   __device__ __forceinline__ explicit RowScale(uint32_t most) {
     const bool finite = most < 0x7f800000u;
-    constexpr float kStep = 1.0f / 127.0f;  // (a product, as a device tensor / 127 is in torch: scales made there are the same bits)
+    constexpr float kStep = 1.0f / 127.0f;  // (a product, as torch makes of a float32 device tensor / 127: scales made there are the same bits)
     scale = finite ? __uint_as_float(most) * kStep : __uint_as_float(0x7fffffffu);
     small = scale < 0x1p-100f;
     inv = finite && scale > 0.0f && !small ? __fdiv_rn(1.0f, scale) : 0.0f;

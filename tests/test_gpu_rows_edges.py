@@ -180,3 +180,29 @@ def test_dropout_backward_into_strided_rows(dtype):
         assert conv.dropout_backward(dy, 0.3, 5, 6, out=out) is out
         assert torch.equal(out, conv.dropout_backward(dy.contiguous(), 0.3, 5, 6))
         assert (full[:, :off] == 77).all() and (full[:, off + width:] == 77).all()
+
+
+def test_norm_of_wide_rows_in_two_graphs_at_once():
+    """Rows too wide for registers: three kernels backward, whose scratch is each graph's own."""
+    x, dy = (normal(9, 17000, dtype="f32", seed=s).cuda() for s in (1, 2))
+    w = normal(17000, dtype="f32", seed=3).cuda()
+
+    def step(x):
+        y, stats = conv.layer_norm(x, w, save=True)
+        return (y, *conv.layer_norm_backward(dy, x, w, stats), conv.layer_norm_backward(dy, x, w, stats, need_dx=False)[1])
+    step(x)
+    graphs, outs = [torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()], []
+    for k, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            outs.append(step(x if k else x * 2))
+    x.copy_(normal(9, 17000, dtype="f32", seed=4))
+    want = [step(x * 2), step(x)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(3):
+        with torch.cuda.stream(side):
+            graphs[0].replay()
+        graphs[1].replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for k in range(2) for a, b in zip(outs[k], want[k]))
+    assert torch.equal(want[0][2], want[0][4])
